@@ -52,6 +52,13 @@ _lib.qmm_admission_clear.argtypes = []
 _lib.qmm_admission_clear.restype = None
 _lib.qmm_stream_read_sink_words.argtypes = [_sz]
 _lib.qmm_stream_read_sink_words.restype = _sz
+_l, _f32 = ctypes.c_int64, ctypes.c_float
+_lib.qmm_qk_norm_rope.argtypes = [_p, _p, _p, _l, _l, _l, _i, _p, _p, _f32, _f32, _p, _p, _i, _i, _p, _p, _p, _p,
+                                  _i, _i, _i, _i, _i, _i, _i, _p]
+_lib.qmm_paged_attention_workspace_bytes.argtypes = [_i] * 9
+_lib.qmm_paged_attention_workspace_bytes.restype = _sz
+_lib.qmm_paged_attention.argtypes = [_p, _l, _p, _p, _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                                     _f32, _i, _i, _p, _sz, _p]
 _lib.qmm_splitk_workspace_bytes.argtypes = [_i, _i, _i]
 _lib.qmm_splitk_workspace_bytes.restype = _sz
 _lib.qmm_validate.argtypes = [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _sz]
@@ -63,7 +70,7 @@ for _f in (_lib.qmm_pack, _lib.qmm_forward, _lib.qmm_forward_rowexact, _lib.qmm_
            _lib.qmm_forward_splitk, _lib.qmm_forward_splitk_noalloc,
            _lib.qmm_forward_kernel, _lib.qmm_forward_fused, _lib.qmm_repack_tiled,
            _lib.qmm_forward_tiled, _lib.qmm_validate, _lib.qmm_stream_read, _lib.qmm_admit,
-           _lib.qmm_admission):
+           _lib.qmm_admission, _lib.qmm_qk_norm_rope, _lib.qmm_paged_attention):
     _f.restype = _i
 
 EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16", "qmm_forward_splitk",
@@ -71,7 +78,8 @@ EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16
             "qmm_splitk_workspace_bytes", "qmm_validate", "qmm_strerror", "qmm_kernel_name",
             "qmm_forward_kernel", "qmm_forward_fused", "qmm_tiled_bytes", "qmm_repack_tiled",
             "qmm_forward_tiled", "qmm_stream_read", "qmm_stream_read_sink_words",
-            "qmm_admit_workspace_bytes", "qmm_admit", "qmm_admission", "qmm_admission_clear")
+            "qmm_admit_workspace_bytes", "qmm_admit", "qmm_admission", "qmm_admission_clear",
+            "qmm_qk_norm_rope", "qmm_paged_attention_workspace_bytes", "qmm_paged_attention")
 
 QMM_MAX_FUSED = 4  # projections per qmm_forward_fused call
 
@@ -380,4 +388,120 @@ def qmm_forward_splitk_noalloc(x, wq, scales, biases, bits: int, G: int, split_k
                                          split_k, _stream(x))
     if rc:
         raise QmmError(rc, "qmm_forward_splitk_noalloc")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Between the products of a decode step.
+# ---------------------------------------------------------------------------
+_TYPE_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}  # QMM_F16, QMM_BF16, QMM_F32
+_HALVES = (torch.float16, torch.bfloat16)
+
+
+def _check_rows(t: torch.Tensor, name: str, dtypes, shape, device) -> int:
+    """_check for a tensor whose rows may lie apart; returns the row stride."""
+    if t.is_contiguous():
+        _check(t, name, dtypes, shape, device)
+        stride = 1
+        for n in shape[1:]:
+            stride *= n
+        return stride
+    if t.dim() < 2 or t.shape[0] < 1 or not t[0].is_contiguous():
+        raise ValueError(f"{name} must be contiguous within a row")
+    _check(t[0], name, dtypes, shape[1:], device)
+    if t.shape[0] != shape[0]:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.stride(0)
+
+
+def _check_caches(k_cache, v_cache, device):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("the caches must be 4-D [num_pages, Hkv, page_size, D]")
+    _check(k_cache, "k_cache", _HALVES, k_cache.shape, device)
+    _check(v_cache, "v_cache", (k_cache.dtype,), k_cache.shape, device)
+    return k_cache.shape
+
+
+def qmm_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, *, eps: float = 1e-6,
+                     weight_offset: float = 0.0, interleaved: bool = False, out=None) -> torch.Tensor:
+    """Per-head norms and rotation of q [M, Hq, D] and k [M, Hkv, D], with k and
+    v appended to the paged caches at `slots`; returns the queries in the
+    caches' type. q, k and v share one type (float32, float16 or bfloat16) and
+    may be views of a fused projection's rows; inv_freq [R/2] float32, or None
+    for no rotation."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be 3-D [M, heads, D]")
+    M, Hq, D = q.shape
+    dev = q.device
+    pages, Hkv, page_size, cache_D = _check_caches(k_cache, v_cache, dev)
+    if cache_D != D:
+        raise ValueError(f"the caches' D is {cache_D}, the queries' {D}")
+    qs = _check_rows(q, "q", tuple(_TYPE_CODES), (M, Hq, D), None)
+    ks = _check_rows(k, "k", (q.dtype,), (M, Hkv, D), dev)
+    vs = _check_rows(v, "v", (q.dtype,), (M, Hkv, D), dev)
+    _check(q_weight, "q_weight", (torch.float32,), (D,), dev)
+    _check(k_weight, "k_weight", (torch.float32,), (D,), dev)
+    _check(positions, "positions", (torch.int32,), (M,), dev)
+    _check(slots, "slots", (torch.int32,), (M,), dev)
+    R = 0
+    if inv_freq is not None:
+        R = 2 * inv_freq.numel()
+        _check(inv_freq, "inv_freq", (torch.float32,), (R // 2,), dev)
+    if out is None:
+        out = torch.empty((M, Hq, D), dtype=k_cache.dtype, device=dev)
+    _check(out, "out", (k_cache.dtype,), (M, Hq, D), dev)
+    rc = _lib.qmm_qk_norm_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _TYPE_CODES[q.dtype],
+                               q_weight.data_ptr(), k_weight.data_ptr(), eps, weight_offset, positions.data_ptr(),
+                               inv_freq.data_ptr() if R else None, R, interleaved, slots.data_ptr(), out.data_ptr(),
+                               k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[k_cache.dtype], M, Hq, Hkv, D,
+                               pages, page_size, _stream(q))
+    if rc:
+        raise QmmError(rc, "qmm_qk_norm_rope")
+    return out
+
+
+def qmm_paged_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int, max_rows: int, max_context: int,
+                                        window: int = 0, sinks: int = 0) -> int:
+    return int(_lib.qmm_paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks))
+
+
+def qmm_paged_attention(q, k_cache, v_cache, block_table, context_lens, row_starts, max_rows: int, max_context: int, *,
+                        scale: float | None = None, window: int = 0, sinks: int = 0, out=None, lse=None,
+                        workspace=None) -> torch.Tensor:
+    """Attention of the newest rows of each sequence over the paged caches.
+
+    q [T, Hq, D]; block_table int32 [B, max_pages]; context_lens int32 [B];
+    row_starts int32 [B + 1] (rows of sequence b of q). `scale` defaults to
+    1/sqrt(D); `lse` (float32 [T, Hq]), when given, receives the logarithm of
+    each row's sum. max_rows bounds the rows of a sequence, max_context guides
+    the split of the length."""
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be 3-D [T, Hq, D] and block_table 2-D [B, max_pages]")
+    T, Hq, D = q.shape
+    B, max_pages = block_table.shape
+    dev = q.device
+    pages, Hkv, page_size, cache_D = _check_caches(k_cache, v_cache, dev)
+    if cache_D != D:
+        raise ValueError(f"the caches' D is {cache_D}, the queries' {D}")
+    qs = _check_rows(q, "q", (k_cache.dtype,), (T, Hq, D), dev)
+    _check(block_table, "block_table", (torch.int32,), (B, max_pages), dev)
+    _check(context_lens, "context_lens", (torch.int32,), (B,), dev)
+    _check(row_starts, "row_starts", (torch.int32,), (B + 1,), dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    _check(out, "out", (q.dtype,), (T, Hq, D), dev)
+    if lse is not None:
+        _check(lse, "lse", (torch.float32,), (T, Hq), dev)
+    need = _lib.qmm_paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = _lib.qmm_paged_attention(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[q.dtype],
+                                  block_table.data_ptr(), context_lens.data_ptr(), row_starts.data_ptr(),
+                                  out.data_ptr(), lse.data_ptr() if lse is not None else None, T, B, Hq, Hkv, D,
+                                  pages, page_size, max_pages, max_rows, max_context,
+                                  scale if scale is not None else D ** -0.5, window, sinks,
+                                  workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(q))
+    if rc:
+        raise QmmError(rc, "qmm_paged_attention")
     return out

@@ -236,11 +236,13 @@ const char *qmm_strerror(int code)
     case QMM_ERR_BITS: return "unsupported bit width (supported: 2, 3, 4, 5, 6, 8)";
     case QMM_ERR_GROUP: return "unsupported group size (supported: 32, 64, 128)";
     case QMM_ERR_SPLIT: return "bad split_k: need 1 <= split_k <= K/G";
-    case QMM_ERR_WORKSPACE: return "workspace smaller than qmm_splitk_workspace_bytes(M, N, split_k)";
-    case QMM_ERR_ALIGN: return "x, wq, scales, biases, y and workspace must be 16-byte aligned";
+    case QMM_ERR_WORKSPACE: return "workspace smaller than the entry point's *_workspace_bytes";
+    case QMM_ERR_ALIGN: return "buffers must be 16-byte aligned (per-row parameters 4), row strides multiples of 8";
     case QMM_ERR_LAUNCH: return "the HIP runtime rejected a kernel launch";
     case QMM_ERR_UNSUPPORTED: return "the requested kernel cannot run this shape";
     case QMM_ERR_SCRATCH: return "split_k * M * N * 4 bytes exceed the static scratch (QMM_NOALLOC_SCRATCH_BYTES)";
+    case QMM_ERR_TYPE: return "unsupported element type";
+    case QMM_ERR_HEAD: return "unsupported head layout: Hq a multiple of Hkv, D and R as the entry point lists";
     default: return "unknown error code";
     }
 }

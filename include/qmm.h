@@ -70,11 +70,13 @@ extern "C" {
 #define QMM_ERR_BITS (-3)          /* bits not in {2, 3, 4, 5, 6, 8} */
 #define QMM_ERR_GROUP (-4)         /* G not in {32, 64, 128} */
 #define QMM_ERR_SPLIT (-5)         /* split_k < 1 or split_k > K/G */
-#define QMM_ERR_WORKSPACE (-6)     /* workspace smaller than qmm_splitk_workspace_bytes */
+#define QMM_ERR_WORKSPACE (-6)     /* workspace smaller than the entry point's *_workspace_bytes */
 #define QMM_ERR_ALIGN (-7)         /* x, wq, scales, biases, y or workspace not 16-byte aligned */
 #define QMM_ERR_LAUNCH (-8)        /* the HIP runtime rejected a kernel launch */
 #define QMM_ERR_UNSUPPORTED (-9)   /* qmm_forward_kernel: that kernel cannot run this shape */
 #define QMM_ERR_SCRATCH (-10)      /* qmm_forward_splitk_noalloc: partials exceed the static scratch */
+#define QMM_ERR_TYPE (-11)         /* an element type code the operator does not take */
+#define QMM_ERR_HEAD (-12)         /* head layout: Hq % Hkv != 0, or D or R not supported */
 
 /*
  * qmm_pack - pack unpacked codes into the bitstream layout above.
@@ -354,6 +356,102 @@ int qmm_forward_kernel(const char *kernel, const uint16_t *x, const uint32_t *wq
  * byte count. Host-only. */
 size_t qmm_stream_read_sink_words(size_t bytes);
 int qmm_stream_read(const void *src, size_t bytes, uint32_t *sink, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Between the products of a decode step: norms, rotation and cache append,
+ * attention over the paged cache, and the choice of a token. Conventions are
+ * those above (caller-owned device buffers, no allocation, host checks before
+ * any launch, work enqueued on `stream`, capturable into HIP graphs; the
+ * default stream of every call is the caller's). Element types:
+ */
+#define QMM_F16 0
+#define QMM_BF16 1
+#define QMM_F32 2
+
+/*
+ * The paged cache: k_cache and v_cache are [num_pages, Hkv, page_size, D]
+ * (fp16 or bf16, row-major, 16-byte aligned). A slot is a token's place in it,
+ * page * page_size + offset. page_size is any number from 1 on;
+ * num_pages * page_size < 2^31 and num_pages * page_size * Hkv < 2^32 - 1
+ * (byte offsets are 64 bits wide).
+ *
+ * qmm_qk_norm_rope - the norms of queries and keys per head, their rotation by
+ * position, and the append of keys and values to the paged cache, in one pass
+ * over the q, k and v projections' outputs. For row m and each head of q and k
+ *
+ *     n_d = x_d * rsqrt(mean over d of x_d^2 + eps) * (weight_offset + w_d)
+ *
+ * then for i < R/2 the pair (n_i, n_{R/2+i}), or with `interleaved` the pair
+ * (n_{2i}, n_{2i+1}), turns by the angle positions[m] * inv_freq[i]:
+ * (a, b) -> (a cos - b sin, b cos + a sin). Values from R on are not turned,
+ * v is only rounded. The angle's product and its reduction to one turn are done
+ * in 64 bits, the rest in fp32; the one rounding is to out_type.
+ *
+ * q [M, Hq*D], k and v [M, Hkv*D] of in_type (fp16, bf16, or fp32 as
+ * qmm_forward writes them), rows q_stride, k_stride, v_stride elements apart
+ * (multiples of 8; views of one fused output are fine). q_weight, k_weight
+ * fp32 [D]; positions int32 [M]; inv_freq fp32 [R/2] (may be NULL for R = 0).
+ * slots int32 [M]: where row m's key and value go; a slot that is negative (a
+ * padding row) or past the cache writes nothing. Two rows with the same slot
+ * leave either's values. q_out [M, Hq, D] of out_type (fp16 or bf16), like the
+ * caches. D a multiple of 8 up to 256, R a multiple of 8 up to D.
+ * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_HEAD,
+ * QMM_ERR_ALIGN (16 bytes; positions and slots 4), QMM_ERR_LAUNCH.
+ */
+int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stride,
+                     int64_t k_stride, int64_t v_stride, int in_type, const float *q_weight,
+                     const float *k_weight, float eps, float weight_offset,
+                     const int32_t *positions, const float *inv_freq, int R, int interleaved,
+                     const int32_t *slots, void *q_out, void *k_cache, void *v_cache,
+                     int out_type, int M, int Hq, int Hkv, int D, int num_pages, int page_size,
+                     hipStream_t stream);
+
+/*
+ * qmm_paged_attention - attention of the newest rows of each of B sequences
+ * over the paged cache (one new token, the rows of a verify step, or more).
+ *
+ * q [T, Hq, D] of `type` (fp16 or bf16, the caches' type), rows q_stride
+ * elements apart (a multiple of 8); row_starts int32 [B+1]: the rows of
+ * sequence b are row_starts[b] .. row_starts[b+1] - 1 of q. context_lens int32
+ * [B]: the tokens of the sequence, its new rows included, so that row r of n
+ * stands at position p = context_len - n + r. block_table int32
+ * [B, max_pages]: token j lies in page block_table[b][j / page_size]. Kv head
+ * h serves query heads h*Hq/Hkv .. (h+1)*Hq/Hkv - 1.
+ *
+ * Row r sees the tokens j <= p; with window > 0 only those with
+ * j > p - window or j < sinks. Tokens past the table, and tokens whose page
+ * is not in [0, num_pages), are seen by no row. out [T, Hq, D] of `type`:
+ *
+ *     s_j = scale * q . k_j,   out = sum_j e^(s_j) v_j / sum_j e^(s_j),
+ *     lse = log(sum_j e^(s_j))
+ *
+ * over the tokens that the row sees; a row that sees none gets zeros and an
+ * lse of -infinity. What lies in places that no row sees is not used, whatever
+ * it is; infinities and NaN of a token reach the rows that see it and no
+ * others. Products are accumulated in fp32, e^(s) and its sums are fp32, and
+ * e^(s) enters the second product as the sum of two 16-bit numbers; `out` is
+ * rounded once. lse (fp32 [T, Hq], natural logarithm) may be NULL. Reruns are
+ * bitwise identical. Rows of q that no sequence holds are not written.
+ *
+ * max_rows: at least the rows of any sequence, at most T (further rows of a
+ * longer sequence are not computed). max_context: an estimate of the longest context; it
+ * sets how the length is split over the GPU and the workspace, not what is
+ * computed. D is 64, 96, 128, 192 or 256. Workspace: see below, 16-byte
+ * aligned, contents irrelevant, NULL when 0 bytes are needed.
+ * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_HEAD,
+ * QMM_ERR_WORKSPACE, QMM_ERR_ALIGN, QMM_ERR_LAUNCH.
+ *
+ * qmm_paged_attention_workspace_bytes: the bytes a call with these arguments
+ * needs (0 for invalid ones). Host-only.
+ */
+size_t qmm_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_rows,
+                                           int max_context, int window, int sinks);
+int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                        int type, const int32_t *block_table, const int32_t *context_lens,
+                        const int32_t *row_starts, void *out, float *lse, int T, int B, int Hq,
+                        int Hkv, int D, int num_pages, int page_size, int max_pages, int max_rows,
+                        int max_context, float scale, int window, int sinks, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
