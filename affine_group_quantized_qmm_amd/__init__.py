@@ -59,6 +59,9 @@ _lib.qmm_paged_attention_workspace_bytes.argtypes = [_i] * 9
 _lib.qmm_paged_attention_workspace_bytes.restype = _sz
 _lib.qmm_paged_attention.argtypes = [_p, _l, _p, _p, _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
                                      _f32, _i, _i, _p, _sz, _p]
+_lib.qmm_sample_workspace_bytes.argtypes = [_i, _i]
+_lib.qmm_sample_workspace_bytes.restype = _sz
+_lib.qmm_sample.argtypes = [_p, _l, _i, _p, _p, _p, _p, _p, _p, _p, _i, _i, _p, _sz, _p]
 _lib.qmm_splitk_workspace_bytes.argtypes = [_i, _i, _i]
 _lib.qmm_splitk_workspace_bytes.restype = _sz
 _lib.qmm_validate.argtypes = [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _sz]
@@ -70,7 +73,7 @@ for _f in (_lib.qmm_pack, _lib.qmm_forward, _lib.qmm_forward_rowexact, _lib.qmm_
            _lib.qmm_forward_splitk, _lib.qmm_forward_splitk_noalloc,
            _lib.qmm_forward_kernel, _lib.qmm_forward_fused, _lib.qmm_repack_tiled,
            _lib.qmm_forward_tiled, _lib.qmm_validate, _lib.qmm_stream_read, _lib.qmm_admit,
-           _lib.qmm_admission, _lib.qmm_qk_norm_rope, _lib.qmm_paged_attention):
+           _lib.qmm_admission, _lib.qmm_qk_norm_rope, _lib.qmm_paged_attention, _lib.qmm_sample):
     _f.restype = _i
 
 EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16", "qmm_forward_splitk",
@@ -79,7 +82,8 @@ EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16
             "qmm_forward_kernel", "qmm_forward_fused", "qmm_tiled_bytes", "qmm_repack_tiled",
             "qmm_forward_tiled", "qmm_stream_read", "qmm_stream_read_sink_words",
             "qmm_admit_workspace_bytes", "qmm_admit", "qmm_admission", "qmm_admission_clear",
-            "qmm_qk_norm_rope", "qmm_paged_attention_workspace_bytes", "qmm_paged_attention")
+            "qmm_qk_norm_rope", "qmm_paged_attention_workspace_bytes", "qmm_paged_attention",
+            "qmm_sample_workspace_bytes", "qmm_sample")
 
 QMM_MAX_FUSED = 4  # projections per qmm_forward_fused call
 
@@ -505,3 +509,45 @@ def qmm_paged_attention(q, k_cache, v_cache, block_table, context_lens, row_star
     if rc:
         raise QmmError(rc, "qmm_paged_attention")
     return out
+
+
+def qmm_sample_workspace_bytes(M: int, V: int) -> int:
+    return int(_lib.qmm_sample_workspace_bytes(M, V))
+
+
+def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, *, tokens=None, logprobs=None,
+               workspace=None) -> torch.Tensor:
+    """A token (int32 [M]) for each row of logits [M, V] from the uniform numbers
+    u [M]; temperature, top_k (int32), top_p and min_p are per-row tensors or
+    None. `logprobs` (float32 [M]), when given, receives the logarithm of each
+    token's share of the kept mass."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [M, V]")
+    M, V = logits.shape
+    dev = logits.device
+    stride = V
+    if logits.is_contiguous():
+        _check(logits, "logits", tuple(_TYPE_CODES), (M, V), None)
+    else:
+        if logits.dtype not in _TYPE_CODES or dev.type != "cuda" or logits.stride(1) != 1:
+            raise ValueError("logits must be a GPU tensor of float32, float16 or bfloat16, contiguous within a row")
+        stride = logits.stride(0)
+    for t, name, dtype in ((u, "u", torch.float32), (temperature, "temperature", torch.float32),
+                           (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
+                           (min_p, "min_p", torch.float32), (tokens, "tokens", torch.int32),
+                           (logprobs, "logprobs", torch.float32)):
+        if t is not None:
+            _check(t, name, (dtype,), (M,), dev)
+    if tokens is None:
+        tokens = torch.empty(M, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(_lib.qmm_sample_workspace_bytes(M, V), dtype=torch.uint8, device=dev)
+    rc = _lib.qmm_sample(logits.data_ptr(), stride, _TYPE_CODES[logits.dtype], u.data_ptr(),
+                         None if temperature is None else temperature.data_ptr(),
+                         None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+                         None if min_p is None else min_p.data_ptr(), tokens.data_ptr(),
+                         None if logprobs is None else logprobs.data_ptr(), M, V, workspace.data_ptr(),
+                         workspace.numel() * workspace.element_size(), _stream(logits))
+    if rc:
+        raise QmmError(rc, "qmm_sample")
+    return tokens

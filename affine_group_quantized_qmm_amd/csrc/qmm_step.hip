@@ -173,4 +173,41 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
     return qmm::launch_paged_attention(a, plan, D, type == QMM_BF16, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 
+size_t qmm_sample_workspace_bytes(int M, int V)
+{
+    return M < 1 || M > 65535 || !qmm::sample_size_supported(V) ? 0 : qmm::sample_workspace_bytes(M, V);
+}
+
+int qmm_sample(const void *logits, int64_t row_stride, int type, const float *u, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens, float *logprobs, int M,
+               int V, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!logits || !u || !tokens || !workspace)
+        return QMM_ERR_NULL;
+    if (!any_type(type))
+        return QMM_ERR_TYPE;
+    if (M < 1 || M > 65535 || !qmm::sample_size_supported(V) || row_stride < V)
+        return QMM_ERR_SHAPE;
+    if (workspace_bytes < qmm::sample_workspace_bytes(M, V))
+        return QMM_ERR_WORKSPACE;
+    if (!aligned(logits, type == QMM_F32 ? 4 : 2) || !aligned(u, 4) || !aligned(temperature, 4) ||
+        !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(tokens, 4) ||
+        !aligned(logprobs, 4) || !aligned(workspace, 16))
+        return QMM_ERR_ALIGN;
+    qmm::SampleArgs a{};
+    a.logits = logits;
+    a.row_stride = row_stride;
+    a.u = u;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.tokens = tokens;
+    a.logprobs = logprobs;
+    a.workspace = workspace;
+    a.M = M;
+    a.V = V;
+    return qmm::launch_sample(a, type, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
 }  // extern "C"

@@ -67,6 +67,7 @@ struct SampleArgs {
     void *workspace;
     int M, V;
 };
+bool sample_size_supported(int V);
 size_t sample_workspace_bytes(int M, int V);
 hipError_t launch_sample(const SampleArgs &a, int type, hipStream_t stream);
 

@@ -453,6 +453,41 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
                         int max_context, float scale, int window, int sinks, void *workspace,
                         size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * qmm_sample - a token for each row of logits from a given uniform number.
+ *
+ * logits [M, V] of `type` (fp16, bf16 or fp32), rows row_stride >= V elements
+ * apart, aligned to their element. Per row, on the device: u fp32 [M] in
+ * [0, 1) (numbers outside are taken as the nearest inside, NaN as 0);
+ * temperature fp32 [M]; top_k int32 [M]; top_p, min_p fp32 [M]. Each of the last
+ * four may be NULL: temperature 1, no filter.
+ *
+ * The logits x_i of a row in falling order, equal ones by rising index, with
+ * w_i = e^((x_i - max) / temperature): kept are the first top_k (all for
+ * top_k <= 0); of these the ones whose predecessors hold less than top_p of
+ * their mass (all for top_p >= 1, at least one); of these the ones with
+ * w_i >= min_p (all for min_p <= 0, the largest always). tokens[m] is the
+ * index of the first, in that order, at which the cumulative kept mass exceeds
+ * u times its total; logprobs[m] (fp32, may be NULL) the logarithm of its share
+ * of the kept mass. temperature <= 0 (or NaN): the largest logit, the lowest
+ * index of equal ones, logprob 0. A logit of -infinity or NaN is never chosen;
+ * +infinity holds all the mass, in equal parts where there are several. A row
+ * without any logit above -infinity gets token -1 and logprob -infinity.
+ *
+ * Weights and their sums are integers and 64-bit floats: the token is that of
+ * 64-bit arithmetic unless u (or top_p) lies within about 1e-9 of the kept mass
+ * from the border between two tokens, and reruns are bitwise identical.
+ * M <= 65535, V <= 2^23. workspace: qmm_sample_workspace_bytes(M, V) bytes (0
+ * for invalid sizes), 16-byte aligned, contents irrelevant.
+ * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_WORKSPACE,
+ * QMM_ERR_ALIGN, QMM_ERR_LAUNCH.
+ */
+size_t qmm_sample_workspace_bytes(int M, int V);
+int qmm_sample(const void *logits, int64_t row_stride, int type, const float *u,
+               const float *temperature, const int32_t *top_k, const float *top_p,
+               const float *min_p, int32_t *tokens, float *logprobs, int M, int V, void *workspace,
+               size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

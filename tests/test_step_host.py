@@ -66,6 +66,30 @@ def test_attention_workspace():
     assert f(4, 2, 4, 3, 128, 2, 100000) == 0 and f(0, 2, 4, 2, 128, 2, 100000) == 0
 
 
+def sample(**kw):
+    a = dict(x=A, stride=1000, type=2, u=A, T=None, k=None, p=None, mp=None, tok=A, lp=None, M=3, V=1000, ws=A,
+             wsb=1 << 30)
+    a.update(kw)
+    return LIB.qmm_sample(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), -1), (dict(u=None), -1), (dict(tok=None), -1), (dict(ws=None), -1),
+    (dict(M=0), -2), (dict(M=1 << 16), -2), (dict(V=0), -2), (dict(V=(1 << 23) + 1, stride=1 << 24), -2),
+    (dict(stride=999), -2), (dict(type=3), -11), (dict(wsb=100), -6),
+    (dict(x=A + 2), -7), (dict(x=A + 1, type=0), -7), (dict(u=A + 2), -7), (dict(T=A + 1), -7), (dict(k=A + 2), -7),
+    (dict(p=A + 3), -7), (dict(mp=A + 2), -7), (dict(tok=A + 2), -7), (dict(lp=A + 2), -7), (dict(ws=A + 8), -7),
+])
+def test_sample_refuses(kw, code):
+    assert sample(**kw) == code
+
+
+def test_sample_workspace():
+    f = qmm.qmm_sample_workspace_bytes
+    assert f(1, 1000) > 0 and f(2, 1000) == 2 * f(1, 1000)
+    assert f(0, 1000) == 0 and f(1, 0) == 0 and f(1, (1 << 23) + 1) == 0 and f(1 << 16, 10) == 0
+
+
 def test_messages():
     for code in (-11, -12):
         assert "unknown" not in qmm.qmm_strerror(code)
@@ -83,5 +107,9 @@ def test_binding_refuses():
         qmm.qmm_paged_attention(q[0], c, c, t, i[:1], i[:2], 3, 10)
     with pytest.raises(ValueError):
         qmm.qmm_qk_norm_rope(q, q[:, :2], q[:, :2], torch.ones(64), torch.ones(64), i, None, i, c, c)
+    with pytest.raises(ValueError):
+        qmm.qmm_sample(torch.zeros(2, 10), torch.zeros(2))
+    with pytest.raises(ValueError):
+        qmm.qmm_sample(torch.zeros(10), torch.zeros(1))
     with pytest.raises(ValueError):
         qmm.qmm_qk_norm_rope(q[0], q, q, torch.ones(64), torch.ones(64), i, None, i, c, c)
