@@ -33,10 +33,17 @@
 namespace qmm {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * kWave;
-constexpr int kTile = 32;                  // tokens of a tile
+constexpr int kJoinThreads = 1024;
+// Waves of a workgroup; each has 16 tokens of a tile. A turn of a wave is some
+// thousand instructions one after the other, which only another wave of the
+// same SIMD can hide: wide heads, whose registers and LDS leave room for one
+// workgroup on a CU, take two waves a SIMD.
+constexpr int waves_of(int D) { return D >= 128 ? 8 : 4; }
+constexpr int tile_of(int D) { return 16 * waves_of(D); }
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;   // token without a row in the cache
+#ifndef PERCU
+#define PERCU 0
+#endif
 constexpr float kRaise = 8.0f;             // a score may pass the running maximum by this (log2)
 
 typedef float float2_t __attribute__((ext_vector_type(2)));
@@ -87,15 +94,15 @@ struct Span {
     int count;           // tiles in all
 };
 
-__device__ __forceinline__ Span span_of(const AttnArgs &a, int b, int x0, int cols)
+template <int TILE>
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int begin, int end, int len, int x0, int cols)
 {
     Span s;
-    const int begin = a.row_starts[b], end = a.row_starts[b + 1];
     const bool sound = begin >= 0 && begin <= end && end <= a.T;
     s.start = sound ? begin : 0;
     s.n = sound ? end - begin : 0;
     const int G = a.Hq / a.Hkv;
-    const int len = a.context_lens[b] < 0 ? 0 : a.context_lens[b];
+    len = len < 0 ? 0 : len;
     s.first_pos = len - s.n;
     s.sink_tiles = s.low = s.count = 0;
     s.pmin = s.pmax = -1;
@@ -109,198 +116,417 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int b, int x0, int co
     const int high = s.pmax + 1 < capacity ? s.pmax + 1 : capacity;
     if (high <= 0)
         return s;
-    const int high_tile = (high + kTile - 1) / kTile;
+    const int high_tile = (high + TILE - 1) / TILE;
     if (a.window > 0) {
         const int first = s.pmin - a.window + 1;
-        s.low = first > 0 ? first / kTile : 0;
+        s.low = first > 0 ? first / TILE : 0;
         s.low = s.low < high_tile ? s.low : high_tile;
-        const int sink_tiles = a.sinks / kTile + (a.sinks % kTile != 0);
+        const int sink_tiles = a.sinks / TILE + (a.sinks % TILE != 0);
         s.sink_tiles = sink_tiles < s.low ? sink_tiles : s.low;
     }
     s.count = s.sink_tiles + high_tile - s.low;
     return s;
 }
 
-// Splits that hold tiles of a span (the last split takes whatever is left).
-__device__ __forceinline__ int splits_of(const AttnArgs &a, int count)
+template <int TILE>
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int b, int x0, int cols)
 {
-    const int n = (count + a.split_tiles - 1) / a.split_tiles;
-    return n < 1 ? 1 : n < a.splits ? n : a.splits;
+    return span_of<TILE>(a, a.row_starts[b], a.row_starts[b + 1], a.context_lens[b], x0, cols);
+}
+
+// An item is one kv head of one column chunk of one sequence; its tiles are
+// at least one, so that rows that see nothing are written too. Items are
+// numbered by sequence, chunk and head. How they are dealt out:
+//   whole    one workgroup an item; no join.
+//   pieces   (few items) each item in equal pieces of at most `size` tiles, one
+//            a workgroup, with the smallest size that gives at most as many
+//            pieces as workgroups.
+//   runs     (about as many items as workgroups) the tiles of all items one after
+//            the other, in equal runs: a run may hold the end of one item and
+//            the beginning of another, and no workgroup has more than its share
+//            whatever the lengths are.
+__device__ __forceinline__ int tiles_of(const Span &s) { return s.count > 1 ? s.count : 1; }
+
+// Run w takes `each` tiles, one more for the first `more` runs.
+struct Runs {
+    int each, more;
+};
+__device__ __forceinline__ int first_tile(Runs r, int w) { return w * r.each + (w < r.more ? w : r.more); }
+__device__ __forceinline__ int owner_of(Runs r, int tile)
+{
+    const int longer = r.more * (r.each + 1);
+    return tile < longer ? tile / (r.each + 1) : r.more + (tile - longer) / r.each;
+}
+
+// A run's partial results: of an item that it begins (but does not finish), and
+// of one that it does not begin (its first).
+__device__ __forceinline__ int slot_of(int w, bool begins) { return 2 * w + (begins ? 1 : 0); }
+
+// What a barrier has to order here is LDS only: loads of the next tile stay in
+// flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 template <typename T, int D, int NT>
-__global__ __launch_bounds__(kThreads, (D * NT <= 128 ? 2 : 1)) void attn_kernel(const AttnArgs a)
+__global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const AttnArgs a)
 {
     using E = Elem<T>;
     using x8 = typename E::x8;
-    constexpr int KS = D / 32;              // contraction steps of K Q^T
-    constexpr int DT = D / 16;              // output tiles along the head
-    constexpr int U = D / 8;                // 16-byte units of a cache row
-    constexpr int NL = U * kTile / kWave;   // loads of a V tile per lane
+    using x4 = typename E::x4;
+    constexpr int kWaves = waves_of(D), kTile = tile_of(D);
+    constexpr int KS = D / 32;                  // contraction steps of K Q^T; loads of a lane for K and for V
+    constexpr int DT = D / 16;                  // output tiles along the head
+    constexpr int DW = (DT + kWaves - 1) / kWaves;  // of one wave: tiles wave, wave + kWaves, ...
+    constexpr int U = D / 8;                    // 16-byte units of a cache row
     // LDS row of V: 32 bytes past the data shift consecutive rows by 8 banks,
     // so that the 8 rows that a transposing read touches at a time do not collide.
     constexpr int kPitch = 2 * D + 32;
-    constexpr int kRegion = kTile * kPitch; // bytes of a wave's V tile
-    constexpr int kJoinPitch = D + 4;       // floats of a column in the join
-    static_assert(16 * kJoinPitch * 4 <= kRegion, "the join reuses the V tiles");
-    static_assert(U * kTile % kWave == 0, "whole loads");
-    __shared__ __align__(16) char lds[kWaves * kRegion];
-    __shared__ float2_t stats[kWaves][NT * 16];
+    constexpr int kColumn = kTile + 8;          // elements of a column of P: 16 bytes of padding for the same reason
     // The queries' operands stay in registers (4 a step and column tile) while
-    // these are few, else in LDS, where the four waves share them.
+    // these are few, else in LDS, where the waves share them.
     constexpr bool kQueriesInLds = NT * KS > 8;
+    // Each wave's 16 rows hold its K tile up to the first barrier of a turn, then V.
+    __shared__ __align__(16) char kv_lds[kTile * kPitch];
+    __shared__ __align__(16) T p_hi[NT * 16 * kColumn], p_lo[NT * 16 * kColumn];
     __shared__ u32x4 q_lds[kQueriesInLds ? NT * KS * kWave : 1];
-
-    // Block -> (chunk, head, split, sequence): the chunks of one piece of the
-    // cache are 8 apart, that is on one XCD, behind one L2.
-    const int grp = blockIdx.x / (8 * a.chunks), rem = blockIdx.x % (8 * a.chunks);
-    const int chunk = rem / 8;
-    int work = grp * 8 + rem % 8;
-    if (work >= a.Hkv * a.splits * a.B)
-        return;
-    const int h = work % a.Hkv;
-    work /= a.Hkv;
-    const int z = work % a.splits, b = work / a.splits;
-
-    const int G = a.Hq / a.Hkv;
-    const int x0 = chunk * 16 * NT;
-    const Span span = span_of(a, b, x0, 16 * NT);
-    const int pieces = splits_of(a, span.count);
-    if (x0 >= span.n * G || z >= pieces)
-        return;
-    const int begin = z * a.split_tiles;
-    const int end = z == pieces - 1 ? span.count : begin + a.split_tiles;
+    __shared__ float col_max[NT * 16], col_sum[kWaves][NT * 16];
+    __shared__ u32x4 bad_tokens[kWaves / 4];  // a word for each wave
+    __shared__ uint32_t rows_lds[kTile];
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int c = lane / 16, n = lane % 16;
+    const int G = a.Hq / a.Hkv;
+    constexpr int kColumns = 16 * NT;
 
-    // Queries of this lane's columns, and their positions (-1: no such column).
-    x8 qf[kQueriesInLds ? 1 : NT][KS];
-    int pos[NT];
+    // Where the run starts: (sequence, chunk, head, tile), and its length.
+    int b, chunk, h, tile = 0, w = 0, left, item_unit = 0, here = 1;
+    Runs runs{1, 0};
+    if (a.whole) {
+        // One item a workgroup; the chunks of a head are 8 apart, that is on one
+        // XCD, behind one L2.
+        const int grp = blockIdx.x / (8 * a.chunks), rem = blockIdx.x % (8 * a.chunks);
+        chunk = rem / 8;
+        const int item = grp * 8 + rem % 8;
+        h = item % a.Hkv;
+        b = item / a.Hkv;
+        if (b >= a.B)
+            return;
+        const Span s = span_of<kTile>(a, b, chunk * kColumns, kColumns);
+        if (chunk * kColumns >= s.n * G)
+            return;
+        left = tiles_of(s);
+    } else {
+        w = blockIdx.x;
+        // Sequences are shared out to the lanes in order; the waves do the same.
+        // The host has checked that the sum of tiles has 31 bits.
+        const int each = (a.B + kWave - 1) / kWave;
+        const int b0 = lane * each, b1 = b0 + each < a.B ? b0 + each : a.B;
+        // Tiles of this lane's items, or pieces of `size` tiles.
+        auto sum_of = [&](int size) {
+            int sum = 0;
+            for (int i = b0; i < b1; ++i)
+                for (int k = 0; k < a.chunks; ++k) {
+                    const Span s = span_of<kTile>(a, i, k * kColumns, kColumns);
+                    if (k * kColumns >= s.n * G)
+                        break;
+                    sum += size == 1 ? tiles_of(s) : (tiles_of(s) + size - 1) / size;
+                }
+            return sum * a.Hkv;
+        };
+        auto wave_total = [&](int v) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int x = x0 + t * 16 + n;
-        const bool live = x < span.n * G;
-        const int r = live ? x / G : 0;
-        pos[t] = live ? span.first_pos + r : -1;
-        const T *qp = static_cast<const T *>(a.q) + (span.start + r) * a.q_stride +
-                      (int64_t)(h * G + (live ? x - r * G : 0)) * D + c * 8;
+            for (int d = 1; d < kWave; d *= 2)
+                v += __shfl_xor(v, d);
+            return __builtin_amdgcn_readfirstlane(v);
+        };
+        int mine = sum_of(1);
+        const int total = wave_total(mine);
+        int size = 1, units = total;  // runs are dealt in tiles, pieces one by one
+        if (a.pieces) {
+            size = (total + a.groups - 1) / a.groups;
+            for (;;) {  // ends: with a size of the longest item every item is one piece
+                size = size > 1 ? size : 1;
+                mine = sum_of(size);
+                units = wave_total(mine);
+                if (units <= a.groups)
+                    break;
+                const int larger = (int)((int64_t)size * units / a.groups);
+                size = larger > size ? larger : size + 1;
+            }
+        }
+        const int groups = units < a.groups ? units : a.groups;
+        if (w >= groups)
+            return;
+        runs.each = units / groups;
+        runs.more = units - runs.each * groups;
+        const int from = first_tile(runs, w);
+        left = first_tile(runs, w + 1) - from;
+        // The lane whose share holds the run's first unit, then the item in it.
+        int upto = mine;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            if constexpr (!kQueriesInLds)
-                qf[t][s] = *reinterpret_cast<const x8 *>(qp + s * 32);
-            else if ((t * KS + s) % kWaves == wave)
-                q_lds[(t * KS + s) * kWave + lane] = *reinterpret_cast<const u32x4 *>(qp + s * 32);
+        for (int d = 1; d < kWave; d *= 2) {
+            const int v = __shfl_up(upto, d);
+            upto += lane >= d ? v : 0;
+        }
+        const int in = __builtin_ctzll(__ballot(from < upto));
+        int at = __builtin_amdgcn_readlane(upto - mine, in);
+        b = in * each;
+        chunk = 0;
+        int count;
+        for (;;) {
+            if (b >= a.B)
+                return;  // not reached: the sums above found the unit
+            const Span s = span_of<kTile>(a, b, chunk * kColumns, kColumns);
+            if (chunk == a.chunks || chunk * kColumns >= s.n * G) {
+                chunk = 0;
+                ++b;
+                continue;
+            }
+            count = tiles_of(s);
+            here = (count + size - 1) / size;
+            if (from < at + here * a.Hkv)
+                break;
+            at += here * a.Hkv;
+            ++chunk;
+        }
+        h = (from - at) / here;
+        item_unit = at + h * here;
+        tile = from - item_unit;
+        if (a.pieces) {  // piece `tile` of `here` equal ones
+            const int q = count / here, more = count - q * here, piece = tile;
+            tile = first_tile(Runs{q, more}, piece);
+            left = first_tile(Runs{q, more}, piece + 1) - tile;
         }
     }
-    if constexpr (kQueriesInLds)
-        __syncthreads();
+    const int tr_offset = (4 * c + n / 4) * kPitch + n % 4 * 8;
 
-    float4_t acc[NT][DT];
-    float m[NT], l[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        m[t] = -__builtin_inff();
-        l[t] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-            acc[t][d] = float4_t{0.f, 0.f, 0.f, 0.f};
-    }
+    for (;; lds_barrier()) {  // the items of the run
+    const int x0 = chunk * kColumns;
+    const Span span = span_of<kTile>(a, b, x0, kColumns);
+    const int count = tiles_of(span);
+    const int begin = tile, end = left < count - begin ? begin + left : count;
+    if (!a.whole && begin == 0 && threadIdx.x == 0)  // who holds the pieces of the item that begins here
+        a.joins[(b * a.chunks + chunk) * a.Hkv + h] =
+            int2{w, a.pieces ? w + here - 1 : owner_of(runs, item_unit + count - 1)};
 
     const int32_t *table = a.block_table + (int64_t)b * a.max_pages;
     const int capacity = a.max_pages * a.page_size;
     const int last_token = span.pmax < capacity ? span.pmax : capacity - 1;
-    auto tile_of = [&](int x) { return x < span.sink_tiles ? x : span.low + x - span.sink_tiles; };
-    // Token (lane % 32) of a tile: whether some row of the workgroup sees it.
-    // The others are not read: their pages may be gone, their values anything.
+    auto first_of = [&](int x) {
+        return (x < span.sink_tiles ? x : span.low + x - span.sink_tiles) * kTile;
+    };
+    // Token (16 * wave + n) of a tile: whether some row of the workgroup sees
+    // it. The others are not read: their pages may be gone, their values anything.
     auto seen_by_any = [&](int j) {
         return j <= last_token && (a.window == 0 || j > span.pmin - a.window || j < a.sinks);
     };
+    // Loads are issued without branches around them (past the end they go to the
+    // cache's first row): where paths with and without a load meet, the compiler
+    // has to wait for all that are in flight.
+    // Pages of whole multiples of 16 tokens: the wave's 16 tokens are in one
+    // page, their rows one after the other.
+    const bool one_page = a.one_page;
     auto look_up = [&](int x) -> int {
-        if (x >= end)
-            return -1;
-        const int j = tile_of(x) * kTile + lane % kTile;
-        return seen_by_any(j) ? table[divide(j, a.page_magic, a.page_shift)] : -1;
+        const int j0 = first_of(x) + 16 * wave, j = one_page ? j0 : j0 + n;
+        const bool seen = x < end && (one_page ? j0 <= last_token && (a.window == 0 || j0 + 15 > span.pmin - a.window ||
+                                                                     j0 < a.sinks)
+                                               : seen_by_any(j));
+        const int page = table[seen ? divide(j, a.page_magic, a.page_shift) : 0u];
+        return seen ? page : -1;
     };
-    auto row_of = [&](int page, int x) -> uint32_t {
-        if ((uint32_t)page >= (uint32_t)a.num_pages)
-            return kNoRow;
-        const uint32_t j = tile_of(x) * kTile + lane % kTile;
-        const uint32_t off = j - divide(j, a.page_magic, a.page_shift) * a.page_size;
-        return ((uint32_t)page * a.Hkv + h) * a.page_size + off;
+    // The cache row of token 16 * wave + n, and where the wave's rows are one
+    // after the other the first of them.
+    struct Rows {
+        uint32_t mine, first;
+    };
+    auto rows_of = [&](int page, int x) -> Rows {
+        const int j0 = first_of(x) + 16 * wave;
+        Rows r{kNoRow, 0u};
+        if (one_page) {
+            const uint32_t p = __builtin_amdgcn_readfirstlane(page);
+            const uint32_t off = j0 - divide(j0, a.page_magic, a.page_shift) * a.page_size;
+            if (p < (uint32_t)a.num_pages) {
+                r.first = (p * a.Hkv + h) * a.page_size + off;
+                r.mine = seen_by_any(j0 + n) ? r.first + n : kNoRow;
+            }
+        } else if ((uint32_t)page < (uint32_t)a.num_pages) {
+            const uint32_t off = j0 + n - divide(j0 + n, a.page_magic, a.page_shift) * a.page_size;
+            r.mine = ((uint32_t)page * a.Hkv + h) * a.page_size + off;
+        }
+        return r;
     };
     // Rows in the cache are below 2^32, byte offsets are not: 64-bit products.
     auto at = [&](const void *cache, uint32_t row) {
         return static_cast<const T *>(cache) + (uint64_t)(row == kNoRow ? 0u : row) * D;
     };
 
-    u32x4 kr[2][KS], vr[NL];
-    auto load_k = [&](uint32_t row) {
+    // Whole rows of the wave's 16 tokens; to LDS in the same order.
+    u32x4 kr[KS], vr[KS];
+    // They are read once: the nontemporal hint gives 6.75 TB/s of such rows
+    // instead of 6.05.
+    auto load = [&](u32x4 (&r)[KS], const void *cache, Rows rows) {
+        if (one_page) {
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const T *>(cache) + (uint64_t)rows.first * D);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const T *p = at(a.k_cache, __shfl(row, t * 16 + n)) + c * 8;
+            for (int i = 0; i < KS; ++i)
+                r[i] = __builtin_nontemporal_load(p + (i * kWave + lane));
+        } else {
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-                kr[t][s] = *reinterpret_cast<const u32x4 *>(p + s * 32);
+            for (int i = 0; i < KS; ++i) {
+                const int unit = i * kWave + lane;
+                const u32x4 *p = reinterpret_cast<const u32x4 *>(at(cache, __shfl(rows.mine, unit / U)) + unit % U * 8);
+                r[i] = __builtin_nontemporal_load(p);
+            }
         }
     };
-    auto load_v = [&](uint32_t row) {
+    auto store = [&](const u32x4 (&r)[KS]) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
+        for (int i = 0; i < KS; ++i) {
             const int unit = i * kWave + lane;
-            vr[i] = *reinterpret_cast<const u32x4 *>(at(a.v_cache, __shfl(row, unit / U)) + unit % U * 8);
+            *reinterpret_cast<u32x4 *>(kv_lds + (16 * wave + unit / U) * kPitch + unit % U * 16) = r[i];
         }
     };
 
-    char *region = lds + wave * kRegion;
-    const char *tr_base = region + (4 * c + n / 4) * kPitch + n % 4 * 8;
-
-    int x = begin + wave;
-    int page = look_up(x);
-    uint32_t row = row_of(page, x);
-    if (x < end) {
-        load_k(row);
-        page = look_up(x + kWaves);
-        load_v(row);
+    int page = look_up(begin);
+    // Queries of column tile t, step q: column n's values 32 q + 8 c ...
+    auto query_at = [&](int t, int q) {
+        const int x = x0 + t * 16 + n;
+        const bool live = x < span.n * G;
+        const int r = live ? x / G : 0, g = live ? x - r * G : 0;
+        return static_cast<const T *>(a.q) + (span.start + r) * a.q_stride + (int64_t)(h * G + g) * D + q * 32 + c * 8;
+    };
+    x8 qf[kQueriesInLds ? 1 : NT][KS];
+    if constexpr (kQueriesInLds) {
+        constexpr int P = (NT * KS + kWaves - 1) / kWaves;
+        u32x4 v[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {  // all in flight before the first is stored
+            const int piece = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
+            v[i] = *reinterpret_cast<const u32x4 *>(query_at(piece / KS, piece % KS));
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int piece = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
+            q_lds[piece * kWave + lane] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int q = 0; q < KS; ++q)
+                qf[t][q] = *reinterpret_cast<const x8 *>(query_at(t, q));
     }
-    for (; x < end; x += kWaves) {
-        const int j0 = tile_of(x) * kTile;
-        const uint32_t present = (uint32_t)__ballot(row != kNoRow);  // bit t: token t has a row
-        const uint32_t row_now = row;
+    int pos[NT];  // positions of this lane's columns (-1: no such column)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int x = x0 + t * 16 + n;
+        pos[t] = x < span.n * G ? span.first_pos + x / G : -1;
+    }
+    if (threadIdx.x < NT * 16)
+        col_max[threadIdx.x] = -__builtin_inff();
+    Rows rows = rows_of(page, begin);
+    load(kr, a.k_cache, rows);
+    page = look_up(begin + 1);
+    load(vr, a.v_cache, rows);
+    lds_barrier();
 
-        float4_t s[NT][2];
+    float4_t acc[NT][DW];
+    float m[NT], l[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            s[t][0] = s[t][1] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t) {
+        m[t] = -__builtin_inff();
+        l[t] = 0.f;
 #pragma unroll
-            for (int q = 0; q < KS; ++q) {
+        for (int d = 0; d < DW; ++d)
+            acc[t][d] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int x = begin; x < end; ++x) {
+        const int j0 = first_of(x) + 16 * wave;  // the wave's first token
+        const uint32_t present = (uint32_t)__ballot(rows.mine != kNoRow) & 0xFFFFu;
+        const uint32_t row_now = rows.mine;
+
+        store(kr);
+        rows = rows_of(page, x + 1);
+        load(kr, a.k_cache, rows);
+        page = look_up(x + 2);
+        wave_lds_sync();
+        float4_t s[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            s[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < KS; ++q) {
+            const x8 kf = *reinterpret_cast<const x8 *>(kv_lds + (16 * wave + n) * kPitch + q * 64 + c * 16);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
                 x8 qv;
                 if constexpr (kQueriesInLds)
                     qv = __builtin_bit_cast(x8, q_lds[(t * KS + q) * kWave + lane]);
                 else
                     qv = qf[t][q];
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    s[t][k] = E::mfma(__builtin_bit_cast(x8, kr[k][q]), qv, s[t][k]);
+                s[t] = E::mfma(kf, qv, s[t]);
             }
-        }
-        const bool more = x + kWaves < end;
-        if (more) {
-            row = row_of(page, x + kWaves);
-            load_k(row);
-            page = look_up(x + 2 * kWaves);
+            if (NT * KS >= 16 && q % 2 == 1)  // not all of the operands in registers at once
+                __builtin_amdgcn_sched_barrier(0);
         }
 
-        // V to LDS. In tiles that not every row sees whole, values that could
-        // poison a product with p = 0 are kept out: tokens without a row are
-        // cleared, non-finite values are cleared here and added back below for
-        // the rows that see them.
-        const bool partial = present != 0xFFFFFFFFu || j0 + kTile - 1 > span.pmin ||
-                             (a.window > 0 && j0 <= span.pmax - a.window && j0 + kTile > a.sinks);
-        uint32_t poisoned = 0;  // tokens with non-finite values
+        // Tiles that not every row sees whole: scores that a row does not see
+        // are -infinity.
+        const bool partial = present != 0xFFFFu || j0 + 15 > span.pmin ||
+                             (a.window > 0 && j0 <= span.pmax - a.window && j0 + 16 > a.sinks);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            s[t] *= a.scale_log2;
+            if (partial) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = j0 + 4 * c + i;
+                    const bool sees = j <= pos[t] && (present >> (4 * c + i) & 1u) &&
+                                      (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
+                    s[t][i] = sees ? s[t][i] : -__builtin_inff();
+                }
+            }
+            const float top = fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3]));
+            if (top > m[t] + kRaise)
+                __hip_atomic_fetch_max(&col_max[t * 16 + n], top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+        lds_barrier();  // the columns' maxima are in
+
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float up = col_max[t * 16 + n];
+            if (__any(up > m[t])) {
+                const float f = up > m[t] ? __builtin_amdgcn_exp2f(m[t] - up) : 1.f;
+                m[t] = up;
+                l[t] *= f;
+#pragma unroll
+                for (int d = 0; d < DW; ++d)
+                    acc[t][d] *= f;
+            }
+            const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+            x4 hi, lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float p = __builtin_amdgcn_exp2f(s[t][i] - base);
+                l[t] += p;
+                hi[i] = (T)p;
+                lo[i] = (T)(p - (float)hi[i]);
+            }
+            const int to = (t * 16 + n) * kColumn + 16 * wave + 4 * c;
+            *reinterpret_cast<x4 *>(&p_hi[to]) = hi;
+            *reinterpret_cast<x4 *>(&p_lo[to]) = lo;
+        }
+        // V to LDS. In partly visible tiles, values that could poison a product
+        // with p = 0 are kept out: tokens without a row are cleared, non-finite
+        // values are cleared here and added back below for the rows that see them.
+        uint32_t bad = 0;
         if (partial) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
+            for (int i = 0; i < KS; ++i) {
                 const int token = (i * kWave + lane) / U;
                 u32x4 v = vr[i];
                 const u32x4 zero{0u, 0u, 0u, 0u};
@@ -309,253 +535,258 @@ __global__ __launch_bounds__(kThreads, (D * NT <= 128 ? 2 : 1)) void attn_kernel
                 const u32x4 f{finite_halves<T>(v.x), finite_halves<T>(v.y), finite_halves<T>(v.z),
                               finite_halves<T>(v.w)};
                 const bool differs = f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w;
-                poisoned |= differs ? 1u << token : 0u;
+                bad |= differs ? 1u << token : 0u;
                 vr[i] = f;
             }
 #pragma unroll
             for (int d = 1; d < kWave; d *= 2)
-                poisoned |= __shfl_xor(poisoned, d);
+                bad |= __shfl_xor(bad, d);
         }
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int unit = i * kWave + lane;
-            *reinterpret_cast<u32x4 *>(region + unit / U * kPitch + unit % U * 16) = vr[i];
+        store(vr);
+        if (lane < 16) {
+            rows_lds[16 * wave + lane] = row_now;
+            reinterpret_cast<uint32_t *>(bad_tokens)[wave] = bad;
         }
-        if (more)
-            load_v(row);
+        load(vr, a.v_cache, rows);
+        lds_barrier();  // P and V are in
 
-        x8 hi[NT], lo[NT];
+        // Step q takes tokens 4c .. 4c+3 of waves 2q and 2q+1.
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float v[8];
+        for (int q = 0; q < kWaves / 2; ++q) {
+            x8 vt[DW];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float w = s[t][k][i] * a.scale_log2;
-                    if (partial) {
-                        const int tok = k * 16 + 4 * c + i, j = j0 + tok;
-                        const bool sees = j <= pos[t] && (present >> tok & 1u) &&
-                                          (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
-                        w = sees ? w : -__builtin_inff();
-                    }
-                    v[4 * k + i] = w;
-                }
-            const float top = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
-                                    fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-            if (__any(top > m[t] + kRaise)) {
-                float up = fmaxf(top, __shfl_xor(top, 16));
-                up = fmaxf(m[t], fmaxf(up, __shfl_xor(up, 32)));
-                const float f = up == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - up);
-                m[t] = up;
-                l[t] *= f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-                    acc[t][d] *= f;
+            for (int d = 0; d < DW; ++d) {
+                const int dt = wave + kWaves * d;
+                if (DT % kWaves != 0 && dt >= DT)
+                    break;
+                typedef __attribute__((address_space(3))) short4_t lds4;
+                const char *p = kv_lds + tr_offset + 32 * q * kPitch + dt * 32;
+                const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
+                const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 16 * kPitch));
+                vt[d] = __builtin_bit_cast(x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
             }
-            const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p = __builtin_amdgcn_exp2f(v[i] - base);
-                sum += p;
-                hi[t][i] = (T)p;
-                lo[t][i] = (T)(p - (float)hi[t][i]);
-            }
-            l[t] += sum;
-        }
-
-        wave_lds_sync();
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            typedef __attribute__((address_space(3))) short4_t lds4;
-            const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(tr_base + d * 32));
-            const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(tr_base + d * 32 + 16 * kPitch));
-            const x8 vt = __builtin_bit_cast(x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                acc[t][d] = E::mfma(vt, hi[t], acc[t][d]);
-                acc[t][d] = E::mfma(vt, lo[t], acc[t][d]);
+                const int from = (t * 16 + n) * kColumn + 32 * q + 4 * c;
+                const x8 hi = __builtin_shufflevector(*reinterpret_cast<const x4 *>(&p_hi[from]),
+                                                      *reinterpret_cast<const x4 *>(&p_hi[from + 16]), 0, 1, 2, 3, 4, 5, 6, 7);
+                const x8 lo = __builtin_shufflevector(*reinterpret_cast<const x4 *>(&p_lo[from]),
+                                                      *reinterpret_cast<const x4 *>(&p_lo[from + 16]), 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                for (int d = 0; d < DW; ++d) {
+                    if (DT % kWaves != 0 && wave + kWaves * d >= DT)
+                        break;
+                    acc[t][d] = E::mfma(vt[d], hi, acc[t][d]);
+                    acc[t][d] = E::mfma(vt[d], lo, acc[t][d]);
+                }
+                if constexpr (NT >= 3)  // not all of the operands in registers at once
+                    __builtin_amdgcn_sched_barrier(0);
             }
         }
-        wave_lds_sync();
 
-        if (poisoned) {  // a token of a partly visible tile holds infinities or NaN
-            for (int tok = 0; tok < kTile; ++tok) {
-                if (!(poisoned >> tok & 1u))
-                    continue;
-                const T *vp = at(a.v_cache, __builtin_amdgcn_readlane(row_now, tok)) + 4 * c;
-                const int from = tok % 16 / 4 * 16 + n, which = tok / 16 * 4 + tok % 4, j = j0 + tok;
+        u32x4 any_bad = bad_tokens[0];
+        if constexpr (kWaves == 8)
+            any_bad |= bad_tokens[1];
+        const uint32_t some = __builtin_amdgcn_readfirstlane(any_bad.x | any_bad.y | any_bad.z | any_bad.w);
+        for (int v = 0; some && v < kWaves; ++v) {
+            uint32_t left = __builtin_amdgcn_readfirstlane(reinterpret_cast<const uint32_t *>(bad_tokens)[v]);
+            while (left) {  // a token of a partly visible tile holds infinities or NaN
+                const int tok = 16 * v + __builtin_ctz(left);
+                left &= left - 1;
+                const int j = first_of(x) + tok;
+                const T *vp = at(a.v_cache, rows_lds[tok]) + 4 * c;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float p = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        p = i == which ? (float)hi[t][i] + (float)lo[t][i] : p;
-                    p = __shfl(p, from);
+                    const int from = (t * 16 + n) * kColumn + tok;
+                    const float p = (float)p_hi[from] + (float)p_lo[from];
                     const bool sees = j <= pos[t] && (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
 #pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        const u32x2 raw = *reinterpret_cast<const u32x2 *>(vp + d * 16);
-                        const typename E::x4 v4 = __builtin_bit_cast(typename E::x4, raw);
+                    for (int d = 0; d < DW; ++d) {
+                        const int dt = wave + kWaves * d;
+                        if (DT % kWaves != 0 && dt >= DT)
+                            break;
+                        const u32x2 raw = *reinterpret_cast<const u32x2 *>(vp + dt * 16);
+                        const x4 v4 = __builtin_bit_cast(x4, raw);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float v = (float)v4[i];
-                            const bool odd = !(__builtin_fabsf(v) < __builtin_inff());
-                            acc[t][d][i] += odd && sees ? p * v : 0.f;
+                            const float f = (float)v4[i];
+                            const bool odd = !(__builtin_fabsf(f) < __builtin_inff());
+                            acc[t][d][i] += odd && sees ? p * f : 0.f;
                         }
                         __builtin_amdgcn_sched_barrier(0);  // rare: few registers rather than loads in flight
                     }
                 }
             }
         }
+        lds_barrier();  // every wave is past V and P
     }
 
-    // Join of the four waves. Every lane of a column has the same m.
+    // Sums of the columns over the lanes and waves that share them.
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         l[t] += __shfl_xor(l[t], 16);
         l[t] += __shfl_xor(l[t], 32);
         if (c == 0)
-            stats[wave][t * 16 + n] = float2_t{m[t], l[t]};
+            col_sum[wave][t * 16 + n] = l[t];
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        float top = -__builtin_inff();
+        const int x = x0 + t * 16 + n;
+        if (x >= span.n * G)
+            continue;
+        float total = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            top = fmaxf(top, stats[w][t * 16 + n].x);
-        const float f = top == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[t] - top);
-        float *mine = reinterpret_cast<float *>(region) + n * kJoinPitch + 4 * c;
+        for (int v = 0; v < kWaves; ++v)
+            total += col_sum[v][t * 16 + n];
+        const int r = x / G;
+        const int64_t at_row = (int64_t)(span.start + r) * a.Hq + h * G + (x - r * G);
+        const bool first = wave == 0 && c == 0;
+        if (begin == 0 && end == count) {
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            T *to = static_cast<T *>(a.out) + at_row * D + wave * 16 + 4 * c;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-            *reinterpret_cast<float4_t *>(mine + d * 16) = acc[t][d] * f;
-        __syncthreads();
-        for (int i = threadIdx.x; i < 16 * D / 4; i += kThreads) {
-            const int col = i / (D / 4), d = i % (D / 4) * 4;
-            const int x = x0 + t * 16 + col;
-            if (x >= span.n * G)
-                continue;
-            float total = 0.f, big = -__builtin_inff();
+            for (int d = 0; d < DW; ++d) {
+                x4 y;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                big = fmaxf(big, stats[w][t * 16 + col].x);
-            float4_t o{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float2_t ml = stats[w][t * 16 + col];
-                total += big == -__builtin_inff() ? ml.y : ml.y * __builtin_amdgcn_exp2f(ml.x - big);
-                o += *reinterpret_cast<const float4_t *>(reinterpret_cast<const float *>(lds + w * kRegion) +
-                                                         col * kJoinPitch + d);
+                for (int i = 0; i < 4; ++i)
+                    y[i] = (T)(acc[t][d][i] * inv);  // the output's one rounding
+                if (DT % kWaves == 0 || wave + kWaves * d < DT)
+                    *reinterpret_cast<x4 *>(to + kWaves * d * 16) = y;
             }
-            const int r = x / G;
-            const int64_t at_row = (int64_t)(span.start + r) * a.Hq + h * G + (x - r * G);
-            if (pieces == 1) {
-                const float inv = total == 0.f ? 0.f : 1.f / total;
-                typename E::x4 y;
+            if (first && a.lse)
+                a.lse[at_row] = total == 0.f ? -__builtin_inff()
+                                             : (m[t] + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f;
+        } else {
+            const int64_t part = (int64_t)slot_of(w, begin == 0) * kColumns + t * 16 + n;
+            float *to = a.part_acc + part * D + wave * 16 + 4 * c;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    y[k] = (T)(o[k] * inv);  // the output's one rounding
-                *reinterpret_cast<typename E::x4 *>(static_cast<T *>(a.out) + at_row * D + d) = y;
-                if (a.lse && d == 0)
-                    a.lse[at_row] = total == 0.f ? -__builtin_inff()
-                                                 : (big + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f;
-            } else {
-                *reinterpret_cast<float4_t *>(a.part_acc + (at_row * a.splits + z) * D + d) = o;
-                if (d == 0)
-                    *reinterpret_cast<float2_t *>(a.part_ml + (at_row * a.splits + z) * 2) = float2_t{big, total};
-            }
+            for (int d = 0; d < DW; ++d)
+                if (DT % kWaves == 0 || wave + kWaves * d < DT)
+                    *reinterpret_cast<float4_t *>(to + kWaves * d * 16) = acc[t][d];
+            if (first)
+                *reinterpret_cast<float2_t *>(a.part_ml + part * 2) = float2_t{m[t], total};
         }
-        __syncthreads();
+    }
+
+    left -= end - begin;
+    if (left <= 0)
+        return;
+    tile = 0;
+    item_unit += count;
+    if (++h == a.Hkv) {  // the next item that exists (there is one: the run is not done)
+        h = 0;
+        ++chunk;
+        while (chunk == a.chunks || chunk * kColumns >= span_of<kTile>(a, b, 0, kColumns).n * G) {
+            chunk = 0;
+            if (++b >= a.B)
+                return;
+        }
+    }
     }
 }
 
-// Join of the splits of one (row, head): sum_z acc_z 2^(m_z - M) over
-// sum_z l_z 2^(m_z - M). A workgroup's threads are D/4 values wide and the rest
-// of them share the splits, so that their loads are in flight together.
+// Join of the pieces of an item that several runs share:
+// sum_z acc_z 2^(m_z - M) over sum_z l_z 2^(m_z - M) for each column. A
+// workgroup's threads are D/4 values wide and the rest of them share the
+// pieces, so that their loads are in flight together.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a, int cols)
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a, int columns)
 {
     using E = Elem<T>;
-    constexpr int W = D / 4;                // threads of one split's values
-    constexpr int P = kThreads / W;         // splits read at a time
-    __shared__ float4_t part[P][W];
-    __shared__ float sums[P];
-    const int head = blockIdx.x % a.Hq, r = blockIdx.x / a.Hq, b = blockIdx.y;
+    constexpr int W = D / 4;                // threads of one piece's values
+    const int P = blockDim.x / W;           // pieces read at a time
+    __shared__ float4_t part[kJoinThreads / W][W];
+    __shared__ float sums[kJoinThreads / W];
     const int G = a.Hq / a.Hkv;
-    const int x = r * G + head % G;
-    const Span span = span_of(a, b, x / cols * cols, cols);
-    const int pieces = splits_of(a, span.count);
-    if (r >= span.n || x >= a.chunks * cols || pieces == 1)
+    const int h = blockIdx.x % a.Hkv, k = blockIdx.x / a.Hkv % a.chunks, b = blockIdx.x / a.Hkv / a.chunks;
+    const int x0 = k * columns;
+    const int begin = a.row_starts[b], end = a.row_starts[b + 1];
+    const int2 join = a.joins[blockIdx.x];  // of items that exist
+    const int rows = begin >= 0 && begin <= end && end <= a.T ? end - begin : 0;
+    const int live = x0 + columns < rows * G ? columns : rows * G - x0;
+    if (live <= 0 || join.x == join.y)
         return;
-    const int64_t at_row = (int64_t)(span.start + r) * a.Hq + head;
-    const float2_t *ml = reinterpret_cast<const float2_t *>(a.part_ml) + at_row * a.splits;
-    float top = -__builtin_inff();
-    for (int z = threadIdx.x % kWave; z < pieces; z += kWave)
-        top = fmaxf(top, ml[z].x);
+    const int pieces = join.y - join.x + 1;
+    auto slot = [&](int z) { return (int64_t)slot_of(join.x + z, z == 0) * columns; };
+    for (int col = blockIdx.y; col < live; col += gridDim.y) {
+        const int x = x0 + col, r = x / G;
+        const int64_t at_row = (int64_t)(begin + r) * a.Hq + h * G + (x - r * G);
+        const float2_t *ml = reinterpret_cast<const float2_t *>(a.part_ml) + col;
+        float top = -__builtin_inff();
+        for (int z = threadIdx.x % kWave; z < pieces; z += kWave)
+            top = fmaxf(top, ml[slot(z)].x);
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2)
-        top = fmaxf(top, __shfl_xor(top, d));
-    const int d4 = threadIdx.x % W, first = threadIdx.x / W;
-    float4_t o{0.f, 0.f, 0.f, 0.f};
-    float total = 0.f;
-    if (first < P) {
-#pragma unroll 4
-        for (int z = first; z < pieces; z += P) {
-            const float2_t v = ml[z];
-            const float f = top == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(v.x - top);
-            total += v.y * f;
-            o += *reinterpret_cast<const float4_t *>(a.part_acc + (at_row * a.splits + z) * D + d4 * 4) * f;
+        for (int d = 1; d < kWave; d *= 2)
+            top = fmaxf(top, __shfl_xor(top, d));
+        const int d4 = threadIdx.x % W, first = threadIdx.x / W;
+        float4_t o{0.f, 0.f, 0.f, 0.f};
+        float total = 0.f;
+        if (first < P) {
+#pragma unroll 8
+            for (int z = first; z < pieces; z += P) {
+                const float2_t v = ml[slot(z)];
+                const float f = top == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(v.x - top);
+                total += v.y * f;
+                o += *reinterpret_cast<const float4_t *>(a.part_acc + (slot(z) + col) * D + d4 * 4) * f;
+            }
+            part[first][d4] = o;
+            if (d4 == 0)
+                sums[first] = total;
         }
-        part[first][d4] = o;
-        if (d4 == 0)
-            sums[first] = total;
-    }
-    __syncthreads();
-    if (first == 0) {
-        for (int p = 1; p < P; ++p) {
-            o += part[p][d4];
-            total += sums[p];
-        }
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        typename E::x4 y;
+        __syncthreads();
+        if (first == 0) {
+            for (int p = 1; p < P && p < pieces; ++p) {
+                o += part[p][d4];
+                total += sums[p];
+            }
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            typename E::x4 y;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            y[k] = (T)(o[k] * inv);
-        *reinterpret_cast<typename E::x4 *>(static_cast<T *>(a.out) + at_row * D + d4 * 4) = y;
-        if (a.lse && d4 == 0)
-            a.lse[at_row] = total == 0.f ? -__builtin_inff()
-                                         : (top + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f;
+            for (int k = 0; k < 4; ++k)
+                y[k] = (T)(o[k] * inv);
+            *reinterpret_cast<typename E::x4 *>(static_cast<T *>(a.out) + at_row * D + d4 * 4) = y;
+            if (a.lse && d4 == 0)
+                a.lse[at_row] = total == 0.f ? -__builtin_inff()
+                                             : (top + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f;
+        }
+        __syncthreads();
     }
 }
 
 template <typename T, int D, int NT>
 hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
-    const int64_t work = (int64_t)a.Hkv * a.splits * a.B;
-    const int64_t blocks = (work + 7) / 8 * 8 * a.chunks;
-    attn_kernel<T, D, NT><<<dim3((uint32_t)blocks), kThreads, 0, stream>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1)
+    attn_kernel<T, D, NT><<<dim3((uint32_t)p.blocks), waves_of(D) * kWave, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.whole)
         return e;
-    const int G = a.Hq / a.Hkv;
-    const int rows = a.chunks * 16 * NT / G + 1;  // at least max_rows
-    attn_join_kernel<T, D><<<dim3((uint32_t)(a.Hq * rows), a.B), kThreads, 0, stream>>>(a, 16 * NT);
+    attn_join_kernel<T, D><<<dim3((uint32_t)p.items, p.join_columns), p.join_threads, 0, stream>>>(a, 16 * NT);
     return hipGetLastError();
 }
+
+// Column tiles that a workgroup takes at most: with more, the accumulators
+// (D / 16 registers a tile) and the queries in LDS would leave room for one
+// workgroup on a CU instead of two.
+constexpr int most_col_tiles(int D) { return D == 64 || D == 128 ? 6 : D == 96 ? 4 : 3; }
 
 template <typename T, int D>
 hipError_t launch_cols(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
-    if (p.col_tiles == 1)
-        return launch<T, D, 1>(a, p, stream);
-    if (p.col_tiles == 2)
-        return launch<T, D, 2>(a, p, stream);
-    if constexpr (D <= 128)
-        if (p.col_tiles == 4)
+    switch (p.col_tiles) {
+    case 1: return launch<T, D, 1>(a, p, stream);
+    case 2: return launch<T, D, 2>(a, p, stream);
+    case 3: return launch<T, D, 3>(a, p, stream);
+    case 4:
+        if constexpr (most_col_tiles(D) >= 4)
             return launch<T, D, 4>(a, p, stream);
-    return hipErrorInvalidValue;
+        return hipErrorInvalidValue;
+    case 6:
+        if constexpr (most_col_tiles(D) >= 6)
+            return launch<T, D, 6>(a, p, stream);
+        return hipErrorInvalidValue;
+    default: return hipErrorInvalidValue;
+    }
 }
 
 template <typename T>
@@ -575,33 +806,58 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, int D, hipStream_t s
 
 bool attn_head_dim_supported(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
-AttnPlan attn_plan(int T, int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks)
+AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks,
+                   int page_size, int max_pages)
 {
     AttnPlan p;
     const int64_t columns = (int64_t)max_rows * (Hq / Hkv);
-    const int most = D <= 128 ? 4 : 2;  // column tiles whose accumulators fit the registers
-    p.col_tiles = columns <= 16 ? 1 : columns <= 32 || most == 2 ? 2 : 4;
-    p.chunks = (int)((columns + 16 * p.col_tiles - 1) / (16 * p.col_tiles));
+    const int64_t col_tiles = (columns + 15) / 16;
+    const int64_t chunks = (col_tiles + most_col_tiles(D) - 1) / most_col_tiles(D);
+    p.col_tiles = (int)((col_tiles + chunks - 1) / chunks);
+    p.col_tiles += p.col_tiles == 5;
+    p.chunks = (int)((col_tiles + p.col_tiles - 1) / p.col_tiles);
+    const int kTile = tile_of(D);
     int64_t visible = max_context;
     if (window > 0 && (int64_t)window + max_rows + sinks + 2 * kTile < visible)
         visible = (int64_t)window + max_rows + sinks + 2 * kTile;
-    const int64_t tiles = (visible + kTile - 1) / kTile;
-    const int64_t base = (int64_t)B * Hkv * p.chunks;
-    const int64_t target = 4 * (int64_t)device_cu_count();
-    int64_t each = (tiles * base + target - 1) / target;
-    each = each < 2 * kWaves ? 2 * kWaves : (each + kWaves - 1) / kWaves * kWaves;
-    p.split_tiles = (int)each;
-    p.splits = (int)((tiles + each - 1) / each);
-    p.splits = p.splits < 1 ? 1 : p.splits;
-    p.workspace_bytes = p.splits == 1 ? 0 : (size_t)T * Hq * p.splits * (D + 2) * sizeof(float);
+    const int64_t tiles = visible > kTile ? (visible + kTile - 1) / kTile : 1;
+    const int64_t items = (int64_t)B * Hkv * p.chunks;
+    // Workgroups of a full GPU: as many as keep 64 KB of K and V or more in
+    // flight on a CU (a workgroup has a tile of each).
+    const int per_cu = PERCU ? PERCU : D >= 128 ? 1 : 4;
+    const int64_t full = (int64_t)per_cu * device_cu_count();
+    // The runs count tiles in 31 bits, up to the block table's end.
+    const int64_t most_tiles = items * ((int64_t)max_pages * page_size / kTile + 1);
+    p.whole = tiles <= 2 || items >= 8 * full || most_tiles > INT32_MAX;
+    const int64_t groups = items * tiles < full ? items * tiles : full;
+    p.groups = (int)groups;
+    p.items = items;
+    p.blocks = p.whole ? ((int64_t)B * Hkv + 7) / 8 * 8 * p.chunks : p.groups;
+    // Workgroups of the join for each item: one for each column while the items
+    // have many pieces, else one for a few columns; and their threads.
+    const int live = (int)(columns < 16 * p.col_tiles ? columns : 16 * p.col_tiles);
+    p.pieces = items * 4 <= groups;
+    p.join_columns = p.pieces ? live : (live + 3) / 4;
+    p.join_threads = items * 16 <= groups ? kJoinThreads : 256;
+    p.join_bytes = p.whole ? 0 : (items * sizeof(int2) + 15) / 16 * 16;
+    p.workspace_bytes =
+        p.whole ? 0 : p.join_bytes + (size_t)p.groups * 2 * 16 * p.col_tiles * (D + 2) * sizeof(float);
     return p;
 }
 
-hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, hipStream_t stream)
+hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, void *workspace, hipStream_t stream)
 {
     a.chunks = p.chunks;
-    a.splits = p.splits;
-    a.split_tiles = p.split_tiles;
+    a.groups = p.groups;
+    a.whole = p.whole;
+    a.pieces = p.pieces;
+    a.one_page = a.page_size % 16 == 0;
+    if (!p.whole) {
+        const size_t columns = (size_t)p.groups * 2 * 16 * p.col_tiles;
+        a.joins = static_cast<int2 *>(workspace);
+        a.part_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.join_bytes);
+        a.part_ml = a.part_acc + columns * D;
+    }
     return bf16 ? launch_dim<__bf16>(a, p, D, stream) : launch_dim<_Float16>(a, p, D, stream);
 }
 

@@ -41,9 +41,11 @@ int check_attention_sizes(int T, int B, int Hq, int Hkv, int D, int max_rows, in
 
 constexpr int kFar = 1 << 30;  // positions minus the window stay in 32 bits
 
-qmm::AttnPlan plan_of(int T, int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks)
+qmm::AttnPlan plan_of(int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks,
+                      int page_size, int max_pages)
 {
-    return qmm::attn_plan(T, B, Hq, Hkv, D, max_rows, max_context, window < kFar ? window : 0, sinks);
+    return qmm::attn_plan(B, Hq, Hkv, D, max_rows, max_context, window < kFar ? window : 0, sinks, page_size,
+                          max_pages);
 }
 
 }  // namespace
@@ -112,7 +114,8 @@ size_t qmm_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D,
 {
     if (check_attention_sizes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks) != QMM_OK)
         return 0;
-    return plan_of(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks).workspace_bytes;
+    // the largest that any block table needs
+    return plan_of(B, Hq, Hkv, D, max_rows, max_context, window, sinks, 1, 1).workspace_bytes;
 }
 
 int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache, int type,
@@ -133,13 +136,13 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
     if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX - 64 || q_stride < (int64_t)Hq * D ||
         !isfinite(scale))
         return QMM_ERR_SHAPE;
-    const qmm::AttnPlan plan = plan_of(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks);
+    const qmm::AttnPlan plan =
+        plan_of(B, Hq, Hkv, D, max_rows, max_context, window, sinks, page_size, max_pages);
     if (plan.workspace_bytes > 0 && !workspace)
         return QMM_ERR_NULL;
     if (workspace_bytes < plan.workspace_bytes)
         return QMM_ERR_WORKSPACE;
-    const int64_t blocks = ((int64_t)Hkv * plan.splits * B + 7) / 8 * 8 * plan.chunks;
-    if (blocks > INT32_MAX / 256)  // the runtime's limit on threads of a launch
+    if (plan.blocks > INT32_MAX / 256 || plan.items > INT32_MAX / 256)  // the runtime's limit on threads of a launch
         return QMM_ERR_SHAPE;
     if (q_stride % 8 != 0 || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         (plan.workspace_bytes > 0 && !aligned(workspace, 16)) || !aligned(block_table, 4) ||
@@ -154,8 +157,6 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
     a.row_starts = row_starts;
     a.out = out;
     a.lse = lse;
-    a.part_acc = static_cast<float *>(workspace);
-    a.part_ml = a.part_acc ? a.part_acc + (size_t)T * Hq * plan.splits * D : nullptr;
     a.q_stride = q_stride;
     a.T = T;
     a.B = B;
@@ -170,7 +171,7 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
     const qmm::MagicDiv d = qmm::magic_div(page_size);
     a.page_magic = d.magic;
     a.page_shift = d.shift;
-    return qmm::launch_paged_attention(a, plan, D, type == QMM_BF16, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+    return qmm::launch_paged_attention(a, plan, D, type == QMM_BF16, workspace, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 
 size_t qmm_sample_workspace_bytes(int M, int V)

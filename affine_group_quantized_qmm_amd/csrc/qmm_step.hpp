@@ -31,12 +31,13 @@ hipError_t launch_qk_norm_rope(const RopeArgs &a, int in_type, bool bf16_out, bo
 struct AttnArgs {
     const void *q;                            // [T, Hq, D], q_stride elements between rows
     const void *k_cache, *v_cache;            // [num_pages, Hkv, page_size, D]
-    const int32_t *block_table;               // [B, table_stride]
+    const int32_t *block_table;               // [B, max_pages]
     const int32_t *context_lens;              // [B]
     const int32_t *row_starts;                // [B + 1]
     void *out;                                // [T, Hq, D]
     float *lse;                               // [T, Hq] or null
-    float *part_acc, *part_ml;                // partials of the split launches
+    int2 *joins;                              // [B, chunks, Hkv]: first and last run of an item
+    float *part_acc, *part_ml;                // partials, two slots a run: [2 groups, columns, D] and [.., 2]
     int64_t q_stride;
     int T, B, Hq, Hkv, page_size, num_pages, max_pages;
     int window, sinks;
@@ -44,17 +45,22 @@ struct AttnArgs {
     uint64_t page_magic;                      // division by page_size (magic_div)
     int page_shift;
     int chunks;                               // column chunks of one (sequence, kv head)
-    int splits, split_tiles;                  // splits of the length, 32-token tiles of each
+    int groups;                               // runs
+    int whole, pieces;                        // how items are dealt out (qmm_attn.hip)
+    int one_page;                             // page_size is a multiple of 16
 };
 // How a call is laid out on the GPU; a function of host arguments only.
 struct AttnPlan {
     int col_tiles;    // 16-column tiles of a workgroup
-    int chunks, splits, split_tiles;
-    size_t workspace_bytes;
+    int chunks, groups, join_columns, join_threads;
+    bool whole, pieces;
+    int64_t blocks, items;
+    size_t join_bytes, workspace_bytes;
 };
 bool attn_head_dim_supported(int D);
-AttnPlan attn_plan(int T, int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks);
-hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, hipStream_t stream);
+AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks,
+                   int page_size, int max_pages);
+hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, void *workspace, hipStream_t stream);
 
 // Sampling (qmm_sample.hip).
 struct SampleArgs {

@@ -59,9 +59,9 @@ def test_attention_refuses(kw, code):
 
 def test_attention_workspace():
     f = qmm.qmm_paged_attention_workspace_bytes
-    assert f(4, 2, 4, 2, 128, 2, 64) == 0          # one split
+    assert f(4, 2, 4, 2, 128, 2, 64) == 0          # one workgroup for each sequence and head
     big = f(4, 2, 4, 2, 128, 2, 100000)
-    assert big > 0 and big % (4 * 4 * (128 + 2) * 4) == 0
+    assert big > 0 and f(4, 2, 4, 2, 128, 2, 10 ** 7) == big  # a full GPU, however long the context
     assert f(4, 2, 4, 2, 128, 2, 100000, 256, 4) < big  # a window is short whatever the context
     assert f(4, 2, 4, 3, 128, 2, 100000) == 0 and f(0, 2, 4, 2, 128, 2, 100000) == 0
 
