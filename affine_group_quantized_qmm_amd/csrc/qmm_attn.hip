@@ -72,6 +72,25 @@ struct Elem<__bf16> {
     }
 };
 
+template <int CTRL>
+__device__ __forceinline__ int dpp_or_zero(int v)
+{
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+// Inclusive sums over the lanes of a wave: within rows of 16 by shifts, then
+// the rows before.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += dpp_or_zero<0x111>(v);  // row_shr:1
+    v += dpp_or_zero<0x112>(v);
+    v += dpp_or_zero<0x114>(v);
+    v += dpp_or_zero<0x118>(v);
+    const int r0 = __builtin_amdgcn_readlane(v, 15), r1 = __builtin_amdgcn_readlane(v, 31),
+              r2 = __builtin_amdgcn_readlane(v, 47);
+    const int row = threadIdx.x % kWave / 16;
+    return v + (row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0);
+}
+
 // A 32-bit word with its non-finite halves set to zero.
 template <typename T>
 __device__ __forceinline__ uint32_t finite_halves(uint32_t w)
@@ -82,6 +101,11 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w)
     if ((w >> 16 & e) == e)
         w &= 0x0000FFFFu;
     return w;
+}
+
+__device__ __forceinline__ int row_of_column(const AttnArgs &a, int x)
+{
+    return divide(x, a.group_magic, a.group_shift);
 }
 
 // The rows and tiles of (sequence b, column chunk): what a workgroup and the
@@ -101,7 +125,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int begin, int end, i
     const bool sound = begin >= 0 && begin <= end && end <= a.T;
     s.start = sound ? begin : 0;
     s.n = sound ? end - begin : 0;
-    const int G = a.Hq / a.Hkv;
+    const int G = a.G;
     len = len < 0 ? 0 : len;
     s.first_pos = len - s.n;
     s.sink_tiles = s.low = s.count = 0;
@@ -109,8 +133,8 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int begin, int end, i
     if (x0 >= s.n * G)
         return s;
     const int last = x0 + cols < s.n * G ? x0 + cols : s.n * G;
-    s.pmin = s.first_pos + x0 / G;
-    s.pmax = s.first_pos + (last - 1) / G;
+    s.pmin = s.first_pos + row_of_column(a, x0);
+    s.pmax = s.first_pos + row_of_column(a, last - 1);
     // tokens past the table have no page
     const int capacity = a.max_pages * a.page_size;
     const int high = s.pmax + 1 < capacity ? s.pmax + 1 : capacity;
@@ -155,7 +179,8 @@ __device__ __forceinline__ int first_tile(Runs r, int w) { return w * r.each + (
 __device__ __forceinline__ int owner_of(Runs r, int tile)
 {
     const int longer = r.more * (r.each + 1);
-    return tile < longer ? tile / (r.each + 1) : r.more + (tile - longer) / r.each;
+    return tile < longer ? (uint32_t)tile / (uint32_t)(r.each + 1)
+                         : r.more + (uint32_t)(tile - longer) / (uint32_t)r.each;
 }
 
 // A run's partial results: of an item that it begins (but does not finish), and
@@ -199,11 +224,12 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int c = lane / 16, n = lane % 16;
-    const int G = a.Hq / a.Hkv;
+    const int G = a.G;
     constexpr int kColumns = 16 * NT;
 
     // Where the run starts: (sequence, chunk, head, tile), and its length.
     int b, chunk, h, tile = 0, w = 0, left, item_unit = 0, here = 1;
+    int run_begin, run_end, run_len;  // of sequence b
     Runs runs{1, 0};
     if (a.whole) {
         // One item a workgroup; the chunks of a head are 8 apart, that is on one
@@ -215,89 +241,109 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
         b = item / a.Hkv;
         if (b >= a.B)
             return;
-        const Span s = span_of<kTile>(a, b, chunk * kColumns, kColumns);
+        run_begin = a.row_starts[b];
+        run_end = a.row_starts[b + 1];
+        run_len = a.context_lens[b];
+        const Span s = span_of<kTile>(a, run_begin, run_end, run_len, chunk * kColumns, kColumns);
         if (chunk * kColumns >= s.n * G)
             return;
         left = tiles_of(s);
     } else {
         w = blockIdx.x;
         // Sequences are shared out to the lanes in order; the waves do the same.
-        // The host has checked that the sum of tiles has 31 bits.
+        // The host has checked that the sum of tiles has 31 bits. Up to 64
+        // sequences of one chunk stay in the lanes' registers.
+        const bool small = a.B <= kWave && a.chunks == 1;
         const int each = (a.B + kWave - 1) / kWave;
         const int b0 = lane * each, b1 = b0 + each < a.B ? b0 + each : a.B;
+        int lane_begin = 0, lane_end = 0, lane_len = 0, lane_tiles = 0;
+        if (__builtin_expect(small, 1)) {
+            if (lane < a.B) {
+                lane_begin = a.row_starts[lane];
+                lane_end = a.row_starts[lane + 1];
+                lane_len = a.context_lens[lane];
+            }
+            const Span s = span_of<kTile>(a, lane_begin, lane_end, lane_len, 0, kColumns);
+            lane_tiles = s.n > 0 ? tiles_of(s) : 0;
+        }
         // Tiles of this lane's items, or pieces of `size` tiles.
         auto sum_of = [&](int size) {
             int sum = 0;
-            for (int i = b0; i < b1; ++i)
-                for (int k = 0; k < a.chunks; ++k) {
-                    const Span s = span_of<kTile>(a, i, k * kColumns, kColumns);
-                    if (k * kColumns >= s.n * G)
-                        break;
-                    sum += size == 1 ? tiles_of(s) : (tiles_of(s) + size - 1) / size;
-                }
+            if (__builtin_expect(small, 1))
+                sum = size == 1 ? lane_tiles : (uint32_t)(lane_tiles + size - 1) / (uint32_t)size;
+            else
+                for (int i = b0; i < b1; ++i)
+                    for (int k = 0; k < a.chunks; ++k) {
+                        const Span s = span_of<kTile>(a, i, k * kColumns, kColumns);
+                        if (k * kColumns >= s.n * G)
+                            break;
+                        sum += size == 1 ? tiles_of(s) : (uint32_t)(tiles_of(s) + size - 1) / (uint32_t)size;
+                    }
             return sum * a.Hkv;
         };
-        auto wave_total = [&](int v) {
-#pragma unroll
-            for (int d = 1; d < kWave; d *= 2)
-                v += __shfl_xor(v, d);
-            return __builtin_amdgcn_readfirstlane(v);
-        };
-        int mine = sum_of(1);
-        const int total = wave_total(mine);
-        int size = 1, units = total;  // runs are dealt in tiles, pieces one by one
+        int mine = sum_of(1), upto = wave_scan(mine), size = 1, from = w;
+        int units = __builtin_amdgcn_readlane(upto, kWave - 1);  // runs are dealt in tiles, pieces one by one
+        left = 1;
         if (a.pieces) {
-            size = (total + a.groups - 1) / a.groups;
+            size = (units + a.groups - 1) / (uint32_t)a.groups;
             for (;;) {  // ends: with a size of the longest item every item is one piece
                 size = size > 1 ? size : 1;
                 mine = sum_of(size);
-                units = wave_total(mine);
+                upto = wave_scan(mine);
+                units = __builtin_amdgcn_readlane(upto, kWave - 1);
                 if (units <= a.groups)
                     break;
-                const int larger = (int)((int64_t)size * units / a.groups);
-                size = larger > size ? larger : size + 1;
+                size += (size + 7) / 8;
             }
+            if (w >= units)
+                return;
+        } else {
+            const uint32_t groups = units < a.groups ? units : a.groups;
+            if (w >= (int)groups)
+                return;
+            runs.each = units / groups;
+            runs.more = units - runs.each * groups;
+            from = first_tile(runs, w);
+            left = first_tile(runs, w + 1) - from;
         }
-        const int groups = units < a.groups ? units : a.groups;
-        if (w >= groups)
-            return;
-        runs.each = units / groups;
-        runs.more = units - runs.each * groups;
-        const int from = first_tile(runs, w);
-        left = first_tile(runs, w + 1) - from;
         // The lane whose share holds the run's first unit, then the item in it.
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const int v = __shfl_up(upto, d);
-            upto += lane >= d ? v : 0;
-        }
         const int in = __builtin_ctzll(__ballot(from < upto));
         int at = __builtin_amdgcn_readlane(upto - mine, in);
         b = in * each;
         chunk = 0;
         int count;
-        for (;;) {
-            if (b >= a.B)
-                return;  // not reached: the sums above found the unit
-            const Span s = span_of<kTile>(a, b, chunk * kColumns, kColumns);
-            if (chunk == a.chunks || chunk * kColumns >= s.n * G) {
-                chunk = 0;
-                ++b;
-                continue;
+        if (__builtin_expect(small, 1)) {
+            count = __builtin_amdgcn_readlane(lane_tiles, in);
+            here = (uint32_t)(count + size - 1) / (uint32_t)size;
+            run_begin = __builtin_amdgcn_readlane(lane_begin, in);
+            run_end = __builtin_amdgcn_readlane(lane_end, in);
+            run_len = __builtin_amdgcn_readlane(lane_len, in);
+        } else {
+            for (;;) {
+                if (b >= a.B)
+                    return;  // not reached: the sums above found the unit
+                const Span s = span_of<kTile>(a, b, chunk * kColumns, kColumns);
+                if (chunk == a.chunks || chunk * kColumns >= s.n * G) {
+                    chunk = 0;
+                    ++b;
+                    continue;
+                }
+                count = tiles_of(s);
+                here = (uint32_t)(count + size - 1) / (uint32_t)size;
+                if (from < at + here * a.Hkv)
+                    break;
+                at += here * a.Hkv;
+                ++chunk;
             }
-            count = tiles_of(s);
-            here = (count + size - 1) / size;
-            if (from < at + here * a.Hkv)
-                break;
-            at += here * a.Hkv;
-            ++chunk;
+            run_begin = a.row_starts[b];
+            run_end = a.row_starts[b + 1];
+            run_len = a.context_lens[b];
         }
-        h = (from - at) / here;
+        h = (uint32_t)(from - at) / (uint32_t)here;
         item_unit = at + h * here;
         tile = from - item_unit;
         if (a.pieces) {  // piece `tile` of `here` equal ones
-            const int q = count / here, more = count - q * here, piece = tile;
+            const int q = (uint32_t)count / (uint32_t)here, more = count - q * here, piece = tile;
             tile = first_tile(Runs{q, more}, piece);
             left = first_tile(Runs{q, more}, piece + 1) - tile;
         }
@@ -306,7 +352,7 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
 
     for (;; lds_barrier()) {  // the items of the run
     const int x0 = chunk * kColumns;
-    const Span span = span_of<kTile>(a, b, x0, kColumns);
+    const Span span = span_of<kTile>(a, run_begin, run_end, run_len, x0, kColumns);
     const int count = tiles_of(span);
     const int begin = tile, end = left < count - begin ? begin + left : count;
     if (!a.whole && begin == 0 && threadIdx.x == 0)  // who holds the pieces of the item that begins here
@@ -396,7 +442,7 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
     auto query_at = [&](int t, int q) {
         const int x = x0 + t * 16 + n;
         const bool live = x < span.n * G;
-        const int r = live ? x / G : 0, g = live ? x - r * G : 0;
+        const int r = live ? row_of_column(a, x) : 0, g = live ? x - r * G : 0;
         return static_cast<const T *>(a.q) + (span.start + r) * a.q_stride + (int64_t)(h * G + g) * D + q * 32 + c * 8;
     };
     x8 qf[kQueriesInLds ? 1 : NT][KS];
@@ -424,7 +470,7 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int x = x0 + t * 16 + n;
-        pos[t] = x < span.n * G ? span.first_pos + x / G : -1;
+        pos[t] = x < span.n * G ? span.first_pos + row_of_column(a, x) : -1;
     }
     if (threadIdx.x < NT * 16)
         col_max[threadIdx.x] = -__builtin_inff();
@@ -525,22 +571,33 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
         // values are cleared here and added back below for the rows that see them.
         uint32_t bad = 0;
         if (partial) {
+            typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+            u16x2 largest{0, 0};  // of the magnitudes' bits: an exponent of all ones is above every finite one
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                const int token = (i * kWave + lane) / U;
-                u32x4 v = vr[i];
-                const u32x4 zero{0u, 0u, 0u, 0u};
-                if (!(present >> token & 1u))
-                    v = zero;
-                const u32x4 f{finite_halves<T>(v.x), finite_halves<T>(v.y), finite_halves<T>(v.z),
-                              finite_halves<T>(v.w)};
-                const bool differs = f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w;
-                bad |= differs ? 1u << token : 0u;
-                vr[i] = f;
-            }
+                const bool there = present >> ((i * kWave + lane) / U) & 1u;
 #pragma unroll
-            for (int d = 1; d < kWave; d *= 2)
-                bad |= __shfl_xor(bad, d);
+                for (int k = 0; k < 4; ++k) {
+                    vr[i][k] = there ? vr[i][k] : 0u;
+                    largest = __builtin_elementwise_max(largest, __builtin_bit_cast(u16x2, vr[i][k] & 0x7FFF7FFFu));
+                }
+            }
+            if (__builtin_expect(__any(largest.x >= E::exponent || largest.y >= E::exponent), 0)) {
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    bool differs = false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t f = finite_halves<T>(vr[i][k]);
+                        differs |= f != vr[i][k];
+                        vr[i][k] = f;
+                    }
+                    bad |= differs ? 1u << (i * kWave + lane) / U : 0u;
+                }
+#pragma unroll
+                for (int d = 1; d < kWave; d *= 2)
+                    bad |= __shfl_xor(bad, d);
+            }
         }
         store(vr);
         if (lane < 16) {
@@ -588,7 +645,7 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
         if constexpr (kWaves == 8)
             any_bad |= bad_tokens[1];
         const uint32_t some = __builtin_amdgcn_readfirstlane(any_bad.x | any_bad.y | any_bad.z | any_bad.w);
-        for (int v = 0; some && v < kWaves; ++v) {
+        for (int v = 0; __builtin_expect(some != 0, 0) && v < kWaves; ++v) {
             uint32_t left = __builtin_amdgcn_readfirstlane(reinterpret_cast<const uint32_t *>(bad_tokens)[v]);
             while (left) {  // a token of a partly visible tile holds infinities or NaN
                 const int tok = 16 * v + __builtin_ctz(left);
@@ -639,7 +696,7 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
 #pragma unroll
         for (int v = 0; v < kWaves; ++v)
             total += col_sum[v][t * 16 + n];
-        const int r = x / G;
+        const int r = row_of_column(a, x);
         const int64_t at_row = (int64_t)(span.start + r) * a.Hq + h * G + (x - r * G);
         const bool first = wave == 0 && c == 0;
         if (begin == 0 && end == count) {
@@ -677,10 +734,13 @@ __global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const Attn
     if (++h == a.Hkv) {  // the next item that exists (there is one: the run is not done)
         h = 0;
         ++chunk;
-        while (chunk == a.chunks || chunk * kColumns >= span_of<kTile>(a, b, 0, kColumns).n * G) {
+        while (chunk == a.chunks || chunk * kColumns >= span_of<kTile>(a, run_begin, run_end, run_len, 0, kColumns).n * G) {
             chunk = 0;
             if (++b >= a.B)
                 return;
+            run_begin = a.row_starts[b];
+            run_end = a.row_starts[b + 1];
+            run_len = a.context_lens[b];
         }
     }
     }
@@ -698,7 +758,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
     const int P = blockDim.x / W;           // pieces read at a time
     __shared__ float4_t part[kJoinThreads / W][W];
     __shared__ float sums[kJoinThreads / W];
-    const int G = a.Hq / a.Hkv;
+    const int G = a.G;
     const int h = blockIdx.x % a.Hkv, k = blockIdx.x / a.Hkv % a.chunks, b = blockIdx.x / a.Hkv / a.chunks;
     const int x0 = k * columns;
     const int begin = a.row_starts[b], end = a.row_starts[b + 1];
@@ -710,7 +770,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
     const int pieces = join.y - join.x + 1;
     auto slot = [&](int z) { return (int64_t)slot_of(join.x + z, z == 0) * columns; };
     for (int col = blockIdx.y; col < live; col += gridDim.y) {
-        const int x = x0 + col, r = x / G;
+        const int x = x0 + col, r = row_of_column(a, x);
         const int64_t at_row = (int64_t)(begin + r) * a.Hq + h * G + (x - r * G);
         const float2_t *ml = reinterpret_cast<const float2_t *>(a.part_ml) + col;
         float top = -__builtin_inff();
@@ -852,6 +912,10 @@ hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf1
     a.whole = p.whole;
     a.pieces = p.pieces;
     a.one_page = a.page_size % 16 == 0;
+    a.G = a.Hq / a.Hkv;
+    const MagicDiv g = magic_div(a.G);
+    a.group_magic = g.magic;
+    a.group_shift = g.shift;
     if (!p.whole) {
         const size_t columns = (size_t)p.groups * 2 * 16 * p.col_tiles;
         a.joins = static_cast<int2 *>(workspace);

@@ -44,6 +44,8 @@ struct AttnArgs {
     float scale_log2;                         // scale * log2(e)
     uint64_t page_magic;                      // division by page_size (magic_div)
     int page_shift;
+    uint64_t group_magic;                     // division by G = Hq / Hkv
+    int group_shift, G;
     int chunks;                               // column chunks of one (sequence, kv head)
     int groups;                               // runs
     int whole, pieces;                        // how items are dealt out (qmm_attn.hip)
