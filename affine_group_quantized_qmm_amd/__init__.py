@@ -16,6 +16,7 @@ Tensors (all on one ROCm device, contiguous):
 from __future__ import annotations
 
 import ctypes
+import math
 from pathlib import Path
 
 import torch
@@ -122,7 +123,14 @@ def qmm_validate(x_ptr: int, wq_ptr: int, s_ptr: int, b_ptr: int, y_ptr: int, M:
                                  ws_bytes))
 
 
+# The current stream's handle without building a Stream object (0.1 us a call
+# instead of 2.2).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -402,28 +410,42 @@ _TYPE_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}  # QMM_F16
 _HALVES = (torch.float16, torch.bfloat16)
 
 
-def _check_rows(t: torch.Tensor, name: str, dtypes, shape, device) -> int:
-    """_check for a tensor whose rows may lie apart; returns the row stride."""
+def _need(t, name: str, dtype, shape, index: int) -> int:
+    """_check for the calls of a decode step, where a microsecond counts: one
+    pass over what has to hold (`index`: the GPU's), and _check itself only to
+    say what does not. Returns the address."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        _check(t, name, (dtype,), shape, torch.device("cuda", index) if index >= 0 else None)
+    return t.data_ptr()
+
+
+def _need_or_none(t, name: str, dtype, shape, index: int):
+    return None if t is None else _need(t, name, dtype, shape, index)
+
+
+def _need_rows(t, name: str, dtype, shape, index: int) -> int:
+    """_need for a tensor whose rows may lie apart; returns the row stride."""
     if t.is_contiguous():
-        _check(t, name, dtypes, shape, device)
-        stride = 1
-        for n in shape[1:]:
-            stride *= n
-        return stride
-    if t.dim() < 2 or t.shape[0] < 1 or not t[0].is_contiguous():
-        raise ValueError(f"{name} must be contiguous within a row")
-    _check(t[0], name, dtypes, shape[1:], device)
-    if t.shape[0] != shape[0]:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        _need(t, name, dtype, shape, index)
+        return math.prod(shape[1:])
+    if t.shape != shape or not t[0].is_contiguous():
+        raise ValueError(f"{name} must have shape {tuple(shape)}, contiguous within a row, got {tuple(t.shape)}")
+    _need(t[0], name, dtype, shape[1:], index)
     return t.stride(0)
 
 
-def _check_caches(k_cache, v_cache, device):
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+def _cache_shape(k_cache, v_cache, D: int, index: int):
+    """(num_pages, Hkv, page_size) of the caches, checked."""
+    if k_cache.dim() != 4:
         raise ValueError("the caches must be 4-D [num_pages, Hkv, page_size, D]")
-    _check(k_cache, "k_cache", _HALVES, k_cache.shape, device)
-    _check(v_cache, "v_cache", (k_cache.dtype,), k_cache.shape, device)
-    return k_cache.shape
+    shape = k_cache.shape
+    if k_cache.dtype not in _HALVES:
+        raise TypeError(f"the caches must be float16 or bfloat16, got {k_cache.dtype}")
+    if shape[3] != D:
+        raise ValueError(f"the caches' D is {shape[3]}, the queries' {D}")
+    _need(k_cache, "k_cache", k_cache.dtype, shape, index)
+    _need(v_cache, "v_cache", k_cache.dtype, shape, index)
+    return shape[0], shape[1], shape[2]
 
 
 def qmm_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, *, eps: float = 1e-6,
@@ -436,29 +458,24 @@ def qmm_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be 3-D [M, heads, D]")
     M, Hq, D = q.shape
-    dev = q.device
-    pages, Hkv, page_size, cache_D = _check_caches(k_cache, v_cache, dev)
-    if cache_D != D:
-        raise ValueError(f"the caches' D is {cache_D}, the queries' {D}")
-    qs = _check_rows(q, "q", tuple(_TYPE_CODES), (M, Hq, D), None)
-    ks = _check_rows(k, "k", (q.dtype,), (M, Hkv, D), dev)
-    vs = _check_rows(v, "v", (q.dtype,), (M, Hkv, D), dev)
-    _check(q_weight, "q_weight", (torch.float32,), (D,), dev)
-    _check(k_weight, "k_weight", (torch.float32,), (D,), dev)
-    _check(positions, "positions", (torch.int32,), (M,), dev)
-    _check(slots, "slots", (torch.int32,), (M,), dev)
-    R = 0
-    if inv_freq is not None:
-        R = 2 * inv_freq.numel()
-        _check(inv_freq, "inv_freq", (torch.float32,), (R // 2,), dev)
+    index, tin = q.get_device(), q.dtype
+    if tin not in _TYPE_CODES or index < 0:
+        raise ValueError(f"q must be float32, float16 or bfloat16 on the GPU, got {tin} on {q.device}")
+    pages, Hkv, page_size = _cache_shape(k_cache, v_cache, D, index)
+    tout = k_cache.dtype
+    qs = _need_rows(q, "q", tin, (M, Hq, D), index)
+    ks = _need_rows(k, "k", tin, (M, Hkv, D), index)
+    vs = _need_rows(v, "v", tin, (M, Hkv, D), index)
+    R = 2 * inv_freq.numel() if inv_freq is not None else 0
     if out is None:
-        out = torch.empty((M, Hq, D), dtype=k_cache.dtype, device=dev)
-    _check(out, "out", (k_cache.dtype,), (M, Hq, D), dev)
-    rc = _lib.qmm_qk_norm_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _TYPE_CODES[q.dtype],
-                               q_weight.data_ptr(), k_weight.data_ptr(), eps, weight_offset, positions.data_ptr(),
-                               inv_freq.data_ptr() if R else None, R, interleaved, slots.data_ptr(), out.data_ptr(),
-                               k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[k_cache.dtype], M, Hq, Hkv, D,
-                               pages, page_size, _stream(q))
+        out = torch.empty((M, Hq, D), dtype=tout, device=q.device)
+    rc = _lib.qmm_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _TYPE_CODES[tin],
+        _need(q_weight, "q_weight", torch.float32, (D,), index), _need(k_weight, "k_weight", torch.float32, (D,), index),
+        eps, weight_offset, _need(positions, "positions", torch.int32, (M,), index),
+        _need_or_none(inv_freq, "inv_freq", torch.float32, (R // 2,), index), R, interleaved,
+        _need(slots, "slots", torch.int32, (M,), index), _need(out, "out", tout, (M, Hq, D), index),
+        k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[tout], M, Hq, Hkv, D, pages, page_size, _stream(q))
     if rc:
         raise QmmError(rc, "qmm_qk_norm_rope")
     return out
@@ -483,29 +500,26 @@ def qmm_paged_attention(q, k_cache, v_cache, block_table, context_lens, row_star
         raise ValueError("q must be 3-D [T, Hq, D] and block_table 2-D [B, max_pages]")
     T, Hq, D = q.shape
     B, max_pages = block_table.shape
-    dev = q.device
-    pages, Hkv, page_size, cache_D = _check_caches(k_cache, v_cache, dev)
-    if cache_D != D:
-        raise ValueError(f"the caches' D is {cache_D}, the queries' {D}")
-    qs = _check_rows(q, "q", (k_cache.dtype,), (T, Hq, D), dev)
-    _check(block_table, "block_table", (torch.int32,), (B, max_pages), dev)
-    _check(context_lens, "context_lens", (torch.int32,), (B,), dev)
-    _check(row_starts, "row_starts", (torch.int32,), (B + 1,), dev)
+    index = q.get_device()
+    if index < 0:
+        raise ValueError(f"q must be on the GPU, got {q.device}")
+    pages, Hkv, page_size = _cache_shape(k_cache, v_cache, D, index)
+    dtype = k_cache.dtype
+    qs = _need_rows(q, "q", dtype, (T, Hq, D), index)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    _check(out, "out", (q.dtype,), (T, Hq, D), dev)
-    if lse is not None:
-        _check(lse, "lse", (torch.float32,), (T, Hq), dev)
+        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
     need = _lib.qmm_paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    rc = _lib.qmm_paged_attention(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[q.dtype],
-                                  block_table.data_ptr(), context_lens.data_ptr(), row_starts.data_ptr(),
-                                  out.data_ptr(), lse.data_ptr() if lse is not None else None, T, B, Hq, Hkv, D,
-                                  pages, page_size, max_pages, max_rows, max_context,
-                                  scale if scale is not None else D ** -0.5, window, sinks,
-                                  workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(q))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    rc = _lib.qmm_paged_attention(
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[dtype],
+        _need(block_table, "block_table", torch.int32, (B, max_pages), index),
+        _need(context_lens, "context_lens", torch.int32, (B,), index),
+        _need(row_starts, "row_starts", torch.int32, (B + 1,), index), _need(out, "out", dtype, (T, Hq, D), index),
+        _need_or_none(lse, "lse", torch.float32, (T, Hq), index), T, B, Hq, Hkv, D, pages, page_size, max_pages,
+        max_rows, max_context, scale if scale is not None else D ** -0.5, window, sinks,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(q))
     if rc:
         raise QmmError(rc, "qmm_paged_attention")
     return out
@@ -524,30 +538,23 @@ def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D [M, V]")
     M, V = logits.shape
-    dev = logits.device
-    stride = V
-    if logits.is_contiguous():
-        _check(logits, "logits", tuple(_TYPE_CODES), (M, V), None)
-    else:
-        if logits.dtype not in _TYPE_CODES or dev.type != "cuda" or logits.stride(1) != 1:
-            raise ValueError("logits must be a GPU tensor of float32, float16 or bfloat16, contiguous within a row")
-        stride = logits.stride(0)
-    for t, name, dtype in ((u, "u", torch.float32), (temperature, "temperature", torch.float32),
-                           (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
-                           (min_p, "min_p", torch.float32), (tokens, "tokens", torch.int32),
-                           (logprobs, "logprobs", torch.float32)):
-        if t is not None:
-            _check(t, name, (dtype,), (M,), dev)
+    index = logits.get_device()
+    if logits.dtype not in _TYPE_CODES or index < 0:
+        raise ValueError(f"logits must be float32, float16 or bfloat16 on the GPU, got {logits.dtype} on {logits.device}")
+    stride = _need_rows(logits, "logits", logits.dtype, (M, V), index)
     if tokens is None:
-        tokens = torch.empty(M, dtype=torch.int32, device=dev)
+        tokens = torch.empty(M, dtype=torch.int32, device=logits.device)
     if workspace is None:
-        workspace = torch.empty(_lib.qmm_sample_workspace_bytes(M, V), dtype=torch.uint8, device=dev)
-    rc = _lib.qmm_sample(logits.data_ptr(), stride, _TYPE_CODES[logits.dtype], u.data_ptr(),
-                         None if temperature is None else temperature.data_ptr(),
-                         None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
-                         None if min_p is None else min_p.data_ptr(), tokens.data_ptr(),
-                         None if logprobs is None else logprobs.data_ptr(), M, V, workspace.data_ptr(),
-                         workspace.numel() * workspace.element_size(), _stream(logits))
+        workspace = torch.empty(_lib.qmm_sample_workspace_bytes(M, V), dtype=torch.uint8, device=logits.device)
+    rows = (M,)
+    rc = _lib.qmm_sample(
+        logits.data_ptr(), stride, _TYPE_CODES[logits.dtype], _need(u, "u", torch.float32, rows, index),
+        _need_or_none(temperature, "temperature", torch.float32, rows, index),
+        _need_or_none(top_k, "top_k", torch.int32, rows, index),
+        _need_or_none(top_p, "top_p", torch.float32, rows, index),
+        _need_or_none(min_p, "min_p", torch.float32, rows, index), _need(tokens, "tokens", torch.int32, rows, index),
+        _need_or_none(logprobs, "logprobs", torch.float32, rows, index), M, V, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(logits))
     if rc:
         raise QmmError(rc, "qmm_sample")
     return tokens
