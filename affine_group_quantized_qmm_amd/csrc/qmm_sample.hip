@@ -18,8 +18,9 @@
 //   2. gather     Cumulative counts and masses over those bins (64-bit floats)
 //                 tell which bins each crossing can fall into; the elements
 //                 of those bins (tens to hundreds of a vocabulary) are listed.
-//   3. finish     Each crossing is resolved inside its bin by narrowing a key
-//                 range with 512-way histograms over the list.
+//   3. finish     Each crossing is resolved inside its bin: a histogram of 512
+//                 parts of the bin's width leaves a few elements (or equal
+//                 ones), which are ranked by comparing all pairs.
 //
 // Tokens have to be equal to what 64-bit arithmetic gives, whatever the order of
 // the sums: the weights' relative errors (below 2^-28, of either sign) shift a
@@ -50,10 +51,13 @@ constexpr float kUnit = 2147483648.0f;   // 2^31: the weight of a bin's centre
 constexpr int kMaxSlice = 1 << 17;   // elements of a slice: the packed number has 18 bits, the sum 45 and a sign
 constexpr int kMaxSlices = 64;
 constexpr int kSliceList = 1024;     // listed elements of a slice
-constexpr int kList = 4096;          // listed elements of a row
+constexpr int kList = 8192;          // listed elements of a row
+constexpr int kParts = kThreads;     // parts of a bin
+constexpr int kRanked = 1024;        // elements that are ranked by pairs
+constexpr int kWhole = 64;           // a bin of up to this many is ranked as it is
 constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it leaves the nearest integer in the low word
 
-// What a slice leaves behind.
+// What a slice leaves behind, and a row (cut into slices).
 struct SliceHead {
     float top;          // largest logit (-inf: none)
     uint32_t listed;    // elements of the gathered bins, before the cap
@@ -63,10 +67,23 @@ struct Entry {
     float x;
     uint32_t index;
 };
+struct RowSums {
+    double mass[kBins];      // mass of bins 0 .. t (bin 0 holds the maximum), e^z relative to bin 0's centre
+    uint32_t count[kBins];   // their elements
+    float top;               // the row's maximum
+    int fine;                // whether it is in the histogram's range
+    uint32_t pad[2];
+};
 __host__ __device__ constexpr size_t slice_bytes() { return sizeof(SliceHead) + kBins * 8 + kSliceList * sizeof(Entry); }
+__host__ __device__ constexpr size_t row_bytes(int S) { return sizeof(RowSums) + S * slice_bytes(); }
+static_assert(sizeof(RowSums) % 16 == 0 && slice_bytes() % 16 == 0, "aligned parts");
+__device__ __forceinline__ RowSums *sums_of(const SampleArgs &a, int row, int S)
+{
+    return reinterpret_cast<RowSums *>(static_cast<char *>(a.workspace) + row * row_bytes(S));
+}
 __device__ __forceinline__ char *slice_at(const SampleArgs &a, int row, int s, int S)
 {
-    return static_cast<char *>(a.workspace) + ((size_t)row * S + s) * slice_bytes();
+    return static_cast<char *>(a.workspace) + row * row_bytes(S) + sizeof(RowSums) + s * slice_bytes();
 }
 __device__ __forceinline__ SliceHead *head_of(char *p) { return reinterpret_cast<SliceHead *>(p); }
 __device__ __forceinline__ uint64_t *hist_of(char *p) { return reinterpret_cast<uint64_t *>(p + sizeof(SliceHead)); }
@@ -115,10 +132,12 @@ __device__ __forceinline__ double scaled(float x, double per_unit, float ref)
         return (double)x * per_unit;
 }
 
-// Bin and weight (2^31 (1 + q)) of a scaled logit within the range.
+// Bin and weight (2^31 (1 + q)) of a scaled logit within the range, and the part
+// of the bin (0: its upper end) that it lies in.
 struct Binned {
     int bin;
     int q;
+    int part;
 };
 __device__ __forceinline__ Binned binned(double d)
 {
@@ -127,6 +146,8 @@ __device__ __forceinline__ Binned binned(double d)
     Binned b;
     b.bin = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
     const float r = (float)(d - (t - kMagic));  // -1/2 .. 1/2, in bins
+    b.part = (int)((0.5f - r) * (float)kParts);  // exact but for the cut
+    b.part = b.part < kParts ? b.part : kParts - 1;
     // 2^31 (e^(r/8) - 1) by its series: the first term left out is below 2^-33 of the weight
     constexpr float c1 = kUnit / 8.f, c2 = c1 / 16.f, c3 = c2 / 24.f, c4 = c3 / 32.f, c5 = c4 / 40.f;
     b.q = (int)(r * __builtin_fmaf(r, __builtin_fmaf(r, __builtin_fmaf(r, __builtin_fmaf(r, c5, c4), c3), c2), c1));
@@ -159,6 +180,23 @@ __device__ __forceinline__ float key_value(uint32_t k)
 template <typename T>
 __device__ __forceinline__ float to_float(T v) { return (float)v; }
 
+// Elements [begin, end) of a row (which need not be aligned): single ones up
+// to `body`, whole units of 16 bytes, single ones from `tail`.
+struct Span {
+    int body, units, tail;
+};
+template <typename T>
+__device__ __forceinline__ Span span_of_row(const T *row, int begin, int end, int size)
+{
+    const int E = 16 / size;
+    const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(row + begin) & 15u)) & 15u) / size;
+    Span s;
+    s.body = begin + (lead < end - begin ? lead : end - begin);
+    s.units = (end - s.body) / E;
+    s.tail = s.body + s.units * E;
+    return s;
+}
+
 // Calls f(x, index) for the elements [begin, end) of a row, `threads` threads
 // together: 16 bytes a load where a unit of 16 bytes lies inside, one by one
 // at the ends (rows need not be aligned).
@@ -167,11 +205,8 @@ __device__ __forceinline__ void for_elements(const T *row, int begin, int end, i
 {
     constexpr int E = 16 / sizeof(T);
     typedef T vec __attribute__((ext_vector_type(E)));
-    const T *first = row + begin;
-    const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(first) & 15u)) & 15u) / (int)sizeof(T);
-    const int body = begin + (lead < end - begin ? lead : end - begin);
-    const int units = (end - body) / E;
-    const int tail = body + units * E;
+    const Span s = span_of_row(row, begin, end, (int)sizeof(T));
+    const int body = s.body, units = s.units, tail = s.tail;
     if ((int)threadIdx.x < body - begin)
         f(to_float(row[begin + threadIdx.x]), begin + (int)threadIdx.x);
     if ((int)threadIdx.x < end - tail)
@@ -251,22 +286,20 @@ __global__ __launch_bounds__(kScanThreads) void sample_histogram_kernel(const Sa
 }
 
 // ---------------------------------------------------------------------------
-// Cumulative counts and masses over a row's bins, in LDS.
+// Cumulative counts and masses over a row's bins.
 // ---------------------------------------------------------------------------
-struct Cumulative {
-    uint32_t count[kBins];   // elements of bins 0 .. t (bin 0 holds the maximum)
-    double mass[kBins];      // their mass, e^z relative to bin 0's centre
-    float top;               // the row's maximum
-    uint32_t wave_count[kScanThreads / kWave];
-    double wave_mass[kScanThreads / kWave];
-};
 
 // Weight of bin t's centre relative to bin 0's, over the weights' unit.
 __device__ __forceinline__ double bin_factor(int t) { return exp(-(double)t / kPerUnit) * 0x1p-31; }
 
 // Inclusive sums over the workgroup's threads, in thread order.
 template <typename M>
-__device__ __forceinline__ void block_sums(uint32_t &c, M &m, uint32_t *wave_c, M *wave_m, int waves)
+struct WaveSums {
+    M mass[kScanThreads / kWave];
+    uint32_t count[kScanThreads / kWave];
+};
+template <int THREADS, typename M>
+__device__ __forceinline__ void block_sums(uint32_t &c, M &m, WaveSums<M> &w)
 {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
 #pragma unroll
@@ -279,37 +312,38 @@ __device__ __forceinline__ void block_sums(uint32_t &c, M &m, uint32_t *wave_c, 
         }
     }
     if (lane == kWave - 1) {
-        wave_c[wave] = c;
-        wave_m[wave] = m;
+        w.count[wave] = c;
+        w.mass[wave] = m;
     }
     __syncthreads();
     uint32_t bc = 0;
     M bm = 0;
-    for (int w = 0; w < waves; ++w)
-        if (w < wave) {
-            bc += wave_c[w];
-            bm += wave_m[w];
-        }
+#pragma unroll
+    for (int v = 0; v < THREADS / kWave; ++v) {
+        bc += v < wave ? w.count[v] : 0;
+        bm += v < wave ? w.mass[v] : 0;
+    }
     c += bc;
     m += bm;
     __syncthreads();
 }
 
-__device__ __forceinline__ void store_cumulative(Cumulative &cum, uint32_t c, double m, int waves)
+template <int THREADS>
+__device__ __forceinline__ void store_sums(RowSums &sums, uint32_t c, double m, WaveSums<double> &w)
 {
-    block_sums(c, m, cum.wave_count, cum.wave_mass, waves);
+    block_sums<THREADS>(c, m, w);
     if (threadIdx.x < kBins) {
-        cum.count[threadIdx.x] = c;
-        cum.mass[threadIdx.x] = m;
+        sums.count[threadIdx.x] = c;
+        sums.mass[threadIdx.x] = m;
     }
     __syncthreads();
 }
 
 // Joins the slices' histograms. The order of the sums is fixed: every
-// workgroup of a row gets the same numbers. False: the row is out of range
-// (or has no logit above -inf); cum.top is set in any case.
-__device__ __forceinline__ bool join_slices(const SampleArgs &a, int row, int S, double per_unit, Cumulative &cum,
-                                            int waves)
+// workgroup of a row gets the same numbers.
+template <int THREADS>
+__device__ __forceinline__ void join_slices(const SampleArgs &a, int row, int S, double per_unit, RowSums &sums,
+                                            WaveSums<double> &w)
 {
     const int lane = threadIdx.x % kWave;
     float top = lane < S ? head_of(slice_at(a, row, lane, S))->top : -__builtin_inff();  // S <= 64
@@ -317,23 +351,25 @@ __device__ __forceinline__ bool join_slices(const SampleArgs &a, int row, int S,
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2)
         top = fmaxf(top, __shfl_xor(top, d));
-    if (threadIdx.x == 0)
-        cum.top = top;
     const bool fine = in_range(top, per_unit);  // false for -inf
+    if (threadIdx.x == 0) {
+        sums.top = top;
+        sums.fine = fine;
+    }
     uint32_t count = 0;
     int64_t sum = 0;
     if (fine) {
         const int bin = binned((double)top * per_unit).bin - (int)threadIdx.x;
-        for (int s0 = 0; s0 < S; s0 += 8) {  // eight loads in flight
-            uint64_t v[8];
+        for (int s0 = 0; s0 < S; s0 += 16) {  // sixteen loads in flight
+            uint64_t v[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 const int s = s0 + j, at = __shfl(own, s & (kWave - 1)) - bin;
                 v[j] = s < S && threadIdx.x < kBins && at >= 0 && at < kBins
                            ? hist_of(slice_at(a, row, s, S))[at] : 0;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 const int64_t q = (int64_t)(v[j] << (64 - kSumBits)) >> (64 - kSumBits);
                 sum += q;
                 count += (uint32_t)((v[j] - (uint64_t)q) >> kSumBits);
@@ -342,56 +378,52 @@ __device__ __forceinline__ bool join_slices(const SampleArgs &a, int row, int S,
     }
     const double mass = threadIdx.x < kBins
                             ? ((double)count * (double)kUnit + (double)sum) * bin_factor(threadIdx.x) : 0.0;
-    store_cumulative(cum, count, mass, waves);
-    return fine;
+    store_sums<THREADS>(sums, count, mass, w);
 }
 
-// First bin whose cumulative mass reaches (or with PAST passes) a value, the
-// last bin if none does; by binary search, the same in every thread.
-template <bool PAST>
-__device__ __forceinline__ int first_mass(const Cumulative &cum, double value)
-{
-    int lo = 0, hi = kBins - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        const bool there = PAST ? cum.mass[mid] > value : cum.mass[mid] >= value;
-        if (there)
-            hi = mid;
-        else
-            lo = mid + 1;
+// The sums in a wave's registers, where a search is a comparison and a count
+// of lanes for each 64 bins: the sums rise, so that the first bin to reach a
+// value is the number of bins that do not.
+struct Search {
+    double mass[kBins / kWave];
+    uint32_t count[kBins / kWave];
+    __device__ __forceinline__ explicit Search(const RowSums &s)
+    {
+#pragma unroll
+        for (int j = 0; j < kBins / kWave; ++j) {
+            mass[j] = s.mass[j * kWave + threadIdx.x % kWave];
+            count[j] = s.count[j * kWave + threadIdx.x % kWave];
+        }
     }
-    return lo;
-}
-// First bin with a cumulative count of at least k; kBins if none.
-__device__ __forceinline__ int first_count(const Cumulative &cum, uint32_t k)
-{
-    int lo = 0, hi = kBins;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (cum.count[mid] >= k)
-            hi = mid;
-        else
-            lo = mid + 1;
+    // First bin whose cumulative mass reaches (or with PAST passes) a value, the
+    // last bin if none does.
+    template <bool PAST>
+    __device__ __forceinline__ int first_mass(double value) const
+    {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kBins / kWave; ++j)
+            n += __popcll(__ballot(PAST ? mass[j] <= value : mass[j] < value));
+        return n < kBins ? n : kBins - 1;
     }
-    return lo;
-}
-__device__ __forceinline__ double mass_before(const Cumulative &cum, int t) { return t > 0 ? cum.mass[t - 1] : 0.0; }
+    // First bin with a cumulative count of at least k; kBins if none.
+    __device__ __forceinline__ int first_count(uint32_t k) const
+    {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kBins / kWave; ++j)
+            n += __popcll(__ballot(count[j] < k));
+        return n;
+    }
+};
+__device__ __forceinline__ double mass_before(const RowSums &s, int t) { return t > 0 ? s.mass[t - 1] : 0.0; }
+__device__ __forceinline__ uint32_t count_before(const RowSums &s, int t) { return t > 0 ? s.count[t - 1] : 0u; }
 
 // The bins whose elements decide. A crossing's value is only known to lie
 // between bounds until the crossing before it is resolved, so it brings a range
 // (widened by more than the roundings of the masses).
 struct Wanted {
     int k_bin, p_low, p_high, m_bin, r_low, r_high;
-    __device__ __forceinline__ bool has(int t) const
-    {
-        return t == k_bin || (t >= p_low && t <= p_high) || t == m_bin || (t >= r_low && t <= r_high);
-    }
-    __device__ __forceinline__ int last() const
-    {
-        int t = k_bin > p_high ? k_bin : p_high;
-        t = t > m_bin ? t : m_bin;
-        return t > r_high ? t : r_high;
-    }
 };
 // The bin of min-p's border, relative to the maximum's bin; -1: none.
 __device__ __forceinline__ int min_p_bin(const RowParams &p, double top_scaled)
@@ -402,56 +434,109 @@ __device__ __forceinline__ int min_p_bin(const RowParams &p, double top_scaled)
     const int t = binned(top_scaled).bin - binned(d).bin;
     return t < kBins ? t : -1;
 }
-__device__ __forceinline__ Wanted wanted_bins(const Cumulative &cum, const RowParams &p, double top_scaled)
+__device__ __forceinline__ Wanted wanted_bins(const RowSums &sums, const RowParams &p, double top_scaled)
 {
+    const Search find(sums);
     Wanted w;
-    double low = cum.mass[kBins - 1], high = low;
+    double low = sums.mass[kBins - 1], high = low;
     w.k_bin = -1;
     if (p.top_k > 0) {
-        const int t = first_count(cum, p.top_k);
+        const int t = find.first_count(p.top_k);
         if (t < kBins) {
             w.k_bin = t;
-            low = mass_before(cum, t);
-            high = cum.mass[t];
+            low = mass_before(sums, t);
+            high = sums.mass[t];
         }
     }
     w.p_low = 0;
     w.p_high = -1;
     if (p.top_p < 1.0) {
-        w.p_low = first_mass<false>(cum, p.top_p * low * (1.0 - 1e-12));
-        w.p_high = first_mass<false>(cum, p.top_p * high * (1.0 + 1e-12));
-        const double l = mass_before(cum, w.p_low), h = cum.mass[w.p_high];
+        w.p_low = find.first_mass<false>(p.top_p * low * (1.0 - 1e-12));
+        w.p_high = find.first_mass<false>(p.top_p * high * (1.0 + 1e-12));
+        const double l = mass_before(sums, w.p_low), h = sums.mass[w.p_high];
         low = l < low ? l : low;
         high = h < high ? h : high;
     }
     w.m_bin = min_p_bin(p, top_scaled);
     if (w.m_bin >= 0) {
-        const double l = mass_before(cum, w.m_bin), h = cum.mass[w.m_bin];
+        const double l = mass_before(sums, w.m_bin), h = sums.mass[w.m_bin];
         low = l < low ? l : low;
         high = h < high ? h : high;
     }
-    w.r_low = first_mass<true>(cum, p.u * low * (1.0 - 1e-12));
-    w.r_high = first_mass<true>(cum, p.u * high * (1.0 + 1e-12));
+    w.r_low = find.first_mass<true>(p.u * low * (1.0 - 1e-12));
+    w.r_high = find.first_mass<true>(p.u * high * (1.0 + 1e-12));
     return w;
 }
 
-// Elements of wanted bins are offered to take(x, index). Most logits lie below
-// the last wanted bin; one comparison with a bound that errs on the safe side
-// drops them.
-template <typename T, typename F>
-__device__ __forceinline__ void for_wanted(const T *row, int begin, int end, int threads, double per_unit,
-                                           double top_scaled, const Wanted &w, F take)
+// Lists the elements [begin, end) of a row that lie in wanted bins. Each of the
+// four kinds of crossing wants an interval of logits; its ends are moved
+// outwards by more than their roundings, and what they let in besides is told
+// apart by its bin later. Nearly every vector has no element in them.
+template <typename T>
+__device__ __forceinline__ void list_wanted(const T *row, int begin, int end, int threads, double per_unit,
+                                            double top_scaled, const Wanted &w, uint32_t *listed, Entry *list, int cap)
 {
     const int top_bin = binned(top_scaled).bin;
-    const double bound = (top_bin - w.last() - 1) / per_unit;
-    const float low = bound > -3e38 && bound < 3e38 ? (float)bound - fabsf((float)bound) * 1e-6f : -__builtin_inff();
-    for_elements<T, 4>(row, begin, end, threads, [&](float x, int index) {
-        if (x >= low) {
-            const double d = scaled<false>(x, per_unit, 0.f);
-            if (d > top_scaled - kBins - 1 && w.has(top_bin - binned(d).bin))
-                take(x, index);
+    float low[4], high[4];
+    const int first[4] = {w.k_bin, w.p_low, w.m_bin, w.r_low}, last[4] = {w.k_bin, w.p_high, w.m_bin, w.r_high};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        // bins of z: (top_bin - t - 1/2) .. (top_bin - t + 1/2); a quarter bin more is above every rounding here
+        const float l = (float)((top_bin - last[k] - 0.75) / per_unit), h = (float)((top_bin - first[k] + 0.75) / per_unit);
+        const bool none = last[k] < first[k] || last[k] < 0;
+        low[k] = none ? __builtin_inff() : l;
+        high[k] = none ? -__builtin_inff() : h;
+    }
+    auto hit = [&](float x) {
+        bool h = x >= low[0] && x <= high[0];
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+            h |= x >= low[k] && x <= high[k];
+        return h;
+    };
+    auto put = [&](float x, int index) {
+        const uint32_t at = atomicAdd(listed, 1u);
+        if (at < (uint32_t)cap)
+            list[at] = Entry{x, (uint32_t)index};
+    };
+    constexpr int E = 16 / sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(E)));
+    const Span s = span_of_row(row, begin, end, (int)sizeof(T));
+    if ((int)threadIdx.x < s.body - begin) {
+        const float x = (float)row[begin + threadIdx.x];
+        if (hit(x))
+            put(x, begin + (int)threadIdx.x);
+    }
+    if ((int)threadIdx.x < end - s.tail) {
+        const float x = (float)row[s.tail + threadIdx.x];
+        if (hit(x))
+            put(x, s.tail + (int)threadIdx.x);
+    }
+    const vec *p = reinterpret_cast<const vec *>(row + s.body);
+    constexpr int UNROLL = 4;
+    for (int i = threadIdx.x; i < s.units; i += UNROLL * threads) {
+        vec v[UNROLL];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j)
+            v[j] = p[i + j * threads < s.units ? i + j * threads : i];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                hits |= hit((float)v[j][e]) ? 1u << e : 0u;
+            hits = i + j * threads < s.units ? hits : 0u;
+            while (hits) {
+                const int e = __builtin_ctz(hits);
+                hits &= hits - 1;
+                float x = (float)v[j][0];
+#pragma unroll
+                for (int k = 1; k < E; ++k)
+                    x = k == e ? (float)v[j][k] : x;
+                put(x, s.body + (i + j * threads) * E + e);
+            }
         }
-    });
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -460,26 +545,29 @@ __device__ __forceinline__ void for_wanted(const T *row, int begin, int end, int
 template <typename T>
 __global__ __launch_bounds__(kScanThreads) void sample_gather_kernel(const SampleArgs a, int S)
 {
-    __shared__ Cumulative cum;
+    __shared__ RowSums sums;
+    __shared__ WaveSums<double> waves;
     __shared__ uint32_t listed;
     const int s = blockIdx.x, row = blockIdx.y;
     if (threadIdx.x == 0)
         listed = 0;
     const RowParams p = params_of(a, row);
-    if (!join_slices(a, row, S, p.per_unit, cum, kScanThreads / kWave))
+    join_slices<kScanThreads>(a, row, S, p.per_unit, sums, waves);
+    if (s == 0) {  // for the finish
+        const uint32_t *from = reinterpret_cast<const uint32_t *>(&sums);
+        uint32_t *to = reinterpret_cast<uint32_t *>(sums_of(a, row, S));
+        for (int i = threadIdx.x; i < (int)(sizeof(RowSums) / 4); i += kScanThreads)
+            to[i] = from[i];
+    }
+    if (!sums.fine)
         return;
-    const double top_scaled = (double)cum.top * p.per_unit;
-    const Wanted w = wanted_bins(cum, p, top_scaled);
+    const double top_scaled = (double)sums.top * p.per_unit;
+    const Wanted w = wanted_bins(sums, p, top_scaled);
     int begin, end;
     slice_of(a.V, S, s, begin, end);
     char *out = slice_at(a, row, s, S);
-    Entry *list = list_of(out);
-    for_wanted(static_cast<const T *>(a.logits) + row * a.row_stride, begin, end, kScanThreads, p.per_unit, top_scaled,
-               w, [&](float x, int index) {
-                   const uint32_t at = atomicAdd(&listed, 1u);
-                   if (at < kSliceList)
-                       list[at] = Entry{x, (uint32_t)index};
-               });
+    list_wanted(static_cast<const T *>(a.logits) + row * a.row_stride, begin, end, kScanThreads, p.per_unit, top_scaled,
+                w, &listed, list_of(out), kSliceList);
     __syncthreads();
     if (threadIdx.x == 0)
         head_of(out)->listed = listed;
@@ -488,51 +576,146 @@ __global__ __launch_bounds__(kScanThreads) void sample_gather_kernel(const Sampl
 // ---------------------------------------------------------------------------
 // 3. Finish: one workgroup a row.
 // ---------------------------------------------------------------------------
+struct Ranked {
+    uint32_t key, index, weight;
+};
 struct Finish {
-    Cumulative cum;
-    uint32_t bin_count[kThreads];
-    unsigned long long bin_sum[kThreads];
+    RowSums sums;
+    WaveSums<double> waves;
+    WaveSums<long long> part_waves;
+    uint32_t part_count[kParts];
+    unsigned long long part_sum[kParts];
     Entry list[kList];
-    uint32_t listed;
+    Ranked ranked[kRanked];
+    uint32_t listed, chosen;
     uint32_t low_key, high_key, number;      // of the current range
-    uint32_t found_bin, found_count, found_total;
+    uint32_t found, found_count, found_last;
     unsigned long long found_sum;
-    unsigned long long total_mass;
-    uint32_t token;
-    uint32_t wave_c[kThreads / kWave];
-    long long wave_m[kThreads / kWave];
+    uint32_t key, nth;                       // the crossing element's
+    unsigned long long mass;
 };
 
-// The elements that a search looks at: those of bin `t` of the row, from the
-// list, or from the row itself where the list could not hold them.
-template <typename T, bool REL>
-struct Source {
-    Finish &f;
-    const T *row;
-    int V;
-    bool rescan;
-    double per_unit, top_scaled;
-    float ref;
-    int top_bin;
+// The four searches: the k-th element, top-p's last, min-p's last, the token.
+enum Query { kTopK, kTopP, kMinP, kToken };
 
-    template <typename F>
-    __device__ __forceinline__ void of_bin(int t, F g) const
-    {
-        auto offer = [&](float x, uint32_t index) {
-            const double d = scaled<REL>(x, per_unit, ref);
-            if (d > top_scaled - kBins - 1) {
-                const Binned b = binned(d);
-                if (top_bin - b.bin == t)
-                    g(order_key(x), index, b.q, d);
-            }
-        };
-        if (rescan)
-            for_elements<T, 1>(row, 0, V, kThreads, [&](float x, int i) { offer(x, (uint32_t)i); });
-        else
-            for (uint32_t i = threadIdx.x; i < f.listed; i += kThreads)
-                offer(f.list[i].x, f.list[i].index);
+// Whether the elements up to one of weight w, before which there are `before`
+// elements of mass `from`, cross.
+__device__ __forceinline__ bool crosses(int query, uint32_t before, unsigned long long from, uint32_t number,
+                                        unsigned long long w, uint32_t count, double value)
+{
+    if (query == kTopK)
+        return before < count && before + number >= count;
+    const double lo = (double)from, hi = (double)(from + w);
+    return query == kTopP ? lo < value && hi >= value : lo <= value && hi > value;
+}
+
+// Where the listed elements of bin t, in order, cross a count or a mass (in
+// units of the weights): f.key, f.nth (its index) and f.mass (of the bin's
+// elements up to and with it). If they do not cross, the last element. False
+// (for all threads) if more elements than can be ranked share a part of the bin.
+__device__ __forceinline__ bool find_listed(Finish &f, int t, int top_bin, double per_unit, int query, uint32_t count,
+                                            double value, double top_scaled, double log_min_p)
+{
+    const uint32_t total = f.sums.count[t] - count_before(f.sums, t);
+    int part = -1;
+    uint32_t before = 0;
+    unsigned long long mass = 0;
+    // Each of a thread's elements of bin t, with its part and weight.
+    auto each = [&](auto g) {
+        for (uint32_t i = threadIdx.x; i < f.listed; i += kThreads) {
+            const Entry e = f.list[i];
+            const double d = scaled<false>(e.x, per_unit, 0.f);
+            const Binned b = binned(d);
+            if (d > top_scaled - kBins - 1 && top_bin - b.bin == t)  // not NaN either
+                g(e, b.part, (uint32_t)(2147483648u + (uint32_t)b.q), d);
+        }
+    };
+    if (threadIdx.x == 0) {
+        f.chosen = 0;
+        f.found = 0xFFFFFFFFu;
+        f.mass = 0;
     }
-};
+    if (query == kMinP) {  // the elements that pass the comparison
+        __syncthreads();
+        unsigned long long sum = 0;
+        each([&](const Entry &, int, uint32_t w, double d) {
+            sum += (d - top_scaled) / kPerUnit >= log_min_p ? w : 0u;
+        });
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2)
+            sum += __shfl_xor(sum, d);
+        if (threadIdx.x % kWave == 0 && sum)
+            atomicAdd(&f.mass, sum);
+        __syncthreads();
+        return true;
+    }
+    if (total > kWhole) {
+        f.part_count[threadIdx.x] = 0;
+        f.part_sum[threadIdx.x] = 0;
+        __syncthreads();
+        each([&](const Entry &, int part, uint32_t w, double) {
+            atomicAdd(&f.part_count[part], 1u);
+            atomicAdd(&f.part_sum[part], (unsigned long long)w);
+        });
+        __syncthreads();
+        const uint32_t mine = f.part_count[threadIdx.x];
+        const long long my_mass = (long long)f.part_sum[threadIdx.x];
+        uint32_t c = mine;
+        long long m = my_mass;
+        block_sums<kThreads>(c, m, f.part_waves);
+        if (mine && crosses(query, c - mine, (unsigned long long)(m - my_mass), mine, (unsigned long long)my_mass, count,
+                            value))
+            f.found = threadIdx.x;
+        if (mine && c == total)
+            f.found_last = threadIdx.x;
+        __syncthreads();
+        part = (int)(f.found != 0xFFFFFFFFu ? f.found : f.found_last);
+        if ((int)threadIdx.x == part) {
+            f.found_count = c - mine;
+            f.found_sum = (unsigned long long)(m - my_mass);
+            f.number = mine;
+        }
+        __syncthreads();
+        before = f.found_count;
+        mass = f.found_sum;
+        if (f.number > kRanked)
+            return false;
+    }
+    __syncthreads();
+    each([&](const Entry &e, int p, uint32_t w, double) {
+        if (part < 0 || p == part)
+            f.ranked[atomicAdd(&f.chosen, 1u)] = Ranked{order_key(e.x), e.index, w};
+    });
+    __syncthreads();
+    const uint32_t n = f.chosen;
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+        const Ranked mine = f.ranked[i];
+        // greater in this number: earlier in the order
+        const uint64_t place = (uint64_t)mine.key << 32 | (uint32_t)~mine.index;
+        uint32_t c = before;
+        unsigned long long from = mass;
+#pragma unroll 4
+        for (uint32_t j = 0; j < n; ++j) {
+            const Ranked e = f.ranked[j];
+            const bool earlier = ((uint64_t)e.key << 32 | (uint32_t)~e.index) > place;
+            c += earlier ? 1u : 0u;
+            from += earlier ? e.weight : 0u;
+        }
+        const bool last = c + 1 == before + n;
+        const bool here = crosses(query, c, from, 1, mine.weight, count, value);
+        // not crossed: the last element (its sum is below the value, or the count)
+        const bool none = last && (query == kTopK   ? c + 1 < count
+                                   : query == kTopP ? (double)(from + mine.weight) < value
+                                                    : (double)(from + mine.weight) <= value);
+        if (here || none) {
+            f.key = mine.key;
+            f.nth = mine.index;
+            f.mass = from + mine.weight;
+        }
+    }
+    __syncthreads();
+    return true;
+}
 
 // Smallest and largest value and number of the elements that pass.
 template <typename Each>
@@ -568,97 +751,95 @@ __device__ __forceinline__ void range_of(Finish &f, Each each)
 __device__ __forceinline__ int shift_for(uint32_t range)
 {
     int s = 0;
-    while ((range >> s) >= (uint32_t)kThreads)
+    while ((range >> s) >= (uint32_t)kParts)
         ++s;
     return s;
 }
 
-enum class Cross { count, reach, pass };  // count >= c, mass >= value, mass > value
-
-struct Found {
-    uint32_t key;            // the crossing element's
-    uint32_t nth;            // which of the elements with this key (1, 2, ...)
-    uint32_t equal;          // how many there are
-    unsigned long long mass; // of the bin's elements up to and with it
-};
-
-// Where the elements of bin t, in order, cross a count or a mass (in units of
-// the weights). If they do not, the last element.
-template <typename S>
-__device__ __forceinline__ Found find_in_bin(Finish &f, const S &src, int t, Cross kind, uint32_t count, double value)
+// The same searches over the row itself, for lists that overflow and rows out of
+// the histogram's range: a range of values is narrowed 512-fold a turn, by keys
+// for the crossing and then by indexes among equal keys. With `indexes` the
+// values are the indexes of the elements whose key is f.key and the crossing is
+// the count'th; else they are keys, and f.key, f.nth (which of the equal ones, 1,
+// 2, ...) and f.mass are set.
+template <typename T, bool REL>
+__device__ __forceinline__ void narrow(Finish &f, const T *row, int V, int t, int top_bin, double per_unit, float ref,
+                                       double top_scaled, bool indexes, int query, uint32_t count, double value)
 {
+    const uint32_t key = f.key;
     uint32_t low = 0, high = 0xFFFFFFFFu, before = 0;
     unsigned long long mass = 0;
-    // A value that rounding took to the bin's edge still crosses at the first
-    // element (every weight is far above 1/2).
-    const double least = kind == Cross::reach ? 0.5 : 0.0;
-    value = value > least ? value : least;
-    for (;;) {  // every turn narrows [low, high] by a factor of 512 or ends
-        range_of(f, [&](auto add) {
-            src.of_bin(t, [&](uint32_t key, uint32_t, int, double) {
-                if (key >= low && key <= high)
-                    add(key);
-            });
+    // Values to find stand in falling order for keys, in rising order for indexes.
+    auto each = [&](auto g) {
+        for_elements<T, 1>(row, 0, V, kThreads, [&](float x, int i) {
+            const double d = scaled<REL>(x, per_unit, ref);
+            if (d > top_scaled - kBins - 1) {
+                const Binned b = binned(d);
+                const uint32_t k = order_key(x), v = indexes ? ~(uint32_t)i : k;
+                if (top_bin - b.bin == t && (!indexes || k == key) && v >= low && v <= high)
+                    g(v, b.q);
+            }
         });
+    };
+    for (;;) {  // every turn narrows [low, high] by a factor of 512 or ends
+        range_of(f, [&](auto add) { each([&](uint32_t v, int) { add(v); }); });
         low = f.low_key;
         high = f.high_key;
         const uint32_t number = f.number;
         __syncthreads();
         if (number == 0 || low == high) {
-            const double d = scaled<S::kRel>(key_value(low), src.per_unit, src.ref);
-            const unsigned long long w = (unsigned long long)(2147483648LL + binned(d).q);
-            uint32_t j = number;
-            if (kind == Cross::count) {
-                j = count - before;
-            } else {
-                const double left = (value - (double)mass) / (double)w;
-                const double n = kind == Cross::reach ? ceil(left) : floor(left) + 1.0;
-                j = n < 1.0 ? 1u : n < (double)number ? (uint32_t)n : number;
+            if (threadIdx.x == 0) {
+                if (indexes) {
+                    f.nth = ~low;
+                } else {
+                    const double d = scaled<REL>(key_value(low), per_unit, ref);
+                    const unsigned long long w = (unsigned long long)(2147483648LL + binned(d).q);
+                    uint32_t j = number;
+                    if (query == kTopK) {
+                        j = count - before;
+                    } else {
+                        const double left = (value - (double)mass) / (double)w;
+                        const double n = query == kTopP ? ceil(left) : floor(left) + 1.0;
+                        j = n < 1.0 ? 1u : n < (double)number ? (uint32_t)n : number;
+                    }
+                    j = j < 1 ? 1 : j > number ? number : j;
+                    f.key = low;
+                    f.nth = j;
+                    f.mass = mass + j * w;
+                }
             }
-            j = j < 1 ? 1 : j > number ? number : j;
-            return Found{low, j, number, mass + j * w};
+            __syncthreads();
+            return;
         }
-        // 512 parts of the range, the highest keys first
         const int shift = shift_for(high - low);
-        f.bin_count[threadIdx.x] = 0;
-        f.bin_sum[threadIdx.x] = 0;
+        f.part_count[threadIdx.x] = 0;
+        f.part_sum[threadIdx.x] = 0;
         if (threadIdx.x == 0)
-            f.found_bin = 0xFFFFFFFFu;
+            f.found = 0xFFFFFFFFu;
         __syncthreads();
-        src.of_bin(t, [&](uint32_t key, uint32_t, int q, double) {
-            if (key >= low && key <= high) {
-                const uint32_t part = (high - key) >> shift;
-                atomicAdd(&f.bin_count[part], 1u);
-                atomicAdd(&f.bin_sum[part], (unsigned long long)(2147483648LL + q));
-            }
+        each([&](uint32_t v, int q) {
+            const uint32_t part = (high - v) >> shift;
+            atomicAdd(&f.part_count[part], 1u);
+            atomicAdd(&f.part_sum[part], (unsigned long long)(2147483648LL + q));
         });
         __syncthreads();
-        const uint32_t mine = f.bin_count[threadIdx.x];
-        const long long my_sum = (long long)f.bin_sum[threadIdx.x];
+        const uint32_t mine = f.part_count[threadIdx.x];
+        const long long my_mass = (long long)f.part_sum[threadIdx.x];
         uint32_t c = mine;
-        long long m = my_sum;
-        block_sums(c, m, f.wave_c, f.wave_m, kThreads / kWave);
-        const unsigned long long upto = mass + (unsigned long long)m, from = upto - (unsigned long long)my_sum;
-        bool here;
-        if (kind == Cross::count)
-            here = before + c >= count && before + c - mine < count;
-        else if (kind == Cross::reach)
-            here = (double)upto >= value && (double)from < value;
-        else
-            here = (double)upto > value && (double)from <= value;
-        if (mine && here) {
-            f.found_bin = threadIdx.x;
+        long long m = my_mass;
+        block_sums<kThreads>(c, m, f.part_waves);
+        if (mine && crosses(indexes ? (int)kTopK : query, before + c - mine, mass + (unsigned long long)(m - my_mass), mine,
+                            (unsigned long long)my_mass, count, value))
+            f.found = threadIdx.x;
+        if (mine && c == number)
+            f.found_last = threadIdx.x;
+        __syncthreads();
+        const uint32_t part = f.found != 0xFFFFFFFFu ? f.found : f.found_last;
+        if (threadIdx.x == part) {
             f.found_count = before + c - mine;
-            f.found_sum = from;
+            f.found_sum = mass + (unsigned long long)(m - my_mass);
         }
         __syncthreads();
-        if (f.found_bin == 0xFFFFFFFFu && mine && c == number) {  // not crossed (uniform): the last part
-            f.found_count = before + c - mine;
-            f.found_sum = from;
-            f.found_total = threadIdx.x;
-        }
-        __syncthreads();
-        const uint32_t part = f.found_bin != 0xFFFFFFFFu ? f.found_bin : f.found_total;
         before = f.found_count;
         mass = f.found_sum;
         const uint32_t top = high - (part << shift);
@@ -669,112 +850,36 @@ __device__ __forceinline__ Found find_in_bin(Finish &f, const S &src, int t, Cro
     }
 }
 
-// The index of the nth (from 1, by rising index) element of bin t with this key.
-template <typename S>
-__device__ __forceinline__ uint32_t nth_index(Finish &f, const S &src, int t, uint32_t key, uint32_t nth)
-{
-    uint32_t low = 0, high = 0xFFFFFFFFu, before = 0;
-    for (;;) {
-        range_of(f, [&](auto add) {
-            src.of_bin(t, [&](uint32_t k, uint32_t index, int, double) {
-                if (k == key && index >= low && index <= high)
-                    add(index);
-            });
-        });
-        low = f.low_key;
-        high = f.high_key;
-        const uint32_t number = f.number;
-        __syncthreads();
-        if (number == 0 || low == high)
-            return low;
-        const int shift = shift_for(high - low);
-        f.bin_count[threadIdx.x] = 0;
-        if (threadIdx.x == 0)
-            f.found_bin = 0;
-        __syncthreads();
-        src.of_bin(t, [&](uint32_t k, uint32_t index, int, double) {
-            if (k == key && index >= low && index <= high)
-                atomicAdd(&f.bin_count[(index - low) >> shift], 1u);
-        });
-        __syncthreads();
-        const uint32_t mine = f.bin_count[threadIdx.x];
-        uint32_t c = mine;
-        long long none = 0;
-        block_sums(c, none, f.wave_c, f.wave_m, kThreads / kWave);
-        if (mine && before + c >= nth && before + c - mine < nth) {
-            f.found_bin = threadIdx.x;
-            f.found_count = before + c - mine;
-        }
-        __syncthreads();
-        before = f.found_count;
-        const uint32_t from = low + (f.found_bin << shift);
-        const uint32_t width = (1u << shift) - 1;
-        high = high - from > width ? from + width : high;
-        low = from;
-        __syncthreads();
-    }
-}
-
 template <typename T, bool REL>
-struct RowSource : Source<T, REL> {
-    static constexpr bool kRel = REL;
-};
-
-// The searches, in the order of the filters.
-template <typename T, bool REL>
-__device__ __forceinline__ void finish_row(const SampleArgs &a, int row, const RowParams &p, Finish &f, const RowSource<T, REL> &src)
+__device__ __forceinline__ void find_in_row(Finish &f, const T *row, int V, int t, int top_bin, double per_unit,
+                                            float ref, double top_scaled, int query, uint32_t count, double value,
+                                            double log_min_p)
 {
-    const Cumulative &cum = f.cum;
-    double kept = cum.mass[kBins - 1];
-    const double all = kept;
-    double limit = all;  // mass of the top-k prefix
-    if (p.top_k > 0) {
-        const int t = first_count(cum, p.top_k);
-        if (t < kBins) {
-            const Found e = find_in_bin(f, src, t, Cross::count, p.top_k - (t > 0 ? cum.count[t - 1] : 0), 0.0);
-            limit = kept = mass_before(cum, t) + (double)e.mass * bin_factor(t);
-        }
-    }
-    if (p.top_p < 1.0) {
-        const double target = p.top_p * limit;
-        const int t = first_mass<false>(cum, target);
-        const Found e = find_in_bin(f, src, t, Cross::reach, 0, (target - mass_before(cum, t)) / bin_factor(t));
-        const double m = mass_before(cum, t) + (double)e.mass * bin_factor(t);
-        kept = m < kept ? m : kept;
-    }
-    const int mt = min_p_bin(p, src.top_scaled);
-    if (mt >= 0) {
+    if (query == kMinP) {
         if (threadIdx.x == 0)
-            f.total_mass = 0;
+            f.mass = 0;
         __syncthreads();
         unsigned long long sum = 0;
-        src.of_bin(mt, [&](uint32_t, uint32_t, int q, double d) {
-            if ((d - src.top_scaled) / kPerUnit >= p.log_min_p)
-                sum += (unsigned long long)(2147483648LL + q);
+        for_elements<T, 1>(row, 0, V, kThreads, [&](float x, int) {
+            const double d = scaled<REL>(x, per_unit, ref);
+            if (d > top_scaled - kBins - 1) {
+                const Binned b = binned(d);
+                if (top_bin - b.bin == t && (d - top_scaled) / kPerUnit >= log_min_p)
+                    sum += (unsigned long long)(2147483648LL + b.q);
+            }
         });
 #pragma unroll
         for (int d = 1; d < kWave; d *= 2)
             sum += __shfl_xor(sum, d);
         if (threadIdx.x % kWave == 0 && sum)
-            atomicAdd(&f.total_mass, sum);
+            atomicAdd(&f.mass, sum);
         __syncthreads();
-        const double m = mass_before(cum, mt) + (double)f.total_mass * bin_factor(mt);
-        kept = m < kept ? m : kept;
-        __syncthreads();
+        return;
     }
-    const double r = p.u * kept;
-    const int t = first_mass<true>(cum, r);
-    const Found e = find_in_bin(f, src, t, Cross::pass, 0, (r - mass_before(cum, t)) / bin_factor(t));
-    const uint32_t index = nth_index(f, src, t, e.key, e.nth);
-    if (threadIdx.x == 0) {
-        a.tokens[row] = (int32_t)index;
-        if (a.logprobs) {
-            // the weight as the sums hold it, so that a token kept alone has share 1
-            const int q = binned(scaled<REL>(key_value(e.key), src.per_unit, src.ref)).q;
-            const double lp = log((double)(2147483648LL + q) * bin_factor(t) / kept);
-            a.logprobs[row] = lp < 0.0 ? (float)lp : 0.f;
-        }
-    }
+    // First the key, then for the token the index among equal keys.
+    for (int pass = 0; pass < (query == kToken ? 2 : 1); ++pass)
+        narrow<T, REL>(f, row, V, t, top_bin, per_unit, ref, top_scaled, pass == 1, query, pass == 1 ? f.nth : count,
+                       value);
 }
 
 template <typename T>
@@ -783,11 +888,19 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
     __shared__ Finish f;
     const int row = blockIdx.x;
     const RowParams p = params_of(a, row);
+    const T *x = static_cast<const T *>(a.logits) + row * a.row_stride;
     if (threadIdx.x == 0)
         f.listed = 0;
-    const bool fine = join_slices(a, row, S, p.per_unit, f.cum, kThreads / kWave);
-    const float top = f.cum.top;
-    const T *x = static_cast<const T *>(a.logits) + row * a.row_stride;
+    if (S == 1) {
+        join_slices<kThreads>(a, row, S, p.per_unit, f.sums, f.waves);
+    } else {
+        const uint32_t *from = reinterpret_cast<const uint32_t *>(sums_of(a, row, S));
+        uint32_t *to = reinterpret_cast<uint32_t *>(&f.sums);
+        for (int i = threadIdx.x; i < (int)(sizeof(RowSums) / 4); i += kThreads)
+            to[i] = from[i];
+        __syncthreads();
+    }
+    const float top = f.sums.top;
     if (top == -__builtin_inff()) {  // no logit above -inf
         if (threadIdx.x == 0) {
             a.tokens[row] = -1;
@@ -796,63 +909,131 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
         }
         return;
     }
-    if (fine) {
-        RowSource<T, false> src{{f, x, a.V, false, p.per_unit, (double)top * p.per_unit, 0.f, 0}};
-        src.top_bin = binned(src.top_scaled).bin;
-        if (S == 1) {
-            const Wanted w = wanted_bins(f.cum, p, src.top_scaled);
-            for_wanted(x, 0, a.V, kThreads, p.per_unit, src.top_scaled, w, [&](float v, int index) {
-                const uint32_t at = atomicAdd(&f.listed, 1u);
-                if (at < kList)
-                    f.list[at] = Entry{v, (uint32_t)index};
-            });
-            __syncthreads();
-            src.rescan = f.listed > kList;
-        } else {
-            const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-            const uint32_t own = lane < S ? head_of(slice_at(a, row, lane, S))->listed : 0;
-            uint32_t upto = own;
-            bool over = own > kSliceList;
+    const bool fine = f.sums.fine;
+    const double top_scaled = fine ? (double)top * p.per_unit : 0.0;
+    const int top_bin = binned(top_scaled).bin;
+    // Elements of the wanted bins: of all searches at once, from the gather or
+    // (one slice) listed below; where these are too many, of one search at a time.
+    Wanted w{-1, 0, -1, -1, 0, -1};
+    bool listed = fine, list_now = false, one_by_one = false;
+    if (fine && S == 1) {
+        w = wanted_bins(f.sums, p, top_scaled);
+        list_now = true;
+    } else if (fine) {
+        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+        const uint32_t own = lane < S ? head_of(slice_at(a, row, lane, S))->listed : 0;
+        uint32_t upto = own;
 #pragma unroll
-            for (int d = 1; d < kWave; d *= 2) {
-                const uint32_t v = __shfl_up(upto, d);
-                upto += lane >= d ? v : 0;
-            }
-            const uint32_t total = __shfl(upto, kWave - 1);
-            src.rescan = __any(over) || total > kList;
-            if (!src.rescan)
-                for (int s = wave; s < S; s += kThreads / kWave) {
-                    const uint32_t n = __shfl(own, s), to = __shfl(upto, s) - n;
-                    const Entry *list = list_of(slice_at(a, row, s, S));
-                    for (uint32_t i = lane; i < n; i += kWave)
-                        f.list[to + i] = list[i];
-                }
-            if (threadIdx.x == 0)
-                f.listed = total;
-            __syncthreads();
+        for (int d = 1; d < kWave; d *= 2) {
+            const uint32_t v = __shfl_up(upto, d);
+            upto += lane >= d ? v : 0;
         }
-        finish_row<T, false>(a, row, p, f, src);
+        const uint32_t total = __shfl(upto, kWave - 1);
+        one_by_one = __any(own > kSliceList) || total > kList;
+        if (!one_by_one)
+            for (int s = wave; s < S; s += kThreads / kWave) {
+                const uint32_t n = __shfl(own, s), to = __shfl(upto, s) - n;
+                const Entry *list = list_of(slice_at(a, row, s, S));
+                for (uint32_t i = lane; i < n; i += kWave)
+                    f.list[to + i] = list[i];
+            }
+        if (threadIdx.x == 0)
+            f.listed = total;
+        __syncthreads();
     } else {
         // Counted again, relative to the maximum.
-        RowSource<T, true> src{{f, x, a.V, true, p.per_unit, 0.0, top, 0}};
-        f.bin_count[threadIdx.x] = 0;
-        f.bin_sum[threadIdx.x] = 0;
+        f.part_count[threadIdx.x] = 0;
+        f.part_sum[threadIdx.x] = 0;
         __syncthreads();
         for_elements<T, 1>(x, 0, a.V, kThreads, [&](float v, int) {
             const double d = scaled<true>(v, p.per_unit, top);
             if (d > -(kBins - 1)) {
                 const Binned b = binned(d);
-                atomicAdd(&f.bin_count[-b.bin & (kThreads - 1)], 1u);
-                atomicAdd(&f.bin_sum[-b.bin & (kThreads - 1)], (unsigned long long)(long long)b.q);
+                atomicAdd(&f.part_count[-b.bin & (kParts - 1)], 1u);
+                atomicAdd(&f.part_sum[-b.bin & (kParts - 1)], (unsigned long long)(long long)b.q);
             }
         });
         __syncthreads();
         const int t = threadIdx.x;
-        const uint32_t c = t < kBins ? f.bin_count[t] : 0;
-        const double m = t < kBins ? ((double)c * (double)kUnit + (double)(long long)f.bin_sum[t]) * bin_factor(t) : 0.0;
+        const uint32_t c = t < kBins ? f.part_count[t] : 0;
+        const double m =
+            t < kBins ? ((double)c * (double)kUnit + (double)(long long)f.part_sum[t]) * bin_factor(t) : 0.0;
         __syncthreads();
-        store_cumulative(f.cum, c, m, kThreads / kWave);
-        finish_row<T, true>(a, row, p, f, src);
+        store_sums<kThreads>(f.sums, c, m, f.waves);
+    }
+
+    // The searches, in the order of the filters.
+    const Search find(f.sums);
+    double kept = f.sums.mass[kBins - 1], limit = kept;  // mass kept so far; of the top-k prefix
+    int t = 0;
+    for (int query = kTopK; query <= kToken; ++query) {
+        uint32_t count = 0;
+        double value = 0.0;
+        if (query == kTopK) {
+            t = p.top_k > 0 ? find.first_count(p.top_k) : kBins;
+            if (t == kBins)
+                continue;
+            count = p.top_k - count_before(f.sums, t);
+        } else if (query == kMinP) {
+            t = min_p_bin(p, top_scaled);
+            if (t < 0)
+                continue;
+        } else {
+            if (query == kTopP && !(p.top_p < 1.0))
+                continue;
+            const double target = query == kTopP ? p.top_p * limit : p.u * kept;
+            t = query == kTopP ? find.first_mass<false>(target) : find.first_mass<true>(target);
+            // A value that rounding took to the bin's edge still crosses at the
+            // first element (every weight is far above 1/2).
+            value = (target - mass_before(f.sums, t)) / bin_factor(t);
+            const double least = query == kTopP ? 0.5 : 0.0;
+            value = value > least ? value : least;
+        }
+        for (bool again = true; again;) {
+            again = false;
+            if (one_by_one) {
+                w = Wanted{t, 0, -1, -1, 0, -1};
+                list_now = true;
+            }
+            if (list_now) {
+                if (threadIdx.x == 0)
+                    f.listed = 0;
+                __syncthreads();
+                list_wanted(x, 0, a.V, kThreads, p.per_unit, top_scaled, w, &f.listed, f.list, kList);
+                __syncthreads();
+                listed = f.listed <= kList;
+                again = !listed && !one_by_one;
+                one_by_one |= !listed;
+                list_now = false;
+                __syncthreads();
+            }
+        }
+        bool done = false;
+        if (listed)
+            done = find_listed(f, t, top_bin, p.per_unit, query, count, value, top_scaled, p.log_min_p);
+        if (__builtin_expect(!done, 0)) {
+            if (fine)
+                find_in_row<T, false>(f, x, a.V, t, top_bin, p.per_unit, 0.f, top_scaled, query, count, value, p.log_min_p);
+            else
+                find_in_row<T, true>(f, x, a.V, t, top_bin, p.per_unit, top, top_scaled, query, count, value, p.log_min_p);
+        }
+        if (query != kToken) {
+            const double m = mass_before(f.sums, t) + (double)f.mass * bin_factor(t);
+            kept = m < kept ? m : kept;
+            if (query == kTopK)
+                limit = kept;
+            __syncthreads();
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.tokens[row] = (int32_t)f.nth;
+        if (a.logprobs) {
+            // the weight as the sums hold it, so that a token kept alone has share 1
+            const float v = key_value(f.key);
+            const int q = binned(fine ? scaled<false>(v, p.per_unit, 0.f) : scaled<true>(v, p.per_unit, top)).q;
+            const double lp = log((double)(2147483648LL + q) * bin_factor(t) / kept);
+            a.logprobs[row] = lp < 0.0 ? (float)lp : 0.f;
+        }
     }
 }
 
@@ -888,7 +1069,7 @@ hipError_t launch(const SampleArgs &a, hipStream_t stream)
 
 bool sample_size_supported(int V) { return V >= 1 && V <= kMaxSlice * kMaxSlices; }
 
-size_t sample_workspace_bytes(int M, int V) { return (size_t)M * slices_of(M, V) * slice_bytes(); }
+size_t sample_workspace_bytes(int M, int V) { return (size_t)M * row_bytes(slices_of(M, V)); }
 
 hipError_t launch_sample(const SampleArgs &a, int type, hipStream_t stream)
 {
