@@ -41,10 +41,11 @@
 namespace qmm {
 namespace {
 
-constexpr int kScanThreads = 1024;   // histogram and gather
-constexpr int kThreads = 512;        // finish
+constexpr int kScanThreads = 1024;   // histogram; finish of rows of one slice, which it scans too
+constexpr int kThreads = 512;        // gather; finish of rows cut into slices
 constexpr int kRange = 8192;         // bins of the histogram: z of -512 .. 512
 constexpr int kBins = 384;           // bins that count, from the maximum's down
+constexpr int kSlots = 512;          // of a slice's histogram: bin b lies in slot b mod 512
 constexpr double kPerUnit = 8.0;     // bins per unit of z
 constexpr int kSumBits = 46;         // low field of a packed bin: the sum of q
 constexpr float kUnit = 2147483648.0f;   // 2^31: the weight of a bin's centre
@@ -52,7 +53,7 @@ constexpr int kMaxSlice = 1 << 17;   // elements of a slice: the packed number h
 constexpr int kMaxSlices = 64;
 constexpr int kSliceList = 1024;     // listed elements of a slice
 constexpr int kList = 8192;          // listed elements of a row
-constexpr int kParts = kThreads;     // parts of a bin
+constexpr int kParts = 512;          // parts of a bin
 constexpr int kRanked = 1024;        // elements that are ranked by pairs
 constexpr int kWhole = 64;           // a bin of up to this many is ranked as it is
 constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it leaves the nearest integer in the low word
@@ -74,7 +75,7 @@ struct RowSums {
     int fine;                // whether it is in the histogram's range
     uint32_t pad[2];
 };
-__host__ __device__ constexpr size_t slice_bytes() { return sizeof(SliceHead) + kBins * 8 + kSliceList * sizeof(Entry); }
+__host__ __device__ constexpr size_t slice_bytes() { return sizeof(SliceHead) + kSlots * 8 + kSliceList * sizeof(Entry); }
 __host__ __device__ constexpr size_t row_bytes(int S) { return sizeof(RowSums) + S * slice_bytes(); }
 static_assert(sizeof(RowSums) % 16 == 0 && slice_bytes() % 16 == 0, "aligned parts");
 __device__ __forceinline__ RowSums *sums_of(const SampleArgs &a, int row, int S)
@@ -89,7 +90,7 @@ __device__ __forceinline__ SliceHead *head_of(char *p) { return reinterpret_cast
 __device__ __forceinline__ uint64_t *hist_of(char *p) { return reinterpret_cast<uint64_t *>(p + sizeof(SliceHead)); }
 __device__ __forceinline__ Entry *list_of(char *p)
 {
-    return reinterpret_cast<Entry *>(p + sizeof(SliceHead) + kBins * 8);
+    return reinterpret_cast<Entry *>(p + sizeof(SliceHead) + kSlots * 8);
 }
 
 // A row's parameters. T <= 0 (or NaN) asks for the largest logit: the first
@@ -280,8 +281,8 @@ __global__ __launch_bounds__(kScanThreads) void sample_histogram_kernel(const Sa
     if (threadIdx.x == 0)
         head_of(out)->top = top;
     if (threadIdx.x < kBins && has_bin(top, per_unit)) {
-        const int b = binned((double)top * per_unit).bin + kRange / 2 - (int)threadIdx.x;
-        hist_of(out)[threadIdx.x] = b >= 0 ? bins[b] : 0;
+        const int b = binned((double)top * per_unit).bin - (int)threadIdx.x, at = b + kRange / 2;
+        hist_of(out)[b & (kSlots - 1)] = at >= 0 ? bins[at] : 0;
     }
 }
 
@@ -289,8 +290,23 @@ __global__ __launch_bounds__(kScanThreads) void sample_histogram_kernel(const Sa
 // Cumulative counts and masses over a row's bins.
 // ---------------------------------------------------------------------------
 
-// Weight of bin t's centre relative to bin 0's, over the weights' unit.
-__device__ __forceinline__ double bin_factor(int t) { return exp(-(double)t / kPerUnit) * 0x1p-31; }
+// Weight of bin t's centre relative to bin 0's, over the weights' unit:
+// e^(-t/8) 2^-31 as powers of e^(-1/8) (a load is shorter than the code of an
+// exponential that every launch would have to fetch first).
+struct Factors {
+    double of[kBins];
+    constexpr Factors() : of()
+    {
+        constexpr double sixteenth[4] = {1.0, 0.88249690258459540286, 0.77880078307140486825, 0.68728927879097219855};
+        double half = 0x1p-31;  // e^(-t/2) for t in steps of 4 bins
+        for (int t = 0; t < kBins; t += 4) {
+            for (int j = 0; j < 4; ++j)
+                of[t + j] = half * sixteenth[j];
+            half *= 0.60653065971263342360;
+        }
+    }
+};
+__device__ const Factors factors{};
 
 // Inclusive sums over the workgroup's threads, in thread order.
 template <typename M>
@@ -298,31 +314,62 @@ struct WaveSums {
     M mass[kScanThreads / kWave];
     uint32_t count[kScanThreads / kWave];
 };
+// A 32- or 64-bit value moved between lanes by a DPP control, 0 where no lane gives one.
+template <int CTRL, typename V>
+__device__ __forceinline__ V moved(V v)
+{
+    if constexpr (sizeof(V) == 4) {
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+    } else {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xF, 0xF, true);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    }
+}
+template <typename V>
+__device__ __forceinline__ V of_lane(V v, int lane)
+{
+    if constexpr (sizeof(V) == 4) {
+        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+    } else {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+        const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    }
+}
+// Inclusive sums over a wave's lanes: shifts within rows of 16, then the rows before.
+template <typename V>
+__device__ __forceinline__ V wave_sums(V v)
+{
+    v += moved<0x111>(v);  // row_shr:1
+    v += moved<0x112>(v);
+    v += moved<0x114>(v);
+    v += moved<0x118>(v);
+    const V r0 = of_lane(v, 15), r1 = of_lane(v, 31), r2 = of_lane(v, 47);
+    const int row = threadIdx.x % kWave / 16;
+    const V before = row == 0 ? (V)0 : row == 1 ? r0 : row == 2 ? r0 + r1 : r0 + r1 + r2;
+    return v + before;
+}
 template <int THREADS, typename M>
 __device__ __forceinline__ void block_sums(uint32_t &c, M &m, WaveSums<M> &w)
 {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t pc = __shfl_up(c, d);
-        const M pm = __shfl_up(m, d);
-        if (lane >= d) {
-            c += pc;
-            m += pm;
-        }
-    }
+    c = wave_sums(c);
+    m = wave_sums(m);
     if (lane == kWave - 1) {
         w.count[wave] = c;
         w.mass[wave] = m;
     }
     __syncthreads();
-    uint32_t bc = 0;
-    M bm = 0;
-#pragma unroll
-    for (int v = 0; v < THREADS / kWave; ++v) {
-        bc += v < wave ? w.count[v] : 0;
-        bm += v < wave ? w.mass[v] : 0;
-    }
+    // the waves before: their sums, in lanes
+    constexpr int WAVES = THREADS / kWave;
+    const uint32_t wc = wave_sums(lane < WAVES ? w.count[lane % WAVES] : 0u);
+    const M wm = wave_sums(lane < WAVES ? w.mass[lane % WAVES] : (M)0);
+    const int before = __builtin_amdgcn_readfirstlane(wave) - 1;
+    const uint32_t bc = before >= 0 ? of_lane(wc, before) : 0u;
+    const M bm = before >= 0 ? of_lane(wm, before) : (M)0;
     c += bc;
     m += bm;
     __syncthreads();
@@ -339,14 +386,36 @@ __device__ __forceinline__ void store_sums(RowSums &sums, uint32_t c, double m, 
     __syncthreads();
 }
 
-// Joins the slices' histograms. The order of the sums is fixed: every
-// workgroup of a row gets the same numbers.
-template <int THREADS>
-__device__ __forceinline__ void join_slices(const SampleArgs &a, int row, int S, double per_unit, RowSums &sums,
-                                            WaveSums<double> &w)
+// Joins the slices' histograms, of THREADS / 512 groups of threads each a share
+// of them. Everything is loaded at once: which bin a slot holds follows from
+// its slice's maximum, and whether the row wants it is seen afterwards. The
+// sums are of integers (and the scan's order is fixed): every workgroup of a
+// row gets the same numbers.
+struct Joined {
+    uint32_t count[kSlots];
+    int64_t sum[kSlots];
+};
+__device__ __forceinline__ void unpack(uint64_t v, uint32_t &count, int64_t &sum)
 {
-    const int lane = threadIdx.x % kWave;
+    const int64_t q = (int64_t)(v << (64 - kSumBits)) >> (64 - kSumBits);
+    sum += q;
+    count += (uint32_t)((v - (uint64_t)q) >> kSumBits);
+}
+template <int THREADS, int AT_ONCE>
+__device__ __forceinline__ void join_slices(const SampleArgs &a, int row, int S, double per_unit, RowSums &sums,
+                                            WaveSums<double> &w, Joined &joined)
+{
+    constexpr int GROUPS = THREADS / kSlots;
+    const int lane = threadIdx.x % kWave, slot = threadIdx.x % kSlots;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kSlots);
+    const double factor = threadIdx.x < kBins ? factors.of[threadIdx.x] : 0.0;
     float top = lane < S ? head_of(slice_at(a, row, lane, S))->top : -__builtin_inff();  // S <= 64
+    uint64_t v[AT_ONCE];
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+        const int s = group + j * GROUPS;
+        v[j] = s < S ? hist_of(slice_at(a, row, s, S))[slot] : 0;
+    }
     const int own = has_bin(top, per_unit) ? binned((double)top * per_unit).bin : -(1 << 30);
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2)
@@ -356,28 +425,51 @@ __device__ __forceinline__ void join_slices(const SampleArgs &a, int row, int S,
         sums.top = top;
         sums.fine = fine;
     }
+    const int top_bin = binned(fine ? (double)top * per_unit : 0.0).bin;
+    const int t = (top_bin - slot) & (kSlots - 1);  // the slot's bin, from the maximum's down
     uint32_t count = 0;
     int64_t sum = 0;
-    if (fine) {
-        const int bin = binned((double)top * per_unit).bin - (int)threadIdx.x;
-        for (int s0 = 0; s0 < S; s0 += 16) {  // sixteen loads in flight
-            uint64_t v[16];
+    uint64_t packed = 0;
+    // Up to this many elements fit the packed fields of one bin.
+    const bool together = a.V <= 250000;
+    for (int s0 = 0; fine && s0 < S; s0 += AT_ONCE * GROUPS) {
+        if (s0 > 0) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int s = s0 + j, at = __shfl(own, s & (kWave - 1)) - bin;
-                v[j] = s < S && threadIdx.x < kBins && at >= 0 && at < kBins
-                           ? hist_of(slice_at(a, row, s, S))[at] : 0;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int64_t q = (int64_t)(v[j] << (64 - kSumBits)) >> (64 - kSumBits);
-                sum += q;
-                count += (uint32_t)((v[j] - (uint64_t)q) >> kSumBits);
+            for (int j = 0; j < AT_ONCE; ++j) {
+                const int s = s0 + group + j * GROUPS;
+                v[j] = s < S ? hist_of(slice_at(a, row, s, S))[slot] : 0;
             }
         }
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) {
+            const int s = s0 + group + j * GROUPS;
+            // the slice's maximum's bin down to this one
+            const int below = __builtin_amdgcn_readlane(own, s & (kWave - 1)) - (top_bin - t);
+            v[j] = s < S && (uint32_t)below < (uint32_t)kBins ? v[j] : 0;
+            packed += v[j];
+        }
+        if (!together) {
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j)
+                unpack(v[j], count, sum);
+        }
     }
-    const double mass = threadIdx.x < kBins
-                            ? ((double)count * (double)kUnit + (double)sum) * bin_factor(threadIdx.x) : 0.0;
+    if (together)
+        unpack(packed, count, sum);
+    if (group == 0) {
+        joined.count[t] = count;
+        joined.sum[t] = sum;
+    }
+    __syncthreads();
+    if constexpr (GROUPS == 2) {
+        if (group == 1) {
+            joined.count[t] += count;
+            joined.sum[t] += sum;
+        }
+        __syncthreads();
+    }
+    count = threadIdx.x < kBins ? joined.count[threadIdx.x] : 0;
+    const double mass = threadIdx.x < kBins ? ((double)count * (double)kUnit + (double)joined.sum[threadIdx.x]) * factor : 0.0;
     store_sums<THREADS>(sums, count, mass, w);
 }
 
@@ -468,74 +560,143 @@ __device__ __forceinline__ Wanted wanted_bins(const RowSums &sums, const RowPara
     return w;
 }
 
-// Lists the elements [begin, end) of a row that lie in wanted bins. Each of the
-// four kinds of crossing wants an interval of logits; its ends are moved
-// outwards by more than their roundings, and what they let in besides is told
-// apart by its bin later. Nearly every vector has no element in them.
-template <typename T>
-__device__ __forceinline__ void list_wanted(const T *row, int begin, int end, int threads, double per_unit,
-                                            double top_scaled, const Wanted &w, uint32_t *listed, Entry *list, int cap)
-{
-    const int top_bin = binned(top_scaled).bin;
+// Intervals of logits that hold the wanted bins. Their ends are moved outwards
+// by more than their roundings; what they let in besides is told apart by its
+// bin later. Overlapping ones are one.
+struct Intervals {
     float low[4], high[4];
+    int number;
+};
+__device__ __forceinline__ Intervals intervals_of(const Wanted &w, double per_unit, int top_bin)
+{
+    const double unit = 1.0 / per_unit;
+    Intervals v;
+    v.number = 0;
     const int first[4] = {w.k_bin, w.p_low, w.m_bin, w.r_low}, last[4] = {w.k_bin, w.p_high, w.m_bin, w.r_high};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        // bins of z: (top_bin - t - 1/2) .. (top_bin - t + 1/2); a quarter bin more is above every rounding here
-        const float l = (float)((top_bin - last[k] - 0.75) / per_unit), h = (float)((top_bin - first[k] + 0.75) / per_unit);
-        const bool none = last[k] < first[k] || last[k] < 0;
-        low[k] = none ? __builtin_inff() : l;
-        high[k] = none ? -__builtin_inff() : h;
+        v.low[k] = __builtin_inff();
+        v.high[k] = -__builtin_inff();
     }
-    auto hit = [&](float x) {
-        bool h = x >= low[0] && x <= high[0];
 #pragma unroll
-        for (int k = 1; k < 4; ++k)
-            h |= x >= low[k] && x <= high[k];
+    for (int k = 0; k < 4; ++k) {
+        if (last[k] < first[k] || last[k] < 0)
+            continue;
+        // bin t: z of (top_bin - t - 1/2) / 8 .. (top_bin - t + 1/2) / 8
+        float l = (float)((top_bin - last[k] - 0.75) * unit), h = (float)((top_bin - first[k] + 0.75) * unit);
+#pragma unroll
+        for (int j = 0; j < k; ++j)
+            if (v.low[j] <= h && l <= v.high[j]) {  // takes j over
+                l = v.low[j] < l ? v.low[j] : l;
+                h = v.high[j] > h ? v.high[j] : h;
+                v.low[j] = __builtin_inff();
+                v.high[j] = -__builtin_inff();
+            }
+        v.low[k] = l;
+        v.high[k] = h;
+    }
+    // The ones that are left, in front; behind them infinity alone, which no
+    // row has whose bins are used.
+    float low[4], high[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        low[k] = high[k] = __builtin_inff();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (!(v.low[k] <= v.high[k]))
+            continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j == v.number) {
+                low[j] = v.low[k];
+                high[j] = v.high[k];
+            }
+        ++v.number;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v.low[k] = low[k];
+        v.high[k] = high[k];
+    }
+    return v;
+}
+
+// Writes the places of the elements [begin, end) of a row that lie in one of N
+// intervals to `places` (up to cap of them; *listed counts all). 32 elements
+// (16 in fp32) give a lane one word of hits and one place to write to.
+template <int N, typename T>
+__device__ __forceinline__ void list_places(const T *row, int begin, int end, int threads, const Intervals &v,
+                                            uint32_t *listed, uint32_t *places, int cap)
+{
+    auto hit = [&](float x) {
+        // the middle of x and an interval's ends is x inside it (and not for NaN)
+        bool h = __builtin_amdgcn_fmed3f(x, v.low[0], v.high[0]) == x;
+#pragma unroll
+        for (int k = 1; k < N; ++k)
+            h |= __builtin_amdgcn_fmed3f(x, v.low[k], v.high[k]) == x;
         return h;
     };
-    auto put = [&](float x, int index) {
-        const uint32_t at = atomicAdd(listed, 1u);
+    auto put = [&](uint32_t at, int place) {
         if (at < (uint32_t)cap)
-            list[at] = Entry{x, (uint32_t)index};
+            places[at] = (uint32_t)place;
     };
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = 16 / sizeof(T), UNROLL = 4;
     typedef T vec __attribute__((ext_vector_type(E)));
     const Span s = span_of_row(row, begin, end, (int)sizeof(T));
-    if ((int)threadIdx.x < s.body - begin) {
-        const float x = (float)row[begin + threadIdx.x];
-        if (hit(x))
-            put(x, begin + (int)threadIdx.x);
-    }
-    if ((int)threadIdx.x < end - s.tail) {
-        const float x = (float)row[s.tail + threadIdx.x];
-        if (hit(x))
-            put(x, s.tail + (int)threadIdx.x);
-    }
+    const int single = (int)threadIdx.x < s.body - begin ? begin + (int)threadIdx.x : -1;
+    if (single >= 0 && hit((float)row[single]))
+        put(atomicAdd(listed, 1u), single);
+    if ((int)threadIdx.x < end - s.tail && hit((float)row[s.tail + threadIdx.x]))
+        put(atomicAdd(listed, 1u), s.tail + (int)threadIdx.x);
     const vec *p = reinterpret_cast<const vec *>(row + s.body);
-    constexpr int UNROLL = 4;
-    for (int i = threadIdx.x; i < s.units; i += UNROLL * threads) {
-        vec v[UNROLL];
+    const int first = threadIdx.x & ~(kWave - 1);  // whole waves: the places are taken together
+    for (int i0 = first; i0 < s.units; i0 += UNROLL * threads) {
+        const int i = i0 + (int)threadIdx.x % kWave;
+        vec x[UNROLL];
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j)
-            v[j] = p[i + j * threads < s.units ? i + j * threads : i];
+            x[j] = p[i + j * threads < s.units ? i + j * threads : i0];
+        uint32_t hits = 0;  // bit E j + e
 #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) {
-            uint32_t hits = 0;
+        for (int j = UNROLL - 1; j >= 0; --j) {
+            uint32_t h = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                hits |= hit((float)v[j][e]) ? 1u << e : 0u;
-            hits = i + j * threads < s.units ? hits : 0u;
+            for (int e = E - 1; e >= 0; --e)
+                h = h + h + (hit((float)x[j][e]) ? 1u : 0u);
+            hits = hits << E | (i + j * threads < s.units ? h : 0u);
+        }
+        if (__any(hits != 0)) {
+            // One lane takes places for the whole wave (the same address from
+            // 64 lanes would be served one by one).
+            const uint32_t mine = __popc(hits), upto = wave_sums(mine), all = of_lane(upto, kWave - 1);
+            uint32_t from = 0;
+            if (threadIdx.x % kWave == 0)
+                from = atomicAdd(listed, all);
+            uint32_t at = of_lane(from, 0) + upto - mine;
             while (hits) {
-                const int e = __builtin_ctz(hits);
+                const int bit = __builtin_ctz(hits);
                 hits &= hits - 1;
-                float x = (float)v[j][0];
-#pragma unroll
-                for (int k = 1; k < E; ++k)
-                    x = k == e ? (float)v[j][k] : x;
-                put(x, s.body + (i + j * threads) * E + e);
+                put(at++, s.body + (i + bit / E * threads) * E + bit % E);
             }
         }
+    }
+}
+
+// Lists the elements [begin, end) that lie in wanted bins, and a few others.
+template <typename T>
+__device__ __forceinline__ void list_wanted(const T *row, int begin, int end, int threads, double per_unit, int top_bin,
+                                            const Wanted &w, uint32_t *listed, uint32_t *places, int cap, Entry *list)
+{
+    const Intervals v = intervals_of(w, per_unit, top_bin);
+    if (v.number <= 2)
+        list_places<2>(row, begin, end, threads, v, listed, places, cap);
+    else
+        list_places<4>(row, begin, end, threads, v, listed, places, cap);
+    __syncthreads();
+    const int n = *listed < (uint32_t)cap ? (int)*listed : cap;
+    for (int i = threadIdx.x; i < n; i += threads) {
+        const uint32_t place = places[i];
+        list[i] = Entry{(float)row[place], place};
     }
 }
 
@@ -543,20 +704,21 @@ __device__ __forceinline__ void list_wanted(const T *row, int begin, int end, in
 // 2. Gather of one slice (rows cut into several).
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ __launch_bounds__(kScanThreads) void sample_gather_kernel(const SampleArgs a, int S)
+__global__ __launch_bounds__(kThreads) void sample_gather_kernel(const SampleArgs a, int S)
 {
     __shared__ RowSums sums;
     __shared__ WaveSums<double> waves;
-    __shared__ uint32_t listed;
+    __shared__ Joined joined;
+    __shared__ uint32_t listed, places[kSliceList];
     const int s = blockIdx.x, row = blockIdx.y;
     if (threadIdx.x == 0)
         listed = 0;
     const RowParams p = params_of(a, row);
-    join_slices<kScanThreads>(a, row, S, p.per_unit, sums, waves);
+    join_slices<kThreads, 32>(a, row, S, p.per_unit, sums, waves, joined);
     if (s == 0) {  // for the finish
         const uint32_t *from = reinterpret_cast<const uint32_t *>(&sums);
         uint32_t *to = reinterpret_cast<uint32_t *>(sums_of(a, row, S));
-        for (int i = threadIdx.x; i < (int)(sizeof(RowSums) / 4); i += kScanThreads)
+        for (int i = threadIdx.x; i < (int)(sizeof(RowSums) / 4); i += kThreads)
             to[i] = from[i];
     }
     if (!sums.fine)
@@ -566,9 +728,8 @@ __global__ __launch_bounds__(kScanThreads) void sample_gather_kernel(const Sampl
     int begin, end;
     slice_of(a.V, S, s, begin, end);
     char *out = slice_at(a, row, s, S);
-    list_wanted(static_cast<const T *>(a.logits) + row * a.row_stride, begin, end, kScanThreads, p.per_unit, top_scaled,
-                w, &listed, list_of(out), kSliceList);
-    __syncthreads();
+    list_wanted(static_cast<const T *>(a.logits) + row * a.row_stride, begin, end, kThreads, p.per_unit,
+                binned(top_scaled).bin, w, &listed, places, kSliceList, list_of(out));
     if (threadIdx.x == 0)
         head_of(out)->listed = listed;
 }
@@ -579,6 +740,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_gather_kernel(const Sampl
 struct Ranked {
     uint32_t key, index, weight;
 };
+template <int THREADS>
 struct Finish {
     RowSums sums;
     WaveSums<double> waves;
@@ -586,7 +748,12 @@ struct Finish {
     uint32_t part_count[kParts];
     unsigned long long part_sum[kParts];
     Entry list[kList];
-    Ranked ranked[kRanked];
+    union {
+        Ranked ranked[kRanked];
+        uint32_t places[kList];
+        Joined joined;
+    };
+    double factor[kBins];
     uint32_t listed, chosen;
     uint32_t low_key, high_key, number;      // of the current range
     uint32_t found, found_count, found_last;
@@ -613,7 +780,8 @@ __device__ __forceinline__ bool crosses(int query, uint32_t before, unsigned lon
 // units of the weights): f.key, f.nth (its index) and f.mass (of the bin's
 // elements up to and with it). If they do not cross, the last element. False
 // (for all threads) if more elements than can be ranked share a part of the bin.
-__device__ __forceinline__ bool find_listed(Finish &f, int t, int top_bin, double per_unit, int query, uint32_t count,
+template <int THREADS>
+__device__ __forceinline__ bool find_listed(Finish<THREADS> &f, int t, int top_bin, double per_unit, int query, uint32_t count,
                                             double value, double top_scaled, double log_min_p)
 {
     const uint32_t total = f.sums.count[t] - count_before(f.sums, t);
@@ -622,7 +790,7 @@ __device__ __forceinline__ bool find_listed(Finish &f, int t, int top_bin, doubl
     unsigned long long mass = 0;
     // Each of a thread's elements of bin t, with its part and weight.
     auto each = [&](auto g) {
-        for (uint32_t i = threadIdx.x; i < f.listed; i += kThreads) {
+        for (uint32_t i = threadIdx.x; i < f.listed; i += THREADS) {
             const Entry e = f.list[i];
             const double d = scaled<false>(e.x, per_unit, 0.f);
             const Binned b = binned(d);
@@ -650,19 +818,21 @@ __device__ __forceinline__ bool find_listed(Finish &f, int t, int top_bin, doubl
         return true;
     }
     if (total > kWhole) {
-        f.part_count[threadIdx.x] = 0;
-        f.part_sum[threadIdx.x] = 0;
+        if (threadIdx.x < kParts) {
+            f.part_count[threadIdx.x] = 0;
+            f.part_sum[threadIdx.x] = 0;
+        }
         __syncthreads();
         each([&](const Entry &, int part, uint32_t w, double) {
             atomicAdd(&f.part_count[part], 1u);
             atomicAdd(&f.part_sum[part], (unsigned long long)w);
         });
         __syncthreads();
-        const uint32_t mine = f.part_count[threadIdx.x];
-        const long long my_mass = (long long)f.part_sum[threadIdx.x];
+        const uint32_t mine = threadIdx.x < kParts ? f.part_count[threadIdx.x] : 0;
+        const long long my_mass = threadIdx.x < kParts ? (long long)f.part_sum[threadIdx.x] : 0;
         uint32_t c = mine;
         long long m = my_mass;
-        block_sums<kThreads>(c, m, f.part_waves);
+        block_sums<THREADS>(c, m, f.part_waves);
         if (mine && crosses(query, c - mine, (unsigned long long)(m - my_mass), mine, (unsigned long long)my_mass, count,
                             value))
             f.found = threadIdx.x;
@@ -688,7 +858,7 @@ __device__ __forceinline__ bool find_listed(Finish &f, int t, int top_bin, doubl
     });
     __syncthreads();
     const uint32_t n = f.chosen;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
         const Ranked mine = f.ranked[i];
         // greater in this number: earlier in the order
         const uint64_t place = (uint64_t)mine.key << 32 | (uint32_t)~mine.index;
@@ -718,8 +888,8 @@ __device__ __forceinline__ bool find_listed(Finish &f, int t, int top_bin, doubl
 }
 
 // Smallest and largest value and number of the elements that pass.
-template <typename Each>
-__device__ __forceinline__ void range_of(Finish &f, Each each)
+template <int THREADS, typename Each>
+__device__ __forceinline__ void range_of(Finish<THREADS> &f, Each each)
 {
     if (threadIdx.x == 0) {
         f.low_key = 0xFFFFFFFFu;
@@ -762,8 +932,8 @@ __device__ __forceinline__ int shift_for(uint32_t range)
 // values are the indexes of the elements whose key is f.key and the crossing is
 // the count'th; else they are keys, and f.key, f.nth (which of the equal ones, 1,
 // 2, ...) and f.mass are set.
-template <typename T, bool REL>
-__device__ __forceinline__ void narrow(Finish &f, const T *row, int V, int t, int top_bin, double per_unit, float ref,
+template <typename T, bool REL, int THREADS>
+__device__ __forceinline__ void narrow(Finish<THREADS> &f, const T *row, int V, int t, int top_bin, double per_unit, float ref,
                                        double top_scaled, bool indexes, int query, uint32_t count, double value)
 {
     const uint32_t key = f.key;
@@ -771,7 +941,7 @@ __device__ __forceinline__ void narrow(Finish &f, const T *row, int V, int t, in
     unsigned long long mass = 0;
     // Values to find stand in falling order for keys, in rising order for indexes.
     auto each = [&](auto g) {
-        for_elements<T, 1>(row, 0, V, kThreads, [&](float x, int i) {
+        for_elements<T, 1>(row, 0, V, THREADS, [&](float x, int i) {
             const double d = scaled<REL>(x, per_unit, ref);
             if (d > top_scaled - kBins - 1) {
                 const Binned b = binned(d);
@@ -812,8 +982,10 @@ __device__ __forceinline__ void narrow(Finish &f, const T *row, int V, int t, in
             return;
         }
         const int shift = shift_for(high - low);
-        f.part_count[threadIdx.x] = 0;
-        f.part_sum[threadIdx.x] = 0;
+        if (threadIdx.x < kParts) {
+            f.part_count[threadIdx.x] = 0;
+            f.part_sum[threadIdx.x] = 0;
+        }
         if (threadIdx.x == 0)
             f.found = 0xFFFFFFFFu;
         __syncthreads();
@@ -823,11 +995,11 @@ __device__ __forceinline__ void narrow(Finish &f, const T *row, int V, int t, in
             atomicAdd(&f.part_sum[part], (unsigned long long)(2147483648LL + q));
         });
         __syncthreads();
-        const uint32_t mine = f.part_count[threadIdx.x];
-        const long long my_mass = (long long)f.part_sum[threadIdx.x];
+        const uint32_t mine = threadIdx.x < kParts ? f.part_count[threadIdx.x] : 0;
+        const long long my_mass = threadIdx.x < kParts ? (long long)f.part_sum[threadIdx.x] : 0;
         uint32_t c = mine;
         long long m = my_mass;
-        block_sums<kThreads>(c, m, f.part_waves);
+        block_sums<THREADS>(c, m, f.part_waves);
         if (mine && crosses(indexes ? (int)kTopK : query, before + c - mine, mass + (unsigned long long)(m - my_mass), mine,
                             (unsigned long long)my_mass, count, value))
             f.found = threadIdx.x;
@@ -850,8 +1022,8 @@ __device__ __forceinline__ void narrow(Finish &f, const T *row, int V, int t, in
     }
 }
 
-template <typename T, bool REL>
-__device__ __forceinline__ void find_in_row(Finish &f, const T *row, int V, int t, int top_bin, double per_unit,
+template <typename T, bool REL, int THREADS>
+__device__ __forceinline__ void find_in_row(Finish<THREADS> &f, const T *row, int V, int t, int top_bin, double per_unit,
                                             float ref, double top_scaled, int query, uint32_t count, double value,
                                             double log_min_p)
 {
@@ -860,7 +1032,7 @@ __device__ __forceinline__ void find_in_row(Finish &f, const T *row, int V, int 
             f.mass = 0;
         __syncthreads();
         unsigned long long sum = 0;
-        for_elements<T, 1>(row, 0, V, kThreads, [&](float x, int) {
+        for_elements<T, 1>(row, 0, V, THREADS, [&](float x, int) {
             const double d = scaled<REL>(x, per_unit, ref);
             if (d > top_scaled - kBins - 1) {
                 const Binned b = binned(d);
@@ -878,25 +1050,27 @@ __device__ __forceinline__ void find_in_row(Finish &f, const T *row, int V, int 
     }
     // First the key, then for the token the index among equal keys.
     for (int pass = 0; pass < (query == kToken ? 2 : 1); ++pass)
-        narrow<T, REL>(f, row, V, t, top_bin, per_unit, ref, top_scaled, pass == 1, query, pass == 1 ? f.nth : count,
+        narrow<T, REL, THREADS>(f, row, V, t, top_bin, per_unit, ref, top_scaled, pass == 1, query, pass == 1 ? f.nth : count,
                        value);
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArgs a, int S)
+template <typename T, int THREADS>
+__global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs a, int S)
 {
-    __shared__ Finish f;
+    __shared__ Finish<THREADS> f;
     const int row = blockIdx.x;
     const RowParams p = params_of(a, row);
     const T *x = static_cast<const T *>(a.logits) + row * a.row_stride;
     if (threadIdx.x == 0)
         f.listed = 0;
-    if (S == 1) {
-        join_slices<kThreads>(a, row, S, p.per_unit, f.sums, f.waves);
+    if (threadIdx.x < kBins)
+        f.factor[threadIdx.x] = factors.of[threadIdx.x];
+    if constexpr (THREADS == kScanThreads) {  // one slice
+        join_slices<THREADS, 1>(a, row, 1, p.per_unit, f.sums, f.waves, f.joined);
     } else {
         const uint32_t *from = reinterpret_cast<const uint32_t *>(sums_of(a, row, S));
         uint32_t *to = reinterpret_cast<uint32_t *>(&f.sums);
-        for (int i = threadIdx.x; i < (int)(sizeof(RowSums) / 4); i += kThreads)
+        for (int i = threadIdx.x; i < (int)(sizeof(RowSums) / 4); i += THREADS)
             to[i] = from[i];
         __syncthreads();
     }
@@ -931,7 +1105,7 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
         const uint32_t total = __shfl(upto, kWave - 1);
         one_by_one = __any(own > kSliceList) || total > kList;
         if (!one_by_one)
-            for (int s = wave; s < S; s += kThreads / kWave) {
+            for (int s = wave; s < S; s += THREADS / kWave) {
                 const uint32_t n = __shfl(own, s), to = __shfl(upto, s) - n;
                 const Entry *list = list_of(slice_at(a, row, s, S));
                 for (uint32_t i = lane; i < n; i += kWave)
@@ -942,10 +1116,12 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
         __syncthreads();
     } else {
         // Counted again, relative to the maximum.
-        f.part_count[threadIdx.x] = 0;
-        f.part_sum[threadIdx.x] = 0;
+        if (threadIdx.x < kParts) {
+            f.part_count[threadIdx.x] = 0;
+            f.part_sum[threadIdx.x] = 0;
+        }
         __syncthreads();
-        for_elements<T, 1>(x, 0, a.V, kThreads, [&](float v, int) {
+        for_elements<T, 1>(x, 0, a.V, THREADS, [&](float v, int) {
             const double d = scaled<true>(v, p.per_unit, top);
             if (d > -(kBins - 1)) {
                 const Binned b = binned(d);
@@ -957,16 +1133,16 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
         const int t = threadIdx.x;
         const uint32_t c = t < kBins ? f.part_count[t] : 0;
         const double m =
-            t < kBins ? ((double)c * (double)kUnit + (double)(long long)f.part_sum[t]) * bin_factor(t) : 0.0;
+            t < kBins ? ((double)c * (double)kUnit + (double)(long long)f.part_sum[t]) * f.factor[t] : 0.0;
         __syncthreads();
-        store_sums<kThreads>(f.sums, c, m, f.waves);
+        store_sums<THREADS>(f.sums, c, m, f.waves);
     }
 
     // The searches, in the order of the filters.
-    const Search find(f.sums);
     double kept = f.sums.mass[kBins - 1], limit = kept;  // mass kept so far; of the top-k prefix
     int t = 0;
     for (int query = kTopK; query <= kToken; ++query) {
+        const Search find(f.sums);  // read again: held over the turns, its 18 registers would spill
         uint32_t count = 0;
         double value = 0.0;
         if (query == kTopK) {
@@ -985,7 +1161,7 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
             t = query == kTopP ? find.first_mass<false>(target) : find.first_mass<true>(target);
             // A value that rounding took to the bin's edge still crosses at the
             // first element (every weight is far above 1/2).
-            value = (target - mass_before(f.sums, t)) / bin_factor(t);
+            value = (target - mass_before(f.sums, t)) / f.factor[t];
             const double least = query == kTopP ? 0.5 : 0.0;
             value = value > least ? value : least;
         }
@@ -999,7 +1175,7 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
                 if (threadIdx.x == 0)
                     f.listed = 0;
                 __syncthreads();
-                list_wanted(x, 0, a.V, kThreads, p.per_unit, top_scaled, w, &f.listed, f.list, kList);
+                list_wanted(x, 0, a.V, THREADS, p.per_unit, top_bin, w, &f.listed, f.places, kList, f.list);
                 __syncthreads();
                 listed = f.listed <= kList;
                 again = !listed && !one_by_one;
@@ -1013,12 +1189,12 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
             done = find_listed(f, t, top_bin, p.per_unit, query, count, value, top_scaled, p.log_min_p);
         if (__builtin_expect(!done, 0)) {
             if (fine)
-                find_in_row<T, false>(f, x, a.V, t, top_bin, p.per_unit, 0.f, top_scaled, query, count, value, p.log_min_p);
+                find_in_row<T, false, THREADS>(f, x, a.V, t, top_bin, p.per_unit, 0.f, top_scaled, query, count, value, p.log_min_p);
             else
-                find_in_row<T, true>(f, x, a.V, t, top_bin, p.per_unit, top, top_scaled, query, count, value, p.log_min_p);
+                find_in_row<T, true, THREADS>(f, x, a.V, t, top_bin, p.per_unit, top, top_scaled, query, count, value, p.log_min_p);
         }
         if (query != kToken) {
-            const double m = mass_before(f.sums, t) + (double)f.mass * bin_factor(t);
+            const double m = mass_before(f.sums, t) + (double)f.mass * f.factor[t];
             kept = m < kept ? m : kept;
             if (query == kTopK)
                 limit = kept;
@@ -1031,7 +1207,7 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(const SampleArg
             // the weight as the sums hold it, so that a token kept alone has share 1
             const float v = key_value(f.key);
             const int q = binned(fine ? scaled<false>(v, p.per_unit, 0.f) : scaled<true>(v, p.per_unit, top)).q;
-            const double lp = log((double)(2147483648LL + q) * bin_factor(t) / kept);
+            const double lp = log((double)(2147483648LL + q) * f.factor[t] / kept);
             a.logprobs[row] = lp < 0.0 ? (float)lp : 0.f;
         }
     }
@@ -1056,12 +1232,15 @@ hipError_t launch(const SampleArgs &a, hipStream_t stream)
     sample_histogram_kernel<T><<<dim3(S, a.M), kScanThreads, 0, stream>>>(a, S);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && S > 1) {
-        sample_gather_kernel<T><<<dim3(S, a.M), kScanThreads, 0, stream>>>(a, S);
+        sample_gather_kernel<T><<<dim3(S, a.M), kThreads, 0, stream>>>(a, S);
         e = hipGetLastError();
     }
     if (e != hipSuccess)
         return e;
-    sample_finish_kernel<T><<<dim3(a.M), kThreads, 0, stream>>>(a, S);
+    if (S > 1)
+        sample_finish_kernel<T, kThreads><<<dim3(a.M), kThreads, 0, stream>>>(a, S);
+    else
+        sample_finish_kernel<T, kScanThreads><<<dim3(a.M), kScanThreads, 0, stream>>>(a, S);
     return hipGetLastError();
 }
 
