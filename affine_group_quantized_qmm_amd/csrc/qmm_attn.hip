@@ -3,29 +3,38 @@
 //
 // For one sequence and one kv head the query rows that read the same keys are
 // the (row, head of the group) pairs; they are the 16-wide columns of the
-// matrix instructions, up to NT tiles of 16 in a workgroup. A wave walks over
-// tiles of 32 tokens:
+// matrix instructions, up to NT tiles of 16 in a workgroup. A wave holds 16
+// tokens at a time:
 //
-//   S^T = K Q^T      16x16x32 MFMA; K goes from memory straight to the operand
-//                    registers (lane = token, 16 bytes of its row)
-//   p = 2^(s - m)    a lane holds 8 tokens of one column, so that maximum and
-//                    sum stay in the lane; m is raised (and the accumulators
-//                    rescaled) only when some score passes it by 2^8, which
-//                    bounds p and needs no exchange between lanes per tile
-//   O^T += V^T P^T   the 8 tokens that a lane holds after the first product are
-//                    the 8 it must supply to the second, so P needs no movement;
-//                    V^T comes out of LDS with transposing reads
+//   S^T = K Q^T      16x16x32 MFMA, tokens by columns
+//   p = 2^(s - m)    a lane holds 4 tokens of one column; the columns' running
+//                    maxima m are in LDS and are raised (and the accumulators
+//                    rescaled) only when some score passes them by 2^8, which
+//                    bounds p and leaves nothing to exchange in most turns
+//   O^T += V^T P^T   over 32 tokens: the 4 + 4 that one lane group wrote of two
+//                    waves; V^T comes out of LDS with transposing reads
 //
 // P is kept as the sum of two 16-bit numbers (a rounding and its remainder):
 // rounding p once to bf16 would add an error as large as the output's own
 // rounding, and the matrix units have room for the second product.
 //
-// What bounds it is the stream of K and V: each byte is read once by a
-// workgroup, and a wave keeps the whole next tile's K and V loads in flight
-// (registers) while it computes. Waves share nothing until the end, where the
-// four waves of a workgroup are joined through LDS. When (sequence, kv head)
-// pairs are few, the visible length is cut into splits of equal token counts
-// whose partials a second kernel joins.
+// A tile is 16 tokens for each wave of a workgroup. Each wave multiplies its own
+// 16 tokens with all columns; the columns' maxima meet in LDS, P and V lie there
+// for the second product, which the waves split along the head (D / waves
+// values each), so that the accumulators of up to 96 columns fit and a piece of
+// the cache is read once by one workgroup. K and V come in whole rows with the
+// nontemporal hint, straight past the barriers into registers: the next tile's
+// are in flight while this one is computed.
+//
+// What bounds it is that stream: 6.2 TB/s of 1.61 GB (64 sequences of 4k to 8k
+// tokens, 8 heads of 128) where a kernel that does nothing but read such pages
+// reaches 6.75; a fixed 10 to 12 us (the plan, the first pages, the join)
+// where there is little to read.
+//
+// How a call is laid out: (sequence, kv head) pairs are too few or too unequal
+// to fill the GPU as they are, and their lengths are known on the GPU alone.
+// Every workgroup sums up the lengths and finds its own equal share (see
+// "How they are dealt out" below); a second kernel joins pieces of one item.
 #include "qmm_device.hpp"
 #include "qmm_kernels.hpp"
 #include "qmm_step.hpp"
@@ -36,14 +45,16 @@ namespace {
 constexpr int kJoinThreads = 1024;
 // Waves of a workgroup; each has 16 tokens of a tile. A turn of a wave is some
 // thousand instructions one after the other, which only another wave of the
-// same SIMD can hide: wide heads, whose registers and LDS leave room for one
-// workgroup on a CU, take two waves a SIMD.
-constexpr int waves_of(int D) { return D >= 128 ? 8 : 4; }
-constexpr int tile_of(int D) { return 16 * waves_of(D); }
+// same SIMD can hide. Heads of 192 and 256, whose registers and LDS leave room
+// for one workgroup on a CU, take two waves a SIMD (131071 tokens of 4 heads of
+// 256: 96 us against 110 with four waves); narrower ones get them from a second
+// workgroup (64 sequences, 8 heads of 128: 260 us with two of four waves, 262
+// with one of eight; 32 sequences of 1000 tokens 28.6 against 31.6).
+// So do the most columns (6 tiles of heads of 128), whose accumulators would
+// spill with four.
+constexpr int waves_of(int D, int NT) { return D >= 192 || (D == 128 && NT == 6) ? 8 : 4; }
+constexpr int tile_of(int D, int NT) { return 16 * waves_of(D, NT); }
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;   // token without a row in the cache
-#ifndef PERCU
-#define PERCU 0
-#endif
 constexpr float kRaise = 8.0f;             // a score may pass the running maximum by this (log2)
 
 typedef float float2_t __attribute__((ext_vector_type(2)));
@@ -197,12 +208,12 @@ __device__ __forceinline__ void lds_barrier()
 }
 
 template <typename T, int D, int NT>
-__global__ __launch_bounds__(waves_of(D) * kWave, 2) void attn_kernel(const AttnArgs a)
+__global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const AttnArgs a)
 {
     using E = Elem<T>;
     using x8 = typename E::x8;
     using x4 = typename E::x4;
-    constexpr int kWaves = waves_of(D), kTile = tile_of(D);
+    constexpr int kWaves = waves_of(D, NT), kTile = tile_of(D, NT);
     constexpr int KS = D / 32;                  // contraction steps of K Q^T; loads of a lane for K and for V
     constexpr int DT = D / 16;                  // output tiles along the head
     constexpr int DW = (DT + kWaves - 1) / kWaves;  // of one wave: tiles wave, wave + kWaves, ...
@@ -817,7 +828,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
 template <typename T, int D, int NT>
 hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
-    attn_kernel<T, D, NT><<<dim3((uint32_t)p.blocks), waves_of(D) * kWave, 0, stream>>>(a);
+    attn_kernel<T, D, NT><<<dim3((uint32_t)p.blocks), waves_of(D, NT) * kWave, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.whole)
         return e;
@@ -876,15 +887,17 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context,
     p.col_tiles = (int)((col_tiles + chunks - 1) / chunks);
     p.col_tiles += p.col_tiles == 5;
     p.chunks = (int)((col_tiles + p.col_tiles - 1) / p.col_tiles);
-    const int kTile = tile_of(D);
+    const int kTile = tile_of(D, p.col_tiles);
     int64_t visible = max_context;
     if (window > 0 && (int64_t)window + max_rows + sinks + 2 * kTile < visible)
         visible = (int64_t)window + max_rows + sinks + 2 * kTile;
     const int64_t tiles = visible > kTile ? (visible + kTile - 1) / kTile : 1;
     const int64_t items = (int64_t)B * Hkv * p.chunks;
-    // Workgroups of a full GPU: as many as keep 64 KB of K and V or more in
-    // flight on a CU (a workgroup has a tile of each).
-    const int per_cu = PERCU ? PERCU : D >= 128 ? 1 : 4;
+    // Workgroups of a full GPU: as many as keep 48 to 64 KB of K and V in flight
+    // on a CU (a workgroup has a tile of each). More only add plans, partial
+    // results and joins: 131071 tokens take 96 us with one on a CU and 111 with
+    // two, heads of 64 with a window 24.3, 23.8 and 24.3 with two, three and four.
+    const int per_cu = waves_of(D, p.col_tiles) == 8 ? 1 : D >= 96 ? 2 : 3;
     const int64_t full = (int64_t)per_cu * device_cu_count();
     // The runs count tiles in 31 bits, up to the block table's end.
     const int64_t most_tiles = items * ((int64_t)max_pages * page_size / kTile + 1);

@@ -50,6 +50,10 @@ constexpr double kPerUnit = 8.0;     // bins per unit of z
 constexpr int kSumBits = 46;         // low field of a packed bin: the sum of q
 constexpr float kUnit = 2147483648.0f;   // 2^31: the weight of a bin's centre
 constexpr int kMaxSlice = 1 << 17;   // elements of a slice: the packed number has 18 bits, the sum 45 and a sign
+// Rows up to this long are gathered by the workgroup that finishes them: 32000
+// logits 19.7 us a call against 20.8 with a launch of its own for the gather,
+// 65000 22.0 and 22.0, 131072 27.3 and 22.9 (one row, top-k and top-p).
+constexpr int kGatherMin = 1 << 16;
 constexpr int kMaxSlices = 64;
 constexpr int kSliceList = 1024;     // listed elements of a slice
 constexpr int kList = 8192;          // listed elements of a row
@@ -818,18 +822,18 @@ __device__ __forceinline__ bool find_listed(Finish<THREADS> &f, int t, int top_b
         return true;
     }
     if (total > kWhole) {
-        if (threadIdx.x < kParts) {
-            f.part_count[threadIdx.x] = 0;
+        if (threadIdx.x < kParts)
             f.part_sum[threadIdx.x] = 0;
-        }
         __syncthreads();
-        each([&](const Entry &, int part, uint32_t w, double) {
-            atomicAdd(&f.part_count[part], 1u);
-            atomicAdd(&f.part_sum[part], (unsigned long long)w);
+        each([&](const Entry &, int part, uint32_t w, double) {  // packed as in the histogram
+            atomicAdd(&f.part_sum[part], ((unsigned long long)1 << kSumBits) + (long long)(int32_t)(w - 2147483648u));
         });
         __syncthreads();
-        const uint32_t mine = threadIdx.x < kParts ? f.part_count[threadIdx.x] : 0;
-        const long long my_mass = threadIdx.x < kParts ? (long long)f.part_sum[threadIdx.x] : 0;
+        uint32_t mine = 0;
+        int64_t q = 0;
+        if (threadIdx.x < kParts)
+            unpack(f.part_sum[threadIdx.x], mine, q);
+        const long long my_mass = (long long)mine * 2147483648LL + q;
         uint32_t c = mine;
         long long m = my_mass;
         block_sums<THREADS>(c, m, f.part_waves);
@@ -1065,8 +1069,9 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
         f.listed = 0;
     if (threadIdx.x < kBins)
         f.factor[threadIdx.x] = factors.of[threadIdx.x];
-    if constexpr (THREADS == kScanThreads) {  // one slice
-        join_slices<THREADS, 1>(a, row, 1, p.per_unit, f.sums, f.waves, f.joined);
+    constexpr bool kLists = THREADS == kScanThreads;  // no gather before
+    if constexpr (kLists) {
+        join_slices<THREADS, 8>(a, row, S, p.per_unit, f.sums, f.waves, f.joined);
     } else {
         const uint32_t *from = reinterpret_cast<const uint32_t *>(sums_of(a, row, S));
         uint32_t *to = reinterpret_cast<uint32_t *>(&f.sums);
@@ -1090,7 +1095,7 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
     // (one slice) listed below; where these are too many, of one search at a time.
     Wanted w{-1, 0, -1, -1, 0, -1};
     bool listed = fine, list_now = false, one_by_one = false;
-    if (fine && S == 1) {
+    if (fine && kLists) {
         w = wanted_bins(f.sums, p, top_scaled);
         list_now = true;
     } else if (fine) {
@@ -1231,13 +1236,14 @@ hipError_t launch(const SampleArgs &a, hipStream_t stream)
     const int S = slices_of(a.M, a.V);
     sample_histogram_kernel<T><<<dim3(S, a.M), kScanThreads, 0, stream>>>(a, S);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && S > 1) {
+    const bool gather = S > 1 && a.V > kGatherMin;
+    if (e == hipSuccess && gather) {
         sample_gather_kernel<T><<<dim3(S, a.M), kThreads, 0, stream>>>(a, S);
         e = hipGetLastError();
     }
     if (e != hipSuccess)
         return e;
-    if (S > 1)
+    if (gather)
         sample_finish_kernel<T, kThreads><<<dim3(a.M), kThreads, 0, stream>>>(a, S);
     else
         sample_finish_kernel<T, kScanThreads><<<dim3(a.M), kScanThreads, 0, stream>>>(a, S);
