@@ -16,19 +16,22 @@ Tensors (all on one ROCm device, contiguous):
 from __future__ import annotations
 
 import ctypes
-import math
 from pathlib import Path
 
 import torch
 
 LIBRARY_PATH = Path(__file__).resolve().parent / "libqmm.so"
 
-if not LIBRARY_PATH.exists():
+_BINDING_PATH = LIBRARY_PATH.with_name("_qmm_torch.so")
+_missing = [str(path) for path in (LIBRARY_PATH, _BINDING_PATH) if not path.exists()]
+if _missing:
     raise ImportError(
-        f"{LIBRARY_PATH} is missing: build the HIP library first "
+        f"{' and '.join(_missing)} missing: build the HIP library first "
         "(python -c 'import __graft_entry__ as g; g.build()' at the repository root)")
 
 _lib = ctypes.CDLL(str(LIBRARY_PATH))
+
+from . import _qmm_torch as _binding  # noqa: E402  (built beside the library, and loads the same libqmm.so)
 
 _p, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _lib.qmm_pack.argtypes = [_p, _p, _i, _i, _i, _p]
@@ -406,46 +409,16 @@ def qmm_forward_splitk_noalloc(x, wq, scales, biases, bits: int, G: int, split_k
 # ---------------------------------------------------------------------------
 # Between the products of a decode step.
 # ---------------------------------------------------------------------------
-_TYPE_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}  # QMM_F16, QMM_BF16, QMM_F32
-_HALVES = (torch.float16, torch.bfloat16)
+# The step operators' checks of tensors are compiled (csrc/qmm_torch.cpp): these
+# calls are made for every layer of a step, with kernels of a few microseconds.
+def _step_result(result, name: str):
+    if type(result) is int:
+        raise QmmError(result, name)
+    return result
 
 
-def _need(t, name: str, dtype, shape, index: int) -> int:
-    """_check for the calls of a decode step, where a microsecond counts: one
-    pass over what has to hold (`index`: the GPU's), and _check itself only to
-    say what does not. Returns the address."""
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
-        _check(t, name, (dtype,), shape, torch.device("cuda", index) if index >= 0 else None)
-    return t.data_ptr()
-
-
-def _need_or_none(t, name: str, dtype, shape, index: int):
-    return None if t is None else _need(t, name, dtype, shape, index)
-
-
-def _need_rows(t, name: str, dtype, shape, index: int) -> int:
-    """_need for a tensor whose rows may lie apart; returns the row stride."""
-    if t.is_contiguous():
-        _need(t, name, dtype, shape, index)
-        return math.prod(shape[1:])
-    if t.shape != shape or not t[0].is_contiguous():
-        raise ValueError(f"{name} must have shape {tuple(shape)}, contiguous within a row, got {tuple(t.shape)}")
-    _need(t[0], name, dtype, shape[1:], index)
-    return t.stride(0)
-
-
-def _cache_shape(k_cache, v_cache, D: int, index: int):
-    """(num_pages, Hkv, page_size) of the caches, checked."""
-    if k_cache.dim() != 4:
-        raise ValueError("the caches must be 4-D [num_pages, Hkv, page_size, D]")
-    shape = k_cache.shape
-    if k_cache.dtype not in _HALVES:
-        raise TypeError(f"the caches must be float16 or bfloat16, got {k_cache.dtype}")
-    if shape[3] != D:
-        raise ValueError(f"the caches' D is {shape[3]}, the queries' {D}")
-    _need(k_cache, "k_cache", k_cache.dtype, shape, index)
-    _need(v_cache, "v_cache", k_cache.dtype, shape, index)
-    return shape[0], shape[1], shape[2]
+def _step_stream(t: torch.Tensor) -> int:
+    return _stream(t) if t.is_cuda else 0  # a tensor elsewhere is refused by the call
 
 
 def qmm_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache, *, eps: float = 1e-6,
@@ -455,30 +428,9 @@ def qmm_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_
     caches' type. q, k and v share one type (float32, float16 or bfloat16) and
     may be views of a fused projection's rows; inv_freq [R/2] float32, or None
     for no rotation."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q, k and v must be 3-D [M, heads, D]")
-    M, Hq, D = q.shape
-    index, tin = q.get_device(), q.dtype
-    if tin not in _TYPE_CODES or index < 0:
-        raise ValueError(f"q must be float32, float16 or bfloat16 on the GPU, got {tin} on {q.device}")
-    pages, Hkv, page_size = _cache_shape(k_cache, v_cache, D, index)
-    tout = k_cache.dtype
-    qs = _need_rows(q, "q", tin, (M, Hq, D), index)
-    ks = _need_rows(k, "k", tin, (M, Hkv, D), index)
-    vs = _need_rows(v, "v", tin, (M, Hkv, D), index)
-    R = 2 * inv_freq.numel() if inv_freq is not None else 0
-    if out is None:
-        out = torch.empty((M, Hq, D), dtype=tout, device=q.device)
-    rc = _lib.qmm_qk_norm_rope(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _TYPE_CODES[tin],
-        _need(q_weight, "q_weight", torch.float32, (D,), index), _need(k_weight, "k_weight", torch.float32, (D,), index),
-        eps, weight_offset, _need(positions, "positions", torch.int32, (M,), index),
-        _need_or_none(inv_freq, "inv_freq", torch.float32, (R // 2,), index), R, interleaved,
-        _need(slots, "slots", torch.int32, (M,), index), _need(out, "out", tout, (M, Hq, D), index),
-        k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[tout], M, Hq, Hkv, D, pages, page_size, _stream(q))
-    if rc:
-        raise QmmError(rc, "qmm_qk_norm_rope")
-    return out
+    return _step_result(_binding.qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache,
+                                              out, eps, weight_offset, interleaved, _step_stream(q)),
+                        "qmm_qk_norm_rope")
 
 
 def qmm_paged_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int, max_rows: int, max_context: int,
@@ -496,33 +448,9 @@ def qmm_paged_attention(q, k_cache, v_cache, block_table, context_lens, row_star
     1/sqrt(D); `lse` (float32 [T, Hq]), when given, receives the logarithm of
     each row's sum. max_rows bounds the rows of a sequence, max_context guides
     the split of the length."""
-    if q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q must be 3-D [T, Hq, D] and block_table 2-D [B, max_pages]")
-    T, Hq, D = q.shape
-    B, max_pages = block_table.shape
-    index = q.get_device()
-    if index < 0:
-        raise ValueError(f"q must be on the GPU, got {q.device}")
-    pages, Hkv, page_size = _cache_shape(k_cache, v_cache, D, index)
-    dtype = k_cache.dtype
-    qs = _need_rows(q, "q", dtype, (T, Hq, D), index)
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
-    need = _lib.qmm_paged_attention_workspace_bytes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    rc = _lib.qmm_paged_attention(
-        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _TYPE_CODES[dtype],
-        _need(block_table, "block_table", torch.int32, (B, max_pages), index),
-        _need(context_lens, "context_lens", torch.int32, (B,), index),
-        _need(row_starts, "row_starts", torch.int32, (B + 1,), index), _need(out, "out", dtype, (T, Hq, D), index),
-        _need_or_none(lse, "lse", torch.float32, (T, Hq), index), T, B, Hq, Hkv, D, pages, page_size, max_pages,
-        max_rows, max_context, scale if scale is not None else D ** -0.5, window, sinks,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(q))
-    if rc:
-        raise QmmError(rc, "qmm_paged_attention")
-    return out
+    return _step_result(_binding.paged_attention(q, k_cache, v_cache, block_table, context_lens, row_starts, max_rows,
+                                                 max_context, scale, window, sinks, out, lse, workspace,
+                                                 _step_stream(q)), "qmm_paged_attention")
 
 
 def qmm_sample_workspace_bytes(M: int, V: int) -> int:
@@ -535,26 +463,5 @@ def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
     u [M]; temperature, top_k (int32), top_p and min_p are per-row tensors or
     None. `logprobs` (float32 [M]), when given, receives the logarithm of each
     token's share of the kept mass."""
-    if logits.dim() != 2:
-        raise ValueError("logits must be 2-D [M, V]")
-    M, V = logits.shape
-    index = logits.get_device()
-    if logits.dtype not in _TYPE_CODES or index < 0:
-        raise ValueError(f"logits must be float32, float16 or bfloat16 on the GPU, got {logits.dtype} on {logits.device}")
-    stride = _need_rows(logits, "logits", logits.dtype, (M, V), index)
-    if tokens is None:
-        tokens = torch.empty(M, dtype=torch.int32, device=logits.device)
-    if workspace is None:
-        workspace = torch.empty(_lib.qmm_sample_workspace_bytes(M, V), dtype=torch.uint8, device=logits.device)
-    rows = (M,)
-    rc = _lib.qmm_sample(
-        logits.data_ptr(), stride, _TYPE_CODES[logits.dtype], _need(u, "u", torch.float32, rows, index),
-        _need_or_none(temperature, "temperature", torch.float32, rows, index),
-        _need_or_none(top_k, "top_k", torch.int32, rows, index),
-        _need_or_none(top_p, "top_p", torch.float32, rows, index),
-        _need_or_none(min_p, "min_p", torch.float32, rows, index), _need(tokens, "tokens", torch.int32, rows, index),
-        _need_or_none(logprobs, "logprobs", torch.float32, rows, index), M, V, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(logits))
-    if rc:
-        raise QmmError(rc, "qmm_sample")
-    return tokens
+    return _step_result(_binding.sample(logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, workspace,
+                                        _step_stream(logits)), "qmm_sample")

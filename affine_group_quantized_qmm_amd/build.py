@@ -1,7 +1,10 @@
-"""Build the gfx950 HIP library ``libqmm.so`` in this package directory.
+"""Build the gfx950 HIP library ``libqmm.so`` in this package directory, and the
+compiled part of the Python binding, ``_qmm_torch.so``.
 
 Every ``csrc/*.hip`` file is compiled with hipcc for gfx950 only and linked
-into one shared library exporting the C ABI of ``include/qmm.h``.
+into one shared library exporting the C ABI of ``include/qmm.h``. The binding
+(``csrc/qmm_torch.cpp``, host code) is compiled with g++ against the installed
+torch and linked to that library.
 
 The build also reads the compiler's kernel-resource-usage remarks and fails if
 any kernel spills registers to scratch memory: the kernels are designed to fit
@@ -15,6 +18,7 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -22,6 +26,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD_DIR = PKG / "_build"
 LIBRARY = PKG / "libqmm.so"
+BINDING = PKG / "_qmm_torch.so"
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -92,7 +97,26 @@ def build(jobs: int | None = None) -> Path:
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", str(tmp), *map(str, objs)]
     subprocess.run(cmd, check=True, capture_output=True, text=True)
     os.replace(tmp, LIBRARY)
+    build_binding()
     return LIBRARY
+
+
+def build_binding() -> Path:
+    """Compile and link ``_qmm_torch.so`` (needs ``libqmm.so``); returns its path."""
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = Path(torch.__file__).resolve().parent / "lib"
+    tmp = BINDING.with_suffix(".so.tmp")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__",
+           f"-I{ROOT / 'include'}", "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"]]
+    for path in include_paths():
+        cmd += ["-isystem", path]
+    cmd += [str(CSRC / "qmm_torch.cpp"), "-o", str(tmp), f"-L{lib}", f"-L{PKG}", "-lqmm", "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    _run(cmd, CSRC / "qmm_torch.cpp")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
