@@ -565,14 +565,16 @@ __device__ __forceinline__ Wanted wanted_bins(const RowSums &sums, const RowPara
 }
 
 // Intervals of logits that hold the wanted bins. Their ends are moved outwards
-// by more than their roundings; what they let in besides is told apart by its
-// bin later. Overlapping ones are one.
+// by more than their roundings (to fp32 at most 4096 bins from zero: 2^-12 of a
+// bin); what they let in besides is told apart by its bin later. Overlapping
+// ones are one.
 struct Intervals {
     float low[4], high[4];
     int number;
 };
 __device__ __forceinline__ Intervals intervals_of(const Wanted &w, double per_unit, int top_bin)
 {
+    constexpr double kReach = 0.5 + 0x1p-10;
     const double unit = 1.0 / per_unit;
     Intervals v;
     v.number = 0;
@@ -587,7 +589,7 @@ __device__ __forceinline__ Intervals intervals_of(const Wanted &w, double per_un
         if (last[k] < first[k] || last[k] < 0)
             continue;
         // bin t: z of (top_bin - t - 1/2) / 8 .. (top_bin - t + 1/2) / 8
-        float l = (float)((top_bin - last[k] - 0.75) * unit), h = (float)((top_bin - first[k] + 0.75) * unit);
+        float l = (float)((top_bin - last[k] - kReach) * unit), h = (float)((top_bin - first[k] + kReach) * unit);
 #pragma unroll
         for (int j = 0; j < k; ++j)
             if (v.low[j] <= h && l <= v.high[j]) {  // takes j over
@@ -741,8 +743,9 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(const SampleArg
 // ---------------------------------------------------------------------------
 // 3. Finish: one workgroup a row.
 // ---------------------------------------------------------------------------
-struct Ranked {
-    uint32_t key, index, weight;
+struct alignas(16) Ranked {
+    uint64_t place;   // order_key and ~index: greater is earlier in the order, 0 is no element
+    uint32_t weight;
 };
 template <int THREADS>
 struct Finish {
@@ -855,35 +858,56 @@ __device__ __forceinline__ bool find_listed(Finish<THREADS> &f, int t, int top_b
         if (f.number > kRanked)
             return false;
     }
+    for (int i = threadIdx.x; i < kRanked; i += THREADS)
+        f.ranked[i].place = 0;
     __syncthreads();
     each([&](const Entry &e, int p, uint32_t w, double) {
         if (part < 0 || p == part)
-            f.ranked[atomicAdd(&f.chosen, 1u)] = Ranked{order_key(e.x), e.index, w};
+            f.ranked[atomicAdd(&f.chosen, 1u)] = Ranked{(uint64_t)order_key(e.x) << 32 | (uint32_t)~e.index, w};
     });
     __syncthreads();
+    // Each element is compared with all, where they are many by several
+    // neighbouring lanes (16-bit logits leave hundreds of equal ones: 258 take
+    // 7.2 us, by one lane each 13); for a few the lanes' sums would cost more.
+    constexpr int AT_ONCE = 4;
     const uint32_t n = f.chosen;
-    for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
+    int lanes = 0;  // their logarithm
+    while ((n >> lanes) > 16 && (n << (lanes + 1)) <= (uint32_t)THREADS)
+        ++lanes;
+    // a turn starts below n, at a multiple of AT_ONCE << lanes, and stays inside
+    static_assert(kRanked % (AT_ONCE * kScanThreads / 16) == 0, "kRanked is a multiple of a turn");
+    const uint32_t share = threadIdx.x & ((1u << lanes) - 1);
+    for (uint32_t i = threadIdx.x >> lanes; i < n; i += (uint32_t)THREADS >> lanes) {
         const Ranked mine = f.ranked[i];
-        // greater in this number: earlier in the order
-        const uint64_t place = (uint64_t)mine.key << 32 | (uint32_t)~mine.index;
-        uint32_t c = before;
-        unsigned long long from = mass;
-#pragma unroll 4
-        for (uint32_t j = 0; j < n; ++j) {
-            const Ranked e = f.ranked[j];
-            const bool earlier = ((uint64_t)e.key << 32 | (uint32_t)~e.index) > place;
-            c += earlier ? 1u : 0u;
-            from += earlier ? e.weight : 0u;
+        uint32_t c = 0;
+        unsigned long long from = 0;
+        for (uint32_t j0 = share; j0 < n; j0 += AT_ONCE << lanes) {
+            Ranked e[AT_ONCE];
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j)
+                e[j] = f.ranked[j0 + (j << lanes)];
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+                const bool earlier = e[j].place > mine.place;
+                c += earlier ? 1u : 0u;
+                from += earlier ? e[j].weight : 0u;
+            }
         }
+        for (int d = 1; d < 1 << lanes; d *= 2) {
+            c += __shfl_xor(c, d);
+            from += __shfl_xor(from, d);
+        }
+        c += before;
+        from += mass;
         const bool last = c + 1 == before + n;
         const bool here = crosses(query, c, from, 1, mine.weight, count, value);
         // not crossed: the last element (its sum is below the value, or the count)
         const bool none = last && (query == kTopK   ? c + 1 < count
                                    : query == kTopP ? (double)(from + mine.weight) < value
                                                     : (double)(from + mine.weight) <= value);
-        if (here || none) {
-            f.key = mine.key;
-            f.nth = mine.index;
+        if (share == 0 && (here || none)) {
+            f.key = (uint32_t)(mine.place >> 32);
+            f.nth = ~(uint32_t)mine.place;
             f.mass = from + mine.weight;
         }
     }
