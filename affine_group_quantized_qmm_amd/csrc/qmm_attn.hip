@@ -901,13 +901,24 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context,
     const int64_t full = (int64_t)per_cu * device_cu_count();
     // The runs count tiles in 31 bits, up to the block table's end.
     const int64_t most_tiles = items * ((int64_t)max_pages * page_size / kTile + 1);
-    p.whole = tiles <= 2 || items >= 8 * full || most_tiles > INT32_MAX;
+    // Whole items where a join costs more than it saves: up to 256 tokens (24
+    // heads over 4 of 128, 150 to 190 tokens: 7.5 us against 10.7; 500 tokens of
+    // heads of 256 18 against 12 in pieces), up to 1024 with two items or more
+    // for each workgroup (256 sequences, 8 heads of 128, 600 tokens: 84 us against
+    // 93; 4000 tokens 515 against 499), and where they are eight (512 sequences of
+    // 600 tokens: 159 against 176).
+    p.whole = visible <= 256 || items >= (visible <= 1024 ? 2 : 8) * full || most_tiles > INT32_MAX;
     const int64_t groups = items * tiles < full ? items * tiles : full;
     p.groups = (int)groups;
     p.items = items;
     p.blocks = p.whole ? ((int64_t)B * Hkv + 7) / 8 * 8 * p.chunks : p.groups;
+    // Pieces where items have four or more (16 sequences of 4000 tokens, 8 heads
+    // of 128: 42 us against 45 in runs), runs where few of unequal length share
+    // the GPU (32 sequences: 74 against 80 in pieces).
     // Workgroups of the join for each item: one for each column while the items
-    // have many pieces, else one for a few columns; and their threads.
+    // have many pieces, else one for a few columns; and their threads (one
+    // sequence of 4000 tokens: 13.3 us with 1024, 13.8 with 256; 64 sequences of
+    // 600 36 with 1024, 31 with 256).
     const int live = (int)(columns < 16 * p.col_tiles ? columns : 16 * p.col_tiles);
     p.pieces = items * 4 <= groups;
     p.join_columns = p.pieces ? live : (live + 3) / 4;

@@ -1242,13 +1242,15 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
     }
 }
 
-// Slices of a row: enough workgroups to fill the GPU, none with fewer
-// elements than its threads load at a time (4 units of 16 bytes of fp32).
+// Slices of a row: enough workgroups to fill the GPU (64 rows of 131072 logits:
+// 34 us a call; with half as many 42, with twice as many 36), none with fewer
+// than 8 elements for each thread (one such row: 22.9 us; with 4 or 16 elements
+// 23.9, for the slices have to be joined by each workgroup of the gather).
 int slices_of(int M, int V)
 {
     const int least = (V + kMaxSlice - 1) / kMaxSlice;
     int s = device_cu_count() / M;
-    const int most = V / (4 * kScanThreads);
+    const int most = V / (8 * kScanThreads);
     s = s < most ? s : most;
     s = s < kMaxSlices ? s : kMaxSlices;
     return s > least ? s : least > 1 ? least : 1;
