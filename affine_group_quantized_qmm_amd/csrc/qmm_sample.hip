@@ -34,6 +34,15 @@
 //
 // Each launch reads the logits at most once; a row is cut into slices so that
 // few rows still fill the GPU.
+//
+// What bounds it. Few rows: two or three launches one after the other, each with
+// its code to fetch: one row of 131072 fp32 logits takes 19 us (histogram 4,
+// gather 9, finish 6), 16 rows with top-k and top-p 27, 32 rows of 32003 fp16
+// logits 24. 256 rows of 131072 bf16 logits with top-p take 68 us: the histogram
+// 25, for which a CU issues 25 instructions and one LDS atomic for every
+// element (67 MB at 2.7 TB/s; neither the issue nor the atomics leave room), and
+// the finish 43, of which listing an element in 15 to 40 takes 11 to 19 and
+// each search up to 9.
 #include "qmm_device.hpp"
 #include "qmm_kernels.hpp"
 #include "qmm_step.hpp"
@@ -56,7 +65,10 @@ constexpr int kMaxSlice = 1 << 17;   // elements of a slice: the packed number h
 constexpr int kGatherMin = 1 << 16;
 constexpr int kMaxSlices = 64;
 constexpr int kSliceList = 1024;     // listed elements of a slice
-constexpr int kList = 8192;          // listed elements of a row
+// Listed elements of a row, as many as the LDS takes: of 16 batches of 256 rows
+// (131072 bf16 logits, top-p 0.95) six had a row with more than 8192, which cost
+// a pass for each search (87 us instead of 68).
+constexpr int kList = 11264;
 constexpr int kParts = 512;          // parts of a bin
 constexpr int kRanked = 1024;        // elements that are ranked by pairs
 constexpr int kWhole = 64;           // a bin of up to this many is ranked as it is
