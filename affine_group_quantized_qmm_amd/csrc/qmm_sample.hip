@@ -927,6 +927,83 @@ __device__ __forceinline__ bool find_listed(Finish<THREADS> &f, int t, int top_b
     return true;
 }
 
+// All searches by one wave, without a barrier, of a list of up to 64 elements, one
+// a lane (16 rows of 151001 logits with top-k and top-p: 26 us a call, 28 without
+// it). Sets f.key and f.nth, the kept mass and the token's bin.
+template <int THREADS>
+__device__ __forceinline__ void search_few(Finish<THREADS> &f, const RowParams &p, int top_bin, double top_scaled,
+                                           double &kept, int &t)
+{
+    const int lane = threadIdx.x;
+    const Search find(f.sums);
+    const bool mine = lane < (int)f.listed;
+    const Entry e = f.list[mine ? lane : 0];
+    const double scale = scaled<false>(e.x, p.per_unit, 0.f);
+    const Binned b = binned(scale);
+    const int below = mine && scale > top_scaled - kBins - 1 ? top_bin - b.bin : -1;
+    const uint64_t place = (uint64_t)order_key(e.x) << 32 | (uint32_t)~e.index;
+    const uint32_t weight = 2147483648u + (uint32_t)b.q;
+    double limit = kept;
+#pragma unroll 1
+    for (int query = kTopK; query <= kToken; ++query) {
+        uint32_t count = 0;
+        double value = 0.0;
+        if (query == kTopK) {
+            t = p.top_k > 0 ? find.first_count(p.top_k) : kBins;
+            if (t == kBins)
+                continue;
+            count = p.top_k - count_before(f.sums, t);
+        } else if (query == kMinP) {
+            t = min_p_bin(p, top_scaled);
+            if (t < 0)
+                continue;
+        } else {
+            if (query == kTopP && !(p.top_p < 1.0))
+                continue;
+            const double target = query == kTopP ? p.top_p * limit : p.u * kept;
+            t = query == kTopP ? find.template first_mass<false>(target) : find.template first_mass<true>(target);
+            value = (target - mass_before(f.sums, t)) / f.factor[t];
+            const double least = query == kTopP ? 0.5 : 0.0;
+            value = value > least ? value : least;
+        }
+        unsigned long long mass;
+        if (query == kMinP) {
+            mass = below == t && (scale - top_scaled) / kPerUnit >= p.log_min_p ? weight : 0u;
+            mass = of_lane(wave_sums(mass), kWave - 1);
+        } else {
+            const uint64_t bin = __ballot(below == t);
+            const uint32_t n = __popcll(bin);
+            uint32_t c = 0;
+            unsigned long long from = 0;
+            for (uint64_t left = bin; left; left &= left - 1) {
+                const int j = __builtin_ctzll(left);
+                const bool earlier = of_lane(place, j) > place;
+                const uint32_t other = of_lane(weight, j);
+                c += earlier ? 1u : 0u;
+                from += earlier ? other : 0u;
+            }
+            const bool here = crosses(query, c, from, 1, weight, count, value);
+            const bool none = c + 1 == n && (query == kTopK   ? n < count
+                                             : query == kTopP ? (double)(from + weight) < value
+                                                              : (double)(from + weight) <= value);
+            const uint64_t found = __ballot(below == t && (here || none));
+            const int who = found ? __builtin_ctzll(found) : 0;  // one is, as no bin with a crossing is empty
+            mass = of_lane(from + weight, who);
+            const uint64_t chosen = of_lane(place, who);
+            if (lane == 0) {
+                f.key = (uint32_t)(chosen >> 32);
+                f.nth = ~(uint32_t)chosen;
+            }
+        }
+        if (query != kToken) {
+            const double m = mass_before(f.sums, t) + (double)mass * f.factor[t];
+            kept = m < kept ? m : kept;
+            if (query == kTopK)
+                limit = kept;
+        }
+    }
+}
+
 // Smallest and largest value and number of the elements that pass.
 template <int THREADS, typename Each>
 __device__ __forceinline__ void range_of(Finish<THREADS> &f, Each each)
@@ -1129,11 +1206,14 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
     const int top_bin = binned(top_scaled).bin;
     // Elements of the wanted bins: of all searches at once, from the gather or
     // (one slice) listed below; where these are too many, of one search at a time.
-    Wanted w{-1, 0, -1, -1, 0, -1};
-    bool listed = fine, list_now = false, one_by_one = false;
+    Wanted w;
+    bool listed = fine, one_by_one = false;
     if (fine && kLists) {
         w = wanted_bins(f.sums, p, top_scaled);
-        list_now = true;
+        list_wanted(x, 0, a.V, THREADS, p.per_unit, top_bin, w, &f.listed, f.places, kList, f.list);
+        __syncthreads();
+        one_by_one = f.listed > kList;
+        __syncthreads();
     } else if (fine) {
         const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
         const uint32_t own = lane < S ? head_of(slice_at(a, row, lane, S))->listed : 0;
@@ -1182,7 +1262,14 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
     // The searches, in the order of the filters.
     double kept = f.sums.mass[kBins - 1], limit = kept;  // mass kept so far; of the top-k prefix
     int t = 0;
-    for (int query = kTopK; query <= kToken; ++query) {
+    bool few = false;
+    if (fine && !one_by_one && f.listed <= kWave) {
+        if (threadIdx.x >= kWave)
+            return;
+        search_few(f, p, top_bin, top_scaled, kept, t);
+        few = true;
+    }
+    for (int query = few ? kToken + 1 : kTopK; query <= kToken; ++query) {
         const Search find(f.sums);  // read again: held over the turns, its 18 registers would spill
         uint32_t count = 0;
         double value = 0.0;
@@ -1206,24 +1293,15 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
             const double least = query == kTopP ? 0.5 : 0.0;
             value = value > least ? value : least;
         }
-        for (bool again = true; again;) {
-            again = false;
-            if (one_by_one) {
-                w = Wanted{t, 0, -1, -1, 0, -1};
-                list_now = true;
-            }
-            if (list_now) {
-                if (threadIdx.x == 0)
-                    f.listed = 0;
-                __syncthreads();
-                list_wanted(x, 0, a.V, THREADS, p.per_unit, top_bin, w, &f.listed, f.places, kList, f.list);
-                __syncthreads();
-                listed = f.listed <= kList;
-                again = !listed && !one_by_one;
-                one_by_one |= !listed;
-                list_now = false;
-                __syncthreads();
-            }
+        if (one_by_one) {
+            if (threadIdx.x == 0)
+                f.listed = 0;
+            __syncthreads();
+            w = Wanted{t, 0, -1, -1, 0, -1};
+            list_wanted(x, 0, a.V, THREADS, p.per_unit, top_bin, w, &f.listed, f.places, kList, f.list);
+            __syncthreads();
+            listed = f.listed <= kList;
+            __syncthreads();
         }
         bool done = false;
         if (listed)
