@@ -27,6 +27,8 @@
 // cumulative sum of n similar tokens by 2^-28 / sqrt(n) of itself, which moves
 // a token only if u falls within that of a border.
 //
+// Many rows of bf16 logits take another way, by their values (see there).
+//
 // Rows whose maximum lies outside the histogram's range (|z| of 500, or an
 // infinity) are counted again relative to their maximum by the finishing
 // workgroup alone, as are rows whose list overflows (thousands of equal
@@ -36,13 +38,12 @@
 // few rows still fill the GPU.
 //
 // What bounds it. Few rows: two or three launches one after the other, each with
-// its code to fetch: one row of 131072 fp32 logits takes 19 us (histogram 4,
-// gather 9, finish 6), 16 rows with top-k and top-p 27, 32 rows of 32003 fp16
-// logits 24. 256 rows of 131072 bf16 logits with top-p take 68 us: the histogram
-// 25, for which a CU issues 25 instructions and one LDS atomic for every
-// element (67 MB at 2.7 TB/s; neither the issue nor the atomics leave room), and
-// the finish 43, of which listing an element in 15 to 40 takes 11 to 19 and
-// each search up to 9.
+// its code to fetch: one row of 131072 fp32 logits takes 18 us (histogram 4,
+// gather 8, finish 5), 16 rows with top-k and top-p 25, 32 rows of 32003 fp16
+// logits 24. 256 rows of 131072 fp32 logits with top-p take 73 us: the histogram
+// 25, for which a CU issues 20 instructions and one LDS atomic for every
+// element, and the finish, of which listing an element in 15 to 40 takes 11 to
+// 19 and each search up to 9.
 #include "qmm_device.hpp"
 #include "qmm_kernels.hpp"
 #include "qmm_step.hpp"
@@ -1332,6 +1333,446 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows of bf16 logits: one workgroup a row and no bins. A row has at most
+// 65536 different logits, so that their numbers fit the LDS; the filters and the
+// token's logit follow from sums over the values in falling order, and one more
+// pass finds which of the equal ones the token is. Counting takes 4 instructions
+// an element where the histogram of bins takes 20, and nothing is listed: 256
+// rows of 131072 logits with top-p take 39 us, by bins 68 (counting 10, the values'
+// sums 9, searches 7, the last pass 9). In fp16, whose values near zero lie four
+// times as densely, the sums take 30 and the call 62 (by bins 46).
+// ---------------------------------------------------------------------------
+constexpr int kWords = 1 << 15;                // of counts: by magnitude; positive logits in the low half, negative in the high
+constexpr int kGroups = 2 * kWords / kWave;    // of 64 values in falling order: positive ones from the largest, then negative ones
+
+constexpr uint32_t kInfinity = 0x7F80;
+
+__device__ __forceinline__ float value_of(uint32_t bits) { return __builtin_bit_cast(float, bits << 16); }
+
+struct Values {
+    uint32_t counts[kWords];
+    double mass[kGroups];       // of the groups up to and with each
+    uint32_t count[kGroups];
+    WaveSums<double> waves;
+    uint32_t seen[kScanThreads / kWave];
+    uint32_t first;             // place of the largest logit in falling order
+    uint32_t heavy[2], heavy_count[2], heavies;  // logits of more than 65535 elements, which have no place in `counts`
+    uint32_t bits, nth, index;  // the token's logit, which of the equal ones, and where it stands
+};
+
+// Bits of the logit at a place in falling order (0: the largest), and how many
+// elements have it; none for NaN and -inf. -0 counts as 0.
+__device__ __forceinline__ uint32_t bits_at(uint32_t place) { return place < kWords ? kWords - 1 - place : place; }
+__device__ __forceinline__ uint32_t count_at(const Values &f, uint32_t place, uint32_t heavies)
+{
+    const uint32_t bits = bits_at(place), word = bits & (kWords - 1);
+    const uint32_t w = f.counts[word];
+    const bool negative = place >= kWords;
+    uint32_t c = negative ? w >> 16 : w & 0xFFFFu;
+    if (word == 0)
+        c = negative ? 0u : c + (w >> 16);
+    for (uint32_t k = 0; k < heavies; ++k) {
+        const uint32_t h = f.heavy[k] == 0x8000u ? 0u : f.heavy[k];
+        c += h == bits ? f.heavy_count[k] : 0u;
+    }
+    return word < kInfinity || (word == kInfinity && !negative) ? c : 0u;
+}
+
+// Scaled logit relative to the largest one.
+__device__ __forceinline__ double below_top(float x, float top, double per_unit, bool fine)
+{
+    return fine ? (double)x * per_unit - (double)top * per_unit : scaled<true>(x, per_unit, top);
+}
+
+// e^(d/8) for d of -384 .. 0, exactly 1 for 0: 2^n times the series of e^r, |r| up to
+// ln 2 / 2, whose first term left out is below 2^-41 (a library's exponential,
+// good to the last bit, is three times the code).
+__device__ __forceinline__ double exp_eighth(double d)
+{
+    const double n = rint(d * 0.18033688011112042);             // log2(e) / 8
+    const double r = __builtin_fma(n, -5.5451774444795623, d) * 0.125;  // 8 ln 2
+    double e = 1.0 / 3628800.0;
+    constexpr double inverse[10] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880};
+#pragma unroll
+    for (int k = 9; k >= 0; --k)
+        e = __builtin_fma(e, r, inverse[k]);
+    return __builtin_ldexp(e, (int)n);
+}
+
+// The lanes' values of a group: how many elements, and their mass each.
+__device__ __forceinline__ void group_at(const Values &f, uint32_t group, uint32_t heavies, float top, double per_unit, bool fine,
+                                         uint32_t &count, double &weight)
+{
+    const uint32_t place = group * kWave + threadIdx.x % kWave;
+    count = count_at(f, place, heavies);
+    const double d = below_top(value_of(bits_at(place)), top, per_unit, fine);
+    if (!(d > 1 - kBins))  // e^-48 of the largest, as above; NaN where infinity times 0 is
+        count = 0;
+    weight = count ? exp_eighth(d) : 0.0;
+}
+
+__device__ __forceinline__ void count_values(Values &f, const uint16_t *bits, int V)
+{
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const Span s = span_of_row(bits, 0, V, 2);
+    auto add = [&](uint32_t b) { atomicAdd(&f.counts[b & (kWords - 1)], b & 0x8000u ? 0x10000u : 1u); };
+    if ((int)threadIdx.x < s.body)
+        add(bits[threadIdx.x]);
+    if ((int)threadIdx.x < V - s.tail)
+        add(bits[s.tail + threadIdx.x]);
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(bits + s.body);
+    constexpr int UNROLL = 4;
+    for (int i = threadIdx.x; i < s.units; i += UNROLL * kScanThreads) {
+        u32x4 v[UNROLL];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j)
+            v[j] = p[i + j * kScanThreads < s.units ? i + j * kScanThreads : i];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j)
+            if (i + j * kScanThreads < s.units)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    add(v[j][e] & 0xFFFFu);
+                    add(v[j][e] >> 16);
+                }
+    }
+}
+
+// For rows with a logit of more than 65535 elements (two at most): which they are,
+// by their high and then their low bytes, and the counts without them.
+__device__ __forceinline__ void count_without_heavy(Values &f, const uint16_t *row, int V)
+{
+    uint32_t high[2] = {0, 0};
+    for (int turn = 0; turn < 3; ++turn) {  // the high bytes; the low ones of up to two high ones
+        if (turn > 0 && high[turn - 1] == 0)
+            break;
+        __syncthreads();
+        if (threadIdx.x < 256)
+            f.counts[threadIdx.x] = 0;
+        __syncthreads();
+        const uint32_t of = turn > 0 ? high[turn - 1] - 1 : 0;
+        for_elements<uint16_t, 1>(row, 0, V, kScanThreads, [&](float x, int) {
+            const uint32_t b = (uint32_t)x;
+            if (turn == 0 || b >> 8 == of)
+                atomicAdd(&f.counts[turn == 0 ? b >> 8 : b & 255], 1u);
+        });
+        __syncthreads();
+        for (uint32_t b = 0; b < 256; ++b)  // by all threads alike
+            if (f.counts[b] > 65535u) {
+                if (turn == 0) {
+                    high[high[0] ? 1 : 0] = b + 1;
+                } else if (threadIdx.x == 0) {
+                    f.heavy[f.heavies] = of << 8 | b;
+                    f.heavy_count[f.heavies++] = f.counts[b];
+                }
+            }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kWords; i += kScanThreads)
+        f.counts[i] = 0;
+    const uint32_t n = f.heavies, h0 = n > 0 ? f.heavy[0] : 0x10000u, h1 = n > 1 ? f.heavy[1] : 0x10000u;
+    __syncthreads();
+    for_elements<uint16_t, 1>(row, 0, V, kScanThreads, [&](float x, int) {
+        const uint32_t b = (uint32_t)x;
+        if (b != h0 && b != h1)
+            atomicAdd(&f.counts[b & (kWords - 1)], b & 0x8000u ? 0x10000u : 1u);
+    });
+    __syncthreads();
+}
+
+// Which of a unit's (or a single) elements have the bits looked for: `mask`
+// leaves out the sign where they are 0.
+__device__ __forceinline__ uint32_t hits_of(uint32_t w, uint32_t mask, uint32_t both)
+{
+    const uint32_t e = (w & mask) ^ both;
+    return ((e & 0xFFFFu) == 0 ? 1u : 0u) + (e < 0x10000u ? 2u : 0u);
+}
+
+// Where the nth (1, 2, ...) element of the given bits stands. Each wave counts
+// those of a sixteenth of the row's whole units of 16 bytes; then every thread
+// looks at one unit of the sixteenth that holds it.
+__device__ __forceinline__ void find_nth(Values &f, const uint16_t *row, int V)
+{
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    constexpr int WAVES = kScanThreads / kWave;
+    static_assert(kMaxSlice / 8 <= WAVES * kScanThreads, "a sixteenth has a unit for each thread at most");
+    const uint32_t wanted = f.bits, mask = wanted ? 0xFFFFFFFFu : 0x7FFF7FFFu, both = wanted << 16 | wanted;
+    const Span s = span_of_row(row, 0, V, 2);
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + s.body);
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int share = (s.units + WAVES - 1) / WAVES;
+    const int begin = wave * share < s.units ? wave * share : s.units;
+    const int end = begin + share < s.units ? begin + share : s.units;
+    uint32_t c = 0;
+    constexpr int UNROLL = 8;
+    for (int i = begin + lane; i < end; i += UNROLL * kWave) {
+        u32x4 v[UNROLL];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j)
+            v[j] = p[i + j * kWave < end ? i + j * kWave : i];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            uint32_t h = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t d = (v[j][e] & mask) ^ both;
+                h += (d & 0xFFFFu) == 0 ? 1u : 0u;
+                h += d < 0x10000u ? 1u : 0u;
+            }
+            c += i + j * kWave < end ? h : 0u;
+        }
+    }
+    // the single elements before the units and behind them
+    const bool head = (int)threadIdx.x < s.body && ((row[threadIdx.x] & mask) ^ wanted) == 0;
+    const uint32_t heads = __popcll(__ballot(head));  // wave 0's: the fewer than 8 first lanes
+    c = of_lane(wave_sums(c), kWave - 1);
+    if (lane == 0)
+        f.seen[wave] = c;
+    if (threadIdx.x == 0)
+        f.count[0] = heads;
+    __syncthreads();
+    uint32_t nth = f.nth;
+    const uint32_t before = f.count[0];
+    if (nth <= before) {
+        if (head && (uint32_t)__popcll(__ballot(head) & (((uint64_t)2 << lane) - 1)) == nth)
+            f.index = threadIdx.x;
+        return;
+    }
+    nth -= before;
+    int in = 0;
+    for (; in < WAVES && nth > f.seen[in]; ++in)
+        nth -= f.seen[in];
+    if (in == WAVES) {  // behind the units
+        const bool tail = (int)threadIdx.x < V - s.tail && ((row[s.tail + threadIdx.x] & mask) ^ wanted) == 0;
+        if (tail && (uint32_t)__popcll(__ballot(tail) & (((uint64_t)2 << lane) - 1)) == nth)
+            f.index = s.tail + threadIdx.x;
+        return;
+    }
+    const int unit = in * share + (int)threadIdx.x;
+    uint32_t hits = 0;
+    if ((int)threadIdx.x < share && unit < s.units) {
+        const u32x4 v = p[unit];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            hits |= hits_of(v[e], mask, both) << 2 * e;
+    }
+    const uint32_t mine = __popc(hits);
+    uint32_t upto = mine;
+    double none = 0.0;
+    block_sums<kScanThreads>(upto, none, f.waves);
+    if (nth > upto - mine && nth <= upto) {
+        for (uint32_t k = upto - mine + 1; k < nth; ++k)
+            hits &= hits - 1;
+        f.index = s.body + 8 * unit + __builtin_ctz(hits);
+    }
+}
+
+__global__ __launch_bounds__(kScanThreads) void sample_values_kernel(const SampleArgs a)
+{
+    __shared__ Values f;
+    constexpr int WAVES = kScanThreads / kWave;
+    const int row = blockIdx.x, lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint16_t *x = static_cast<const uint16_t *>(a.logits) + row * a.row_stride;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    for (int i = threadIdx.x; i < kWords / 4; i += kScanThreads)
+        reinterpret_cast<u32x4 *>(f.counts)[i] = u32x4{0, 0, 0, 0};
+    if (threadIdx.x == 0) {
+        f.heavies = 0;
+        f.first = 0xFFFFFFFFu;
+    }
+    const RowParams p = params_of(a, row);
+    __syncthreads();
+    count_values(f, x, a.V);
+    __syncthreads();
+    // Both halves' groups of a word's 64 go to one wave. The sum of all counts
+    // tells whether one passed 65535: each time takes 65535 or 65536 off.
+    uint32_t sum = 0, used = 0;  // bit j: group wave + 16 j has elements
+    for (int j = 0; j < kWords / kWave / WAVES; ++j) {
+        const uint32_t w = f.counts[(wave + WAVES * j) * kWave + lane];
+        sum += (w & 0xFFFFu) + (w >> 16);
+        used |= __any(w != 0) ? 1u << j : 0u;
+    }
+    sum = of_lane(wave_sums(sum), kWave - 1);
+    if (lane == 0)
+        f.seen[wave] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int j = 0; j < WAVES; ++j)
+        sum += f.seen[j];
+    if (__builtin_expect(sum != (uint32_t)a.V, 0)) {
+        count_without_heavy(f, x, a.V);
+        used = 0xFFFFFFFFu;
+    }
+    const uint32_t heavies = f.heavies;
+    // The largest logit: the first place in falling order that has elements.
+    uint32_t first = 0xFFFFFFFFu;
+    for (uint32_t left = used; left; left &= left - 1) {  // the highest group last
+        const uint32_t place = kWords - (wave + WAVES * __builtin_ctz(left) + 1) * kWave + lane;
+        first = count_at(f, place, heavies) ? place : first;
+    }
+    if (!__any(first != 0xFFFFFFFFu))
+        for (uint32_t left = used; left; left &= ~(0x80000000u >> __builtin_clz(left))) {  // the lowest group last
+            const uint32_t place = kWords + (wave + WAVES * (31 - __builtin_clz(left))) * kWave + lane;
+            first = count_at(f, place, heavies) ? place : first;
+        }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t o = __shfl_xor(first, d);
+        first = o < first ? o : first;
+    }
+    if (lane == 0)
+        atomicMin(&f.first, first);
+    for (int i = threadIdx.x; i < kGroups; i += kScanThreads) {
+        f.mass[i] = 0.0;
+        f.count[i] = 0;
+    }
+    __syncthreads();
+    first = f.first;
+    if (first == 0xFFFFFFFFu) {  // no logit above -inf
+        if (threadIdx.x == 0) {
+            a.tokens[row] = -1;
+            if (a.logprobs)
+                a.logprobs[row] = -__builtin_inff();
+        }
+        return;
+    }
+    const float top = value_of(bits_at(first));
+    const bool fine = in_range(top, p.per_unit);
+    // Each group's number and mass.
+    for (int half = 0; half < 2; ++half)
+        for (uint32_t left = used; left; left &= left - 1) {
+            const uint32_t words = wave + WAVES * __builtin_ctz(left);
+            const uint32_t group = half ? kGroups / 2 + words : kGroups / 2 - 1 - words;
+            uint32_t count;
+            double weight;
+            group_at(f, group, heavies, top, p.per_unit, fine, count, weight);
+            if (!__any(count != 0))
+                continue;
+            const uint32_t c = wave_sums(count);
+            const double m = wave_sums((double)count * weight);
+            if (lane == kWave - 1) {
+                f.count[group] = c;
+                f.mass[group] = m;
+            }
+        }
+    __syncthreads();
+    static_assert(kGroups == kScanThreads, "a thread a group");
+    uint32_t gc = f.count[threadIdx.x];
+    double gm = f.mass[threadIdx.x];
+    block_sums<kScanThreads>(gc, gm, f.waves);
+    f.count[threadIdx.x] = gc;
+    f.mass[threadIdx.x] = gm;
+    __syncthreads();
+
+    // The searches, by one wave: the group first (how many lie before the crossing),
+    // then the value inside it, then which of its elements.
+    double kept = 0.0, weight = 0.0;
+    if (wave == 0) {
+        kept = f.mass[kGroups - 1];
+        double limit = kept;
+#pragma unroll 1
+        for (int query = kTopK; query <= kToken; ++query) {
+            double value = 0.0;
+            uint32_t last = 0;  // of min-p: the places that pass
+            if (query == kTopK) {
+                if (p.top_k <= 0 || f.count[kGroups - 1] < (uint32_t)p.top_k)
+                    continue;
+            } else if (query == kTopP) {
+                if (!(p.top_p < 1.0))
+                    continue;
+                value = p.top_p * limit;
+                value = value > 0.5 ? value : 0.5;  // the first element has mass 1
+            } else if (query == kMinP) {
+                if (!(p.log_min_p > -1e299))
+                    continue;
+                for (uint32_t step = kGroups; step; step /= kWave) {  // of 1024, then 16, then 1 place
+                    const uint32_t place = last + step * lane;
+                    const bool passes = place < 2 * kWords &&
+                        (place <= first || below_top(value_of(bits_at(place)), top, p.per_unit, fine) / kPerUnit >= p.log_min_p);
+                    const uint64_t no = ~__ballot(passes);
+                    const uint32_t n = no ? __builtin_ctzll(no) : kWave;
+                    last += step * (n - 1);  // place 0 passes
+                    if (step == 16) {
+                        const uint32_t at = last + lane;
+                        const uint64_t out = ~__ballot(lane < 16 && at < 2 * kWords &&
+                            (at <= first || below_top(value_of(bits_at(at)), top, p.per_unit, fine) / kPerUnit >= p.log_min_p));
+                        last += __builtin_ctzll(out) - 1;
+                        break;
+                    }
+                }
+            } else {
+                value = p.u * kept;
+            }
+            uint32_t group = 0;
+            if (query == kMinP) {
+                group = last / kWave;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kGroups / kWave; ++j) {
+                    const uint32_t c = f.count[j * kWave + lane];
+                    const double m = f.mass[j * kWave + lane];
+                    group += __popcll(__ballot(query == kTopK ? c < (uint32_t)p.top_k : query == kTopP ? m < value : m <= value));
+                }
+                group = group < (uint32_t)kGroups ? group : kGroups - 1;
+                // past a border by a rounding: back to a group with elements
+                while (group && f.count[group] == f.count[group - 1])
+                    --group;
+            }
+            const uint32_t count_before = group ? f.count[group - 1] : 0u;
+            const double mass_before = group ? f.mass[group - 1] : 0.0;
+            uint32_t count;
+            double w;
+            group_at(f, group, heavies, top, p.per_unit, fine, count, w);
+            const double own = (double)count * w, upto = wave_sums(own);
+            const uint32_t number = wave_sums(count);
+            const uint64_t some = __ballot(count != 0);
+            if (query == kMinP) {
+                const double m = mass_before + of_lane(upto, last % kWave);
+                kept = m < kept ? m : kept;
+                continue;
+            }
+            const uint64_t over = some & __ballot(query == kTopK   ? count_before + number >= (uint32_t)p.top_k
+                                                  : query == kTopP ? mass_before + upto >= value
+                                                                   : mass_before + upto > value);
+            // rounding at the group's end: its last value
+            const int who = over ? __builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : 0;
+            const double before = mass_before + (upto - own), left = (value - before) / w;
+            uint32_t nth = 0;
+            if (query == kTopK) {
+                nth = p.top_k - (count_before + number - count);
+            } else {
+                const double n = query == kTopP ? ceil(left) : floor(left) + 1.0;
+                nth = n < 1.0 ? 1u : n < (double)count ? (uint32_t)n : count;
+            }
+            const double m = of_lane(before + (double)nth * w, who);
+            if (query == kToken) {
+                weight = of_lane(w, who);
+                const uint32_t j = of_lane(nth, who);
+                if (lane == 0) {
+                    f.bits = bits_at(group * kWave + who);
+                    f.nth = j;
+                }
+            } else {
+                kept = m < kept ? m : kept;
+                if (query == kTopK)
+                    limit = kept;
+            }
+        }
+    }
+    __syncthreads();
+    find_nth(f, x, a.V);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a.tokens[row] = (int32_t)f.index;
+        if (a.logprobs) {
+            const double lp = log(weight / kept);
+            a.logprobs[row] = lp < 0.0 ? (float)lp : 0.f;
+        }
+    }
+}
+
 // Slices of a row: enough workgroups to fill the GPU (64 rows of 131072 logits:
 // 34 us a call; with half as many 42, with twice as many 36), none with fewer
 // than 8 elements for each thread (one such row: 22.9 us; with 4 or 16 elements
@@ -1346,9 +1787,23 @@ int slices_of(int M, int V)
     return s > least ? s : least > 1 ? least : 1;
 }
 
+// Whether rows of bf16 logits are taken by their values: where they fill the GPU
+// and the fixed 20 us of a row pay (us by bins and by values, with top-k 50 and
+// top-p 0.9, then without top-k):
+//   64 x 131072   31 : 34,  46 : 33        128 x 32000   21 : 25,  27 : 24
+//   256 x 32000   25 : 25,  31 : 25        512 x  8000   33 : 43,  41 : 42
+//   256 x 131072  47 : 40,  59 : 39
+bool by_values(int M, int V) { return V >= 1 << 14 && V <= kMaxSlice && (int64_t)M * V >= 6 << 20; }
+
 template <typename T>
 hipError_t launch(const SampleArgs &a, hipStream_t stream)
 {
+    if constexpr (__is_same(T, __bf16)) {
+        if (by_values(a.M, a.V)) {
+            sample_values_kernel<<<dim3(a.M), kScanThreads, 0, stream>>>(a);
+            return hipGetLastError();
+        }
+    }
     const int S = slices_of(a.M, a.V);
     sample_histogram_kernel<T><<<dim3(S, a.M), kScanThreads, 0, stream>>>(a, S);
     hipError_t e = hipGetLastError();

@@ -32,9 +32,9 @@ def sample(x, u, T=None, k=None, p=None, mp=None):
     return tok.cpu().numpy(), lp.cpu().numpy()
 
 
-def check(x, u, T=None, k=None, p=None, mp=None, borders=False):
+def check(x, u, T=None, k=None, p=None, mp=None, borders=False, most_near=None):
     """`borders`: the inputs put u or p exactly on borders, and the answer there
-    is exact in both forms."""
+    is exact in both forms. `most_near`: how many rows the inputs put near one."""
     got, lp = sample(x, u, T, k, p, mp)
     M = x.shape[0]
 
@@ -53,7 +53,8 @@ def check(x, u, T=None, k=None, p=None, mp=None, borders=False):
         else:
             # weights and their sum to 2^-28 each, one rounding
             assert abs(float(lp[i]) - want_lp) <= 2.0 ** -27 + abs(want_lp) * 2.0 ** -24, f"row {i}: {lp[i]} {want_lp}"
-    assert near <= max(1, M // 20), f"{near} of {M} rows near a border"
+    assert near <= max(1, M // 20 if most_near is None else most_near), f"{near} of {M} rows near a border"
+    return got, lp
 
 
 def logits(M, V, dtype, seed, spread=3.0):
@@ -242,3 +243,78 @@ def test_graph_replays_reruns_and_streams(M, V):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(tok, eager) and torch.equal(lp, eager_lp), f"replay {rep}"
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heavy", [(0.0,), (-3.0,), (0.0, -0.0), (1.5, 1.25), ("lowest",), (2.0, "-inf")], ids=str)
+def test_logits_of_more_than_65535_elements(heavy, dtype):
+    """One or two logits fill most of a row, as the largest, among the others or far below."""
+    M, V = 48, 131072
+    x = logits(M, V, dtype, 1)
+    x[::2] = logits(M // 2, V, dtype, 2, 1.0)
+    g = torch.Generator().manual_seed(10)
+    for i in range(M):
+        order, at = torch.randperm(V, generator=g), 0
+        for h in heavy:
+            value = torch.finfo(dtype).min if h == "lowest" else float(h)
+            n = [65536, 100000, V][i % 3] if len(heavy) == 1 else [65536, 65535, 66000][i % 3]
+            x[i, order[at:at + n]] = value
+            at += n
+    u, T, k = uniform(M, 3), np.tile([1.0, 0.7, 1.3, 1.0, 1.0, 0.7], 8), np.tile([0, 0, 60000, 70000, 100, 0], 8)
+    p, mp = np.tile([1.0, 0.9, 0.95, 1.0, 1.0, 0.5], 8), np.tile([0.0, 0.0, 0.0, 0.1, 0.0, 0.0], 8)
+    tok, lp = check(x, u, T, k, p, mp, most_near=M // 6)  # half of equal logits is a border: every sixth row
+    if len(heavy) == 1:
+        for i in range(5, M, 6):  # the first half by index, and u takes its place in it
+            assert tok[i] == int(np.floor(np.float64(u[i]) * (V // 2)))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("M,V", [(24, 1), (24, 17), (24, 9001), (24, 131073), (400, 16384), (100, 65001), (49, 131071),
+                                 (48, 131072)])
+def test_16_bit_rows_of_every_alignment(M, V, dtype):
+    """Rows whose first elements lie at every distance from 16 bytes; tokens among equal logits by their index."""
+    x = torch.empty(M, V + 3, dtype=dtype)[:, :V]
+    x.copy_(logits(M, V, dtype, V, 2.0))
+    g = torch.Generator().manual_seed(V)
+    x[::3] = torch.randint(0, 3, x[::3].shape, generator=g).to(dtype)
+    check(x, uniform(M, V), k=np.resize([0, 3, 700], M), p=np.resize([1.0, 0.9, 1.0, 0.6], M),
+          mp=np.resize([0.0] * 20 + [0.3] * 4, M))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_many_16_bit_rows_of_all_kinds(dtype):
+    """Masks, infinities, NaN, zeros of both signs, extreme temperatures and parameters, in one call of many rows."""
+    M, V = 400, 16389
+    x = logits(M, V, dtype, 5)
+    inf, low = float("inf"), torch.finfo(dtype).min
+    g = torch.Generator().manual_seed(6)
+    some = torch.rand(M, V, generator=g) < 0.9
+    T = np.ones(M)
+    k, p, mp = np.zeros(M, int), np.ones(M), np.zeros(M)
+    for i in range(M):
+        kind = i % 20
+        if kind in (1, 2, 3):
+            x[i, some[i]] = [-inf, low, float("nan")][kind - 1]
+        elif kind == 4:
+            x[i] = -inf
+        elif kind == 5:
+            x[i], x[i, 77] = -inf, -5.0
+        elif kind == 6:
+            x[i, 5::1000] = inf
+        elif kind == 7:
+            x[i], x[i, ::2] = -1.0, -0.0
+            x[i, 1::4] = 0.0
+        elif kind == 8:
+            x[i] = float("nan")
+        elif kind == 9:
+            x[i] = low
+        elif kind == 10:
+            x[i] = x[i] * 1000
+        elif kind == 11:
+            x[i] = x[i] * 2.0 ** -12
+        T[i] = {12: 1e-30, 13: 0.004, 14: 50.0, 15: 1e6, 16: inf, 17: 0.0, 18: -1.0}.get(kind, 1.0)
+        j = i // 20
+        k[i] = [0, 1, 50, V, 2 * V][j % 5]
+        p[i] = [1.0, 0.9, 0.5, 0.0][j % 4]
+        mp[i] = [0.0, 0.05, 1.0][j % 3]
+    check(x, uniform(M, 7), T=T, k=k, p=p, mp=mp)
