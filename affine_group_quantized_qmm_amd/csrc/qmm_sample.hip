@@ -1608,15 +1608,17 @@ __global__ __launch_bounds__(kScanThreads) void sample_values_kernel(const Sampl
     const uint32_t heavies = f.heavies;
     // The largest logit: the first place in falling order that has elements.
     uint32_t first = 0xFFFFFFFFu;
-    for (uint32_t left = used; left; left &= left - 1) {  // the highest group last
-        const uint32_t place = kWords - (wave + WAVES * __builtin_ctz(left) + 1) * kWave + lane;
+    bool found = false;
+    for (uint32_t left = used; left && !found; left &= ~(0x80000000u >> __builtin_clz(left))) {  // positive ones from the largest
+        const uint32_t place = kWords - (wave + WAVES * (31 - __builtin_clz(left)) + 1) * kWave + lane;
         first = count_at(f, place, heavies) ? place : first;
+        found = __any(first != 0xFFFFFFFFu);
     }
-    if (!__any(first != 0xFFFFFFFFu))
-        for (uint32_t left = used; left; left &= ~(0x80000000u >> __builtin_clz(left))) {  // the lowest group last
-            const uint32_t place = kWords + (wave + WAVES * (31 - __builtin_clz(left))) * kWave + lane;
-            first = count_at(f, place, heavies) ? place : first;
-        }
+    for (uint32_t left = used; left && !found; left &= left - 1) {  // negative ones from the smallest
+        const uint32_t place = kWords + (wave + WAVES * __builtin_ctz(left)) * kWave + lane;
+        first = count_at(f, place, heavies) ? place : first;
+        found = __any(first != 0xFFFFFFFFu);
+    }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
         const uint32_t o = __shfl_xor(first, d);
@@ -1709,12 +1711,15 @@ __global__ __launch_bounds__(kScanThreads) void sample_values_kernel(const Sampl
             if (query == kMinP) {
                 group = last / kWave;
             } else {
-#pragma unroll
-                for (int j = 0; j < kGroups / kWave; ++j) {
-                    const uint32_t c = f.count[j * kWave + lane];
-                    const double m = f.mass[j * kWave + lane];
-                    group += __popcll(__ballot(query == kTopK ? c < (uint32_t)p.top_k : query == kTopP ? m < value : m <= value));
-                }
+                auto below = [&](uint32_t at) {
+                    return query == kTopK   ? f.count[at] < (uint32_t)p.top_k
+                           : query == kTopP ? f.mass[at] < value
+                                            : f.mass[at] <= value;
+                };
+                constexpr uint32_t BLOCKS = kGroups / kWave;  // of 64 groups, first by their ends
+                uint32_t block = __popcll(__ballot(lane < (int)BLOCKS && below(lane % BLOCKS * kWave + kWave - 1)));
+                block = block < BLOCKS ? block : BLOCKS - 1;
+                group = block * kWave + __popcll(__ballot(below(block * kWave + lane)));
                 group = group < (uint32_t)kGroups ? group : kGroups - 1;
                 // past a border by a rounding: back to a group with elements
                 while (group && f.count[group] == f.count[group - 1])
