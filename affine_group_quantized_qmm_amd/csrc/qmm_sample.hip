@@ -1358,6 +1358,7 @@ struct Values {
     uint32_t seen[kScanThreads / kWave];
     uint32_t first;             // place of the largest logit in falling order
     uint32_t heavy[2], heavy_count[2], heavies;  // logits of more than 65535 elements, which have no place in `counts`
+    uint32_t numbers[2][kWave];
     uint32_t bits, nth, index;  // the token's logit, which of the equal ones, and where it stands
 };
 
@@ -1481,91 +1482,88 @@ __device__ __forceinline__ void count_without_heavy(Values &f, const uint16_t *r
     __syncthreads();
 }
 
-// Which of a unit's (or a single) elements have the bits looked for: `mask`
-// leaves out the sign where they are 0.
+// Which of a word's two elements have the bits looked for: `mask` leaves out the
+// sign where they are 0.
 __device__ __forceinline__ uint32_t hits_of(uint32_t w, uint32_t mask, uint32_t both)
 {
     const uint32_t e = (w & mask) ^ both;
     return ((e & 0xFFFFu) == 0 ? 1u : 0u) + (e < 0x10000u ? 2u : 0u);
 }
 
-// Where the nth (1, 2, ...) element of the given bits stands. Each wave counts
-// those of a sixteenth of the row's whole units of 16 bytes; then every thread
-// looks at one unit of the sixteenth that holds it.
+// Where the nth (1, 2, ...) element of the given bits stands: 4096 units of 16
+// bytes at a time, in order, until it is among them (the next ones on their way).
 __device__ __forceinline__ void find_nth(Values &f, const uint16_t *row, int V)
 {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    constexpr int WAVES = kScanThreads / kWave;
-    static_assert(kMaxSlice / 8 <= WAVES * kScanThreads, "a sixteenth has a unit for each thread at most");
+    constexpr int WAVES = kScanThreads / kWave, TURN = 4;
+    static_assert(TURN * WAVES == kWave, "a wave's lanes look at all numbers of a turn");
+    uint32_t nth = f.nth;
     const uint32_t wanted = f.bits, mask = wanted ? 0xFFFFFFFFu : 0x7FFF7FFFu, both = wanted << 16 | wanted;
     const Span s = span_of_row(row, 0, V, 2);
     const u32x4 *p = reinterpret_cast<const u32x4 *>(row + s.body);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int share = (s.units + WAVES - 1) / WAVES;
-    const int begin = wave * share < s.units ? wave * share : s.units;
-    const int end = begin + share < s.units ? begin + share : s.units;
-    uint32_t c = 0;
-    constexpr int UNROLL = 8;
-    for (int i = begin + lane; i < end; i += UNROLL * kWave) {
-        u32x4 v[UNROLL];
+    // Single elements before the units and behind them, fewer than 8: by every wave alike.
+    auto single = [&](int begin, int end) {
+        const bool hit = begin + lane < end && ((row[begin + lane] & mask) ^ (wanted & mask)) == 0;
+        const uint64_t hits = __ballot(hit);
+        if (hit && (uint32_t)__popcll(hits & (((uint64_t)2 << lane) - 1)) == nth)
+            f.index = begin + lane;
+        const uint32_t n = __popcll(hits);
+        const bool found = nth <= n;
+        nth -= found ? 0 : n;
+        return found;
+    };
+    if (single(0, s.body))
+        return;
+    u32x4 v[TURN], next[TURN];
+    auto load = [&](u32x4 *to, int i) {
 #pragma unroll
-        for (int j = 0; j < UNROLL; ++j)
-            v[j] = p[i + j * kWave < end ? i + j * kWave : i];
+        for (int j = 0; j < TURN; ++j)
+            to[j] = p[i + j * kScanThreads < s.units ? i + j * kScanThreads : 0];
+    };
+    if (s.units > 0)
+        load(next, threadIdx.x);
+    int turn = 0;
+    for (int i0 = 0; i0 < s.units; i0 += TURN * kScanThreads, turn ^= 1) {
+        const int i = i0 + (int)threadIdx.x;
 #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) {
+        for (int j = 0; j < TURN; ++j)
+            v[j] = next[j];
+        load(next, i + TURN * kScanThreads);
+        uint32_t hits = 0;  // bit 8 j + e
+#pragma unroll
+        for (int j = 0; j < TURN; ++j) {
             uint32_t h = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t d = (v[j][e] & mask) ^ both;
-                h += (d & 0xFFFFu) == 0 ? 1u : 0u;
-                h += d < 0x10000u ? 1u : 0u;
-            }
-            c += i + j * kWave < end ? h : 0u;
+            for (int e = 0; e < 4; ++e)
+                h |= hits_of(v[j][e], mask, both) << 2 * e;
+            hits |= (i + j * kScanThreads < s.units ? h : 0u) << 8 * j;
         }
+        // a wave's numbers of each quarter (512 at most), two to a word
+        const uint32_t n01 = of_lane(wave_sums(__popc(hits & 0xFFu) | __popc(hits & 0xFF00u) << 16), kWave - 1);
+        const uint32_t n23 = of_lane(wave_sums(__popc(hits & 0xFF0000u) | __popc(hits >> 24) << 16), kWave - 1);
+        if (lane < TURN)
+            f.numbers[turn][lane * WAVES + wave] = ((lane & 2 ? n23 : n01) >> (lane & 1 ? 16 : 0)) & 0xFFFFu;
+        __syncthreads();
+        const uint32_t own = f.numbers[turn][lane], upto = wave_sums(own);
+        const uint64_t reached = __ballot(upto >= nth);
+        if (reached) {
+            const int at = __builtin_ctzll(reached);
+            nth -= of_lane(upto - own, at);
+            if (wave == at % WAVES) {
+                uint32_t h = hits >> 8 * (at / WAVES) & 0xFFu;
+                const uint32_t mine = __popc(h), to = wave_sums(mine);
+                if (nth > to - mine && nth <= to) {
+                    for (uint32_t k = to - mine + 1; k < nth; ++k)
+                        h &= h - 1;
+                    f.index = s.body + 8 * (i + at / WAVES * kScanThreads) + __builtin_ctz(h);
+                }
+            }
+            return;
+        }
+        nth -= of_lane(upto, kWave - 1);
     }
-    // the single elements before the units and behind them
-    const bool head = (int)threadIdx.x < s.body && ((row[threadIdx.x] & mask) ^ wanted) == 0;
-    const uint32_t heads = __popcll(__ballot(head));  // wave 0's: the fewer than 8 first lanes
-    c = of_lane(wave_sums(c), kWave - 1);
-    if (lane == 0)
-        f.seen[wave] = c;
-    if (threadIdx.x == 0)
-        f.count[0] = heads;
-    __syncthreads();
-    uint32_t nth = f.nth;
-    const uint32_t before = f.count[0];
-    if (nth <= before) {
-        if (head && (uint32_t)__popcll(__ballot(head) & (((uint64_t)2 << lane) - 1)) == nth)
-            f.index = threadIdx.x;
-        return;
-    }
-    nth -= before;
-    int in = 0;
-    for (; in < WAVES && nth > f.seen[in]; ++in)
-        nth -= f.seen[in];
-    if (in == WAVES) {  // behind the units
-        const bool tail = (int)threadIdx.x < V - s.tail && ((row[s.tail + threadIdx.x] & mask) ^ wanted) == 0;
-        if (tail && (uint32_t)__popcll(__ballot(tail) & (((uint64_t)2 << lane) - 1)) == nth)
-            f.index = s.tail + threadIdx.x;
-        return;
-    }
-    const int unit = in * share + (int)threadIdx.x;
-    uint32_t hits = 0;
-    if ((int)threadIdx.x < share && unit < s.units) {
-        const u32x4 v = p[unit];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            hits |= hits_of(v[e], mask, both) << 2 * e;
-    }
-    const uint32_t mine = __popc(hits);
-    uint32_t upto = mine;
-    double none = 0.0;
-    block_sums<kScanThreads>(upto, none, f.waves);
-    if (nth > upto - mine && nth <= upto) {
-        for (uint32_t k = upto - mine + 1; k < nth; ++k)
-            hits &= hits - 1;
-        f.index = s.body + 8 * unit + __builtin_ctz(hits);
-    }
+    single(s.tail, V);
 }
 
 __global__ __launch_bounds__(kScanThreads) void sample_values_kernel(const SampleArgs a)
