@@ -27,7 +27,7 @@
 // cumulative sum of n similar tokens by 2^-28 / sqrt(n) of itself, which moves
 // a token only if u falls within that of a border.
 //
-// Many rows of bf16 logits take another way, by their values (see there).
+// Rows of bf16 logits take another way, by their values (see there).
 //
 // Rows whose maximum lies outside the histogram's range (|z| of 500, or an
 // infinity) are counted again relative to their maximum by the finishing
@@ -1334,14 +1334,14 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
 }
 
 // ---------------------------------------------------------------------------
-// Many rows of bf16 logits: one workgroup a row and no bins. A row has at most
+// Rows of bf16 logits: one workgroup a row and no bins. A row has at most
 // 65536 different logits, so that their numbers fit the LDS; the filters and the
 // token's logit follow from sums over the values in falling order, and one more
 // pass finds which of the equal ones the token is. Counting takes 4 instructions
 // an element where the histogram of bins takes 20, and nothing is listed: 256
-// rows of 131072 logits with top-p take 39 us, by bins 68 (counting 10, the values'
-// sums 9, searches 7, the last pass 9). In fp16, whose values near zero lie four
-// times as densely, the sums take 30 and the call 62 (by bins 46).
+// rows of 131072 logits with top-p take 35 us, by bins 68 (counting 11, at 6 TB/s,
+// the values' sums 9, searches 4, the last pass 3 to 8). In fp16, whose values near
+// zero lie four times as densely, the sums took 25 and the call 62 (by bins 46).
 // ---------------------------------------------------------------------------
 constexpr int kWords = 1 << 15;                // of counts: by magnitude; positive logits in the low half, negative in the high
 constexpr int kGroups = 2 * kWords / kWave;    // of 64 values in falling order: positive ones from the largest, then negative ones
@@ -1790,13 +1790,15 @@ int slices_of(int M, int V)
     return s > least ? s : least > 1 ? least : 1;
 }
 
-// Whether rows of bf16 logits are taken by their values: where they fill the GPU
-// and the fixed 20 us of a row pay (us by bins and by values, with top-k 50 and
-// top-p 0.9, then without top-k):
-//   64 x 131072   31 : 34,  46 : 33        128 x 32000   21 : 25,  27 : 24
-//   256 x 32000   25 : 25,  31 : 25        512 x  8000   33 : 43,  41 : 42
-//   256 x 131072  47 : 40,  59 : 39
-bool by_values(int M, int V) { return V >= 1 << 14 && V <= kMaxSlice && (int64_t)M * V >= 6 << 20; }
+// Whether rows of bf16 logits are taken by their values: its fixed 15 us and one
+// CU for a row are too much for short rows, and for few long ones (us by bins and
+// by values, with top-k 50 and top-p 0.9, then without top-k):
+//   8 x 500       15 : 16,  13 : 16       1 x 131072    21 : 27,  27 : 25
+//   8 x 4000      15 : 17,  17 : 16       32 x 131072   25 : 31,  37 : 30
+//   8 x 16000     19 : 18,  23 : 17       64 x 131072   30 : 33,  46 : 32
+//   32 x 65000    23 : 23,  29 : 23       128 x 131072  39 : 33,  75 : 32
+//   256 x 32000   26 : 21,  31 : 20       256 x 131072  48 : 36,  59 : 35
+bool by_values(int M, int V) { return V >= 1 << 13 && V <= (M >= 64 ? kMaxSlice : 1 << 16); }
 
 template <typename T>
 hipError_t launch(const SampleArgs &a, hipStream_t stream)
