@@ -369,6 +369,30 @@ __device__ __forceinline__ V wave_sums(V v)
     const V before = row == 0 ? (V)0 : row == 1 ? r0 : row == 2 ? r0 + r1 : r0 + r1 + r2;
     return v + before;
 }
+// Their total alone, in the last lane: half as many instructions.
+template <int CTRL, int ROWS, typename V>
+__device__ __forceinline__ V moved_to_rows(V v)
+{
+    if constexpr (sizeof(V) == 4) {
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+    } else {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    }
+}
+template <typename V>
+__device__ __forceinline__ V wave_total(V v)
+{
+    v += moved<0x111>(v);
+    v += moved<0x112>(v);
+    v += moved<0x114>(v);
+    v += moved<0x118>(v);
+    v += moved_to_rows<0x142, 0xA>(v);  // row_bcast:15: a row's sum to the next, for the odd rows
+    v += moved_to_rows<0x143, 0xC>(v);  // row_bcast:31: the first half's sum to the second
+    return v;
+}
 template <int THREADS, typename M>
 __device__ __forceinline__ void block_sums(uint32_t &c, M &m, WaveSums<M> &w)
 {
@@ -1340,8 +1364,9 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
 // pass finds which of the equal ones the token is. Counting takes 4 instructions
 // an element where the histogram of bins takes 20, and nothing is listed: 256
 // rows of 131072 logits with top-p take 35 us, by bins 68 (counting 11, at 6 TB/s,
-// the values' sums 9, searches 4, the last pass 3 to 8). In fp16, whose values near
-// zero lie four times as densely, the sums took 25 and the call 62 (by bins 46).
+// the values' sums 8, searches 4, the last pass 3 to 8). In fp16, whose values near
+// zero lie four times as densely, the sums take more than that saves: the same
+// rows 49 us (46 by bins), 32 rows of 32003 with top-k and min-p 31 (24).
 // ---------------------------------------------------------------------------
 constexpr int kWords = 1 << 15;                // of counts: by magnitude; positive logits in the low half, negative in the high
 constexpr int kGroups = 2 * kWords / kWave;    // of 64 values in falling order: positive ones from the largest, then negative ones
@@ -1650,8 +1675,8 @@ __global__ __launch_bounds__(kScanThreads) void sample_values_kernel(const Sampl
             group_at(f, group, heavies, top, p.per_unit, fine, count, weight);
             if (!__any(count != 0))
                 continue;
-            const uint32_t c = wave_sums(count);
-            const double m = wave_sums((double)count * weight);
+            const uint32_t c = wave_total(count);
+            const double m = wave_total((double)count * weight);
             if (lane == kWave - 1) {
                 f.count[group] = c;
                 f.mass[group] = m;
