@@ -72,7 +72,10 @@ constexpr int kSliceList = 1024;     // listed elements of a slice
 constexpr int kList = 11264;
 constexpr int kParts = 512;          // parts of a bin
 constexpr int kRanked = 1024;        // elements that are ranked by pairs
-constexpr int kWhole = 64;           // a bin of up to this many is ranked as it is
+// A bin of up to this many is ranked as it is (32 rows of 32003 logits with top-k
+// 1000 and min-p 24.0 us a call, with 64 24.6; with 192 16 rows of 131072 take 30
+// instead of 28).
+constexpr int kWhole = 128;
 constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it leaves the nearest integer in the low word
 
 // What a slice leaves behind, and a row (cut into slices).
