@@ -38,12 +38,12 @@
 // few rows still fill the GPU.
 //
 // What bounds it. Few rows: two or three launches one after the other, each with
-// its code to fetch: one row of 131072 fp32 logits takes 18 us (histogram 4,
-// gather 8, finish 5), 16 rows with top-k and top-p 25, 32 rows of 32003 fp16
-// logits 24. 256 rows of 131072 fp32 logits with top-p take 73 us: the histogram
-// 25, for which a CU issues 20 instructions and one LDS atomic for every
-// element, and the finish, of which listing an element in 15 to 40 takes 11 to
-// 19 and each search up to 9.
+// its code to fetch: one row of 131072 fp32 logits takes 20 us (histogram 5,
+// gather 8, finish 5), 16 rows of 151001 with top-k and top-p 24, 32 rows of 32003
+// fp16 logits 24. 256 rows of 131072 fp32 logits take 58 us with top-k 50 and top-p
+// 0.9, without top-k 66: two passes over 134 MB (27 each at the rate of a copy), and
+// the searches, up to 9 each. With 16-bit logits the histogram still takes 25: a
+// CU issues 20 instructions and one LDS atomic for every element.
 #include "qmm_device.hpp"
 #include "qmm_kernels.hpp"
 #include "qmm_step.hpp"
@@ -61,8 +61,8 @@ constexpr int kSumBits = 46;         // low field of a packed bin: the sum of q
 constexpr float kUnit = 2147483648.0f;   // 2^31: the weight of a bin's centre
 constexpr int kMaxSlice = 1 << 17;   // elements of a slice: the packed number has 18 bits, the sum 45 and a sign
 // Rows up to this long are gathered by the workgroup that finishes them: 32000
-// logits 19.7 us a call against 20.8 with a launch of its own for the gather,
-// 65000 22.0 and 22.0, 131072 27.3 and 22.9 (one row, top-k and top-p).
+// logits 17.6 us a call against 20.4 with a launch of its own for the gather,
+// 65000 20.9 and 20.5, 131072 24.1 and 20.5 (one row, top-k and top-p).
 constexpr int kGatherMin = 1 << 16;
 constexpr int kMaxSlices = 64;
 constexpr int kSliceList = 1024;     // listed elements of a slice
@@ -1805,9 +1805,9 @@ __global__ __launch_bounds__(kScanThreads) void sample_values_kernel(const Sampl
 }
 
 // Slices of a row: enough workgroups to fill the GPU (64 rows of 131072 logits:
-// 34 us a call; with half as many 42, with twice as many 36), none with fewer
-// than 8 elements for each thread (one such row: 22.9 us; with 4 or 16 elements
-// 23.9, for the slices have to be joined by each workgroup of the gather).
+// 32 us a call; with half as many 40, with twice as many 34), none with fewer
+// than 8 elements for each thread (one such row: 20.5 us; with 4 or 16 elements
+// 21.5, for the slices have to be joined by each workgroup of the gather).
 int slices_of(int M, int V)
 {
     const int least = (V + kMaxSlice - 1) / kMaxSlice;

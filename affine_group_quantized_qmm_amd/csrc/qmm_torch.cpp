@@ -1,7 +1,7 @@
 // The step operators' Python calls: checks of the tensors and the call into the
 // C ABI, compiled. A decode step makes these calls for every layer, with
 // kernels of a few microseconds. One token through the norm and rotation takes
-// 4.4 us a call, its kernel 3.0; with the same checks in Python it took 10.5.
+// 4 to 4.5 us a call, its kernel 3.0; with the same checks in Python it took 10.5.
 // Nothing here computes or launches anything itself.
 //
 // Every function takes its arguments by position (the package's Python
