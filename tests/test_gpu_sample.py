@@ -208,10 +208,11 @@ def test_strided_and_unaligned_rows():
             view.fill_(99.0)
 
 
-@pytest.mark.parametrize("M,V", [(1, 90000), (3, 5000), (280, 30000)])
-def test_graph_replays_reruns_and_streams(M, V):
+@pytest.mark.parametrize("M,V,dtype", [(1, 90000, F32), (3, 5000, F32), (280, 30000, F32), (3, 30000, BF16),
+                                       (70, 131072, BF16), (70, 131072, F16)])
+def test_graph_replays_reruns_and_streams(M, V, dtype):
     qmm, dev = _gpu.lib(), _gpu.dev()
-    x = logits(M, V, F32, 18).to(dev)
+    x = logits(M, V, dtype, 18).to(dev)
     u = torch.as_tensor(uniform(M, 21)).to(dev)
     p = torch.full((M,), 0.9, device=dev)
     ws = torch.empty(qmm.qmm_sample_workspace_bytes(M, V), dtype=torch.uint8, device=dev)
@@ -249,7 +250,7 @@ def test_graph_replays_reruns_and_streams(M, V):
 @pytest.mark.parametrize("heavy", [(0.0,), (-3.0,), (0.0, -0.0), (1.5, 1.25), ("lowest",), (2.0, "-inf")], ids=str)
 def test_logits_of_more_than_65535_elements(heavy, dtype):
     """One or two logits fill most of a row, as the largest, among the others or far below."""
-    M, V = 48, 131072
+    M, V = 66, 131072
     x = logits(M, V, dtype, 1)
     x[::2] = logits(M // 2, V, dtype, 2, 1.0)
     g = torch.Generator().manual_seed(10)
@@ -260,17 +261,34 @@ def test_logits_of_more_than_65535_elements(heavy, dtype):
             n = [65536, 100000, V][i % 3] if len(heavy) == 1 else [65536, 65535, 66000][i % 3]
             x[i, order[at:at + n]] = value
             at += n
-    u, T, k = uniform(M, 3), np.tile([1.0, 0.7, 1.3, 1.0, 1.0, 0.7], 8), np.tile([0, 0, 60000, 70000, 100, 0], 8)
-    p, mp = np.tile([1.0, 0.9, 0.95, 1.0, 1.0, 0.5], 8), np.tile([0.0, 0.0, 0.0, 0.1, 0.0, 0.0], 8)
+    u, T, k = uniform(M, 3), np.tile([1.0, 0.7, 1.3, 1.0, 1.0, 0.7], 11), np.tile([0, 0, 60000, 70000, 100, 0], 11)
+    p, mp = np.tile([1.0, 0.9, 0.95, 1.0, 1.0, 0.5], 11), np.tile([0.0, 0.0, 0.0, 0.1, 0.0, 0.0], 11)
     tok, lp = check(x, u, T, k, p, mp, most_near=M // 6)  # half of equal logits is a border: every sixth row
     if len(heavy) == 1:
         for i in range(5, M, 6):  # the first half by index, and u takes its place in it
             assert tok[i] == int(np.floor(np.float64(u[i]) * (V // 2)))
 
 
+@pytest.mark.parametrize("n", [65534, 65535, 65536])
+@pytest.mark.parametrize("value", [0.0, -0.0, -7.0, 5.0])
+def test_row_of_65536_bf16_logits_that_are_nearly_all_equal(value, n):
+    M, V = 5, 65536
+    x = torch.full((M, V), value).to(BF16)
+    x[:, n:] = -1.0
+    u = uniform(M, 23)
+    tok, lp = sample(x, u)
+    assert (tok >= 0).all()
+    for i in range(M):
+        if n == V:  # sums of ones are exact
+            assert tok[i] == int(np.floor(np.float64(u[i]) * n)) and abs(lp[i] + math.log(n)) <= 2.0 ** -20
+        want, want_lp, margin = _step.sample_reference(_step.f64(x[i]), float(u[i]), 1.0, 0, 1.0, 0.0)
+        if margin >= MARGIN:
+            assert tok[i] == want and abs(float(lp[i]) - want_lp) <= 2.0 ** -27 + abs(want_lp) * 2.0 ** -24
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("M,V", [(24, 1), (24, 17), (24, 9001), (24, 131073), (400, 16384), (100, 65001), (49, 131071),
-                                 (48, 131072)])
+@pytest.mark.parametrize("M,V", [(24, 1), (24, 17), (24, 9001), (24, 131073), (400, 16384), (100, 65001), (65, 131071),
+                                 (64, 131072)])
 def test_16_bit_rows_of_every_alignment(M, V, dtype):
     """Rows whose first elements lie at every distance from 16 bytes; tokens among equal logits by their index."""
     x = torch.empty(M, V + 3, dtype=dtype)[:, :V]
