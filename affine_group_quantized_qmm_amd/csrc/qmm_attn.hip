@@ -9,14 +9,17 @@
 //   S^T = K Q^T      16x16x32 MFMA, tokens by columns
 //   p = 2^(s - m)    a lane holds 4 tokens of one column; the columns' running
 //                    maxima m are in LDS and are raised (and the accumulators
-//                    rescaled) only when some score passes them by 2^8, which
+//                    rescaled) only when some score passes them by kRaise, which
 //                    bounds p and leaves nothing to exchange in most turns
 //   O^T += V^T P^T   over 32 tokens: the 4 + 4 that one lane group wrote of two
 //                    waves; V^T comes out of LDS with transposing reads
 //
 // P is kept as the sum of two 16-bit numbers (a rounding and its remainder):
 // rounding p once to bf16 would add an error as large as the output's own
-// rounding, and the matrix units have room for the second product.
+// rounding, and the matrix units have room for the second product. In fp16 all of
+// p is scaled by 2^15 (kLift), for the numbers below 2^-14 lose bits there: a
+// first token with a large score and a small value, and a long tail of small
+// weights that makes up the output, are ordinary.
 //
 // A tile is 16 tokens for each wave of a workgroup. Each wave multiplies its own
 // 16 tokens with all columns; the columns' maxima meet in LDS, P and V lie there
@@ -55,11 +58,13 @@ constexpr int kJoinThreads = 1024;
 constexpr int waves_of(int D, int NT) { return D >= 192 || (D == 128 && NT == 6) ? 8 : 4; }
 constexpr int tile_of(int D, int NT) { return 16 * waves_of(D, NT); }
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;   // token without a row in the cache
-constexpr float kRaise = 8.0f;             // a score may pass the running maximum by this (log2)
 
 typedef float float2_t __attribute__((ext_vector_type(2)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
 
+// A type's matrix instructions and how its weights are scaled: p = 2^(s - m +
+// kLift), where a score may pass the running maximum m by kRaise (both log2);
+// kUnlift is 2^-kLift.
 template <typename T>
 struct Elem;
 template <>
@@ -67,6 +72,9 @@ struct Elem<_Float16> {
     typedef _Float16 x8 __attribute__((ext_vector_type(8)));
     typedef _Float16 x4 __attribute__((ext_vector_type(4)));
     static constexpr uint32_t exponent = 0x7C00u;
+    // p is at most 2^15.5, below the type's largest, and 2^15 at the maximum: the
+    // second part's steps of 2^-24 then hold a weight to 2^-40 of the largest one.
+    static constexpr float kLift = 15.0f, kUnlift = 0x1p-15f, kRaise = 0.5f;
     static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -77,6 +85,7 @@ struct Elem<__bf16> {
     typedef __bf16 x8 __attribute__((ext_vector_type(8)));
     typedef __bf16 x4 __attribute__((ext_vector_type(4)));
     static constexpr uint32_t exponent = 0x7F80u;
+    static constexpr float kLift = 0.0f, kUnlift = 1.0f, kRaise = 8.0f;  // fp32's range: no floor to keep away from
     static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -548,7 +557,7 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
                 }
             }
             const float top = fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3]));
-            if (top > m[t] + kRaise)
+            if (top > m[t] + E::kRaise)
                 __hip_atomic_fetch_max(&col_max[t * 16 + n], top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
         lds_barrier();  // the columns' maxima are in
@@ -564,7 +573,7 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
                 for (int d = 0; d < DW; ++d)
                     acc[t][d] *= f;
             }
-            const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+            const float base = m[t] == -__builtin_inff() ? 0.f : m[t] - E::kLift;
             x4 hi, lo;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -724,7 +733,7 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
             }
             if (first && a.lse)
                 a.lse[at_row] = total == 0.f ? -__builtin_inff()
-                                             : (m[t] + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f;
+                                             : (m[t] + __builtin_amdgcn_logf(total * E::kUnlift)) * 0.69314718055994530942f;
         } else {
             const int64_t part = (int64_t)slot_of(w, begin == 0) * kColumns + t * 16 + n;
             float *to = a.part_acc + part * D + wave * 16 + 4 * c;
@@ -819,7 +828,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
             *reinterpret_cast<typename E::x4 *>(static_cast<T *>(a.out) + at_row * D + d4 * 4) = y;
             if (a.lse && d4 == 0)
                 a.lse[at_row] = total == 0.f ? -__builtin_inff()
-                                             : (top + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f;
+                                             : (top + __builtin_amdgcn_logf(total * E::kUnlift)) * 0.69314718055994530942f;
         }
         __syncthreads();
     }

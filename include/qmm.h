@@ -429,9 +429,11 @@ int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stri
  * lse of -infinity. What lies in places that no row sees is not used, whatever
  * it is; infinities and NaN of a token reach the rows that see it and no
  * others. Products are accumulated in fp32, e^(s) and its sums are fp32, and
- * e^(s) enters the second product as the sum of two 16-bit numbers; `out` is
- * rounded once. lse (fp32 [T, Hq], natural logarithm) may be NULL. Reruns are
- * bitwise identical. Rows of q that no sequence holds are not written.
+ * e^(s) enters the second product as the sum of two 16-bit numbers (good to
+ * 2^-16 of itself in bf16, in fp16 to 2^-22, or 2^-40 of the row's largest where
+ * that is more); `out` is rounded once. lse (fp32 [T, Hq], natural logarithm) may
+ * be NULL. Reruns are bitwise identical. Rows of q that no sequence holds are
+ * not written.
  *
  * max_rows: at least the rows of any sequence, at most T (further rows of a
  * longer sequence are not computed). max_context: an estimate of the longest context; it
