@@ -895,8 +895,10 @@ __device__ __forceinline__ bool find_listed(Finish<THREADS> &f, int t, int top_b
         __syncthreads();
         before = f.found_count;
         mass = f.found_sum;
-        if (f.number > kRanked)
+        if (f.number > kRanked) {
+            __syncthreads();  // all have read f.number, which the caller's next search clears
             return false;
+        }
     }
     for (int i = threadIdx.x; i < kRanked; i += THREADS)
         f.ranked[i].place = 0;
