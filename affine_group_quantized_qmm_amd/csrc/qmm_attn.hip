@@ -239,7 +239,7 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
     __shared__ __align__(16) T p_hi[NT * 16 * kColumn], p_lo[NT * 16 * kColumn];
     __shared__ u32x4 q_lds[kQueriesInLds ? NT * KS * kWave : 1];
     __shared__ float col_max[NT * 16], col_sum[kWaves][NT * 16];
-    __shared__ u32x4 bad_tokens[kWaves / 4];  // a word for each wave
+    __shared__ u32x4 bad_tokens[kWaves / 4];  // a word for each wave; after the last tile whether its sums are not all finite
     __shared__ uint32_t rows_lds[kTile];
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -370,6 +370,12 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
     }
     const int tr_offset = (4 * c + n / 4) * kPitch + n % 4 * 8;
 
+    // Infinities and NaN in V of a tile that every row sees whole go through both
+    // products as they are, where infinity times a remainder of 0 or below is not
+    // infinity. They leave no output of the piece finite: then it is computed once
+    // more with every tile treated as partly visible (`careful`), which takes
+    // them one by one. Nothing is looked for in the tiles themselves.
+    bool careful = false;
     for (;; lds_barrier()) {  // the items of the run
     const int x0 = chunk * kColumns;
     const Span span = span_of<kTile>(a, run_begin, run_end, run_len, x0, kColumns);
@@ -542,7 +548,7 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
 
         // Tiles that not every row sees whole: scores that a row does not see
         // are -infinity.
-        const bool partial = present != 0xFFFFu || j0 + 15 > span.pmin ||
+        const bool partial = careful || present != 0xFFFFu || j0 + 15 > span.pmin ||
                              (a.window > 0 && j0 <= span.pmax - a.window && j0 + 16 > a.sinks);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -675,7 +681,8 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const int from = (t * 16 + n) * kColumn + tok;
-                    const float p = (float)p_hi[from] + (float)p_lo[from];
+                    // a weight that was too small for its type is not zero
+                    const float p = (float)p_hi[from] + (float)p_lo[from] + 0x1p-126f;
                     const bool sees = j <= pos[t] && (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
 #pragma unroll
                     for (int d = 0; d < DW; ++d) {
@@ -699,14 +706,31 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
     }
 
     // Sums of the columns over the lanes and waves that share them.
+    float zero = 0.f;  // NaN if some sum is not finite
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         l[t] += __shfl_xor(l[t], 16);
         l[t] += __shfl_xor(l[t], 32);
         if (c == 0)
             col_sum[wave][t * 16 + n] = l[t];
+#pragma unroll
+        for (int d = 0; d < DW; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                zero = __builtin_fmaf(acc[t][d][i], 0.f, zero);
     }
+    const uint32_t odd = __any(zero != 0.f);
+    if (lane == 0)
+        reinterpret_cast<uint32_t *>(bad_tokens)[wave] = odd;
     lds_barrier();
+    u32x4 any_odd = bad_tokens[0];
+    if constexpr (kWaves == 8)
+        any_odd |= bad_tokens[1];
+    if (!careful && __builtin_amdgcn_readfirstlane(any_odd.x | any_odd.y | any_odd.z | any_odd.w)) {
+        careful = true;
+        continue;
+    }
+    careful = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int x = x0 + t * 16 + n;
