@@ -223,6 +223,7 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
     using x8 = typename E::x8;
     using x4 = typename E::x4;
     constexpr int kWaves = waves_of(D, NT), kTile = tile_of(D, NT);
+    static_assert(kTile <= kAttnMostTile, "the host's limit on token numbers");
     constexpr int KS = D / 32;                  // contraction steps of K Q^T; loads of a lane for K and for V
     constexpr int DT = D / 16;                  // output tiles along the head
     constexpr int DW = (DT + kWaves - 1) / kWaves;  // of one wave: tiles wave, wave + kWaves, ...

@@ -133,8 +133,10 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
         rc = check_cache(num_pages, page_size, Hkv);
     if (rc != QMM_OK)
         return rc;
-    if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX - 64 || q_stride < (int64_t)Hq * D ||
-        !isfinite(scale))
+    // Token numbers have 32 bits up to the end of a tile that begins at the
+    // table's end, and loads run two tiles ahead.
+    if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX - 4 * qmm::kAttnMostTile ||
+        q_stride < (int64_t)Hq * D || !isfinite(scale))
         return QMM_ERR_SHAPE;
     const qmm::AttnPlan plan =
         plan_of(B, Hq, Hkv, D, max_rows, max_context, window, sinks, page_size, max_pages);

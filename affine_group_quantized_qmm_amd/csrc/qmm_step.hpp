@@ -59,6 +59,7 @@ struct AttnPlan {
     int64_t blocks, items;
     size_t join_bytes, workspace_bytes;
 };
+constexpr int kAttnMostTile = 128;  // tokens of the largest tile
 bool attn_head_dim_supported(int D);
 AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks,
                    int page_size, int max_pages);

@@ -438,8 +438,9 @@ int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stri
  * max_rows: at least the rows of any sequence, at most T (further rows of a
  * longer sequence are not computed). max_context: an estimate of the longest context; it
  * sets how the length is split over the GPU and the workspace, not what is
- * computed. D is 64, 96, 128, 192 or 256. Workspace: see below, 16-byte
- * aligned, contents irrelevant, NULL when 0 bytes are needed.
+ * computed. D is 64, 96, 128, 192 or 256; max_pages * page_size is at most
+ * 2^31 - 513. Workspace: see below, 16-byte aligned, contents irrelevant, NULL
+ * when 0 bytes are needed.
  * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_HEAD,
  * QMM_ERR_WORKSPACE, QMM_ERR_ALIGN, QMM_ERR_LAUNCH.
  *
