@@ -63,7 +63,8 @@ int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stri
         return QMM_ERR_NULL;
     if (!any_type(in_type) || !output_type(out_type))
         return QMM_ERR_TYPE;
-    if (M < 1 || Hq < 1 || M >= (1 << 30) || Hq > 65535 || Hkv > 65535)
+    // a workgroup of 256 threads for each row: the runtime counts a launch's threads in 32 bits
+    if (M < 1 || Hq < 1 || M > (int)(UINT32_MAX / 256) || Hq > 65535 || Hkv > 65535)
         return QMM_ERR_SHAPE;
     const int rc = check_cache(num_pages, page_size, Hkv);
     if (rc != QMM_OK)

@@ -394,7 +394,7 @@ int qmm_stream_read(const void *src, size_t bytes, uint32_t *sink, hipStream_t s
  * slots int32 [M]: where row m's key and value go; a slot that is negative (a
  * padding row) or past the cache writes nothing. Two rows with the same slot
  * leave either's values. q_out [M, Hq, D] of out_type (fp16 or bf16), like the
- * caches. D a multiple of 8 up to 256, R a multiple of 8 up to D.
+ * caches. D a multiple of 8 up to 256, R a multiple of 8 up to D, M < 2^24.
  * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_HEAD,
  * QMM_ERR_ALIGN (16 bytes; positions and slots 4), QMM_ERR_LAUNCH.
  */

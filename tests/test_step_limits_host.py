@@ -12,3 +12,9 @@ MOST = (1 << 31) - 1
 def test_table_capacity(D, capacity):
     """Tiles have up to 128 tokens and loads run two tiles ahead of the last one."""
     assert attn(D=D, qs=4 * D, ps=1, max_pages=capacity) == -2
+
+
+@pytest.mark.parametrize("M", [1 << 24, (1 << 24) + 1, 1 << 29, MOST])
+def test_rows_of_the_norm(M):
+    """A workgroup of 256 threads for each row, in 32 bits."""
+    assert rope(M=M) == -2
