@@ -22,16 +22,32 @@ import torch
 
 LIBRARY_PATH = Path(__file__).resolve().parent / "libqmm.so"
 
-_BINDING_PATH = LIBRARY_PATH.with_name("_qmm_torch.so")
-_missing = [str(path) for path in (LIBRARY_PATH, _BINDING_PATH) if not path.exists()]
-if _missing:
+if not LIBRARY_PATH.exists():
     raise ImportError(
-        f"{' and '.join(_missing)} missing: build the HIP library first "
+        f"{LIBRARY_PATH} is missing: build the HIP library first "
         "(python -c 'import __graft_entry__ as g; g.build()' at the repository root)")
 
 _lib = ctypes.CDLL(str(LIBRARY_PATH))
 
-from . import _qmm_torch as _binding  # noqa: E402  (built beside the library, and loads the same libqmm.so)
+
+class _NoBinding:
+    """In the place of the step operators' compiled part where it cannot be
+    loaded (not built, or built against another torch): their calls fail, the
+    products do not need it."""
+
+    def __init__(self, cause: ImportError):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError(f"{LIBRARY_PATH.with_name('_qmm_torch.so')} cannot be loaded: build it against the installed "
+                          "torch (python -c 'import __graft_entry__ as g; g.build()' at the repository root)"
+                          ) from self._cause
+
+
+try:
+    from . import _qmm_torch as _binding  # built beside the library, and loads the same libqmm.so
+except ImportError as _e:
+    _binding = _NoBinding(_e)
 
 _p, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _lib.qmm_pack.argtypes = [_p, _p, _i, _i, _i, _p]
