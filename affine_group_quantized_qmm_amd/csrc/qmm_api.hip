@@ -232,12 +232,15 @@ const char *qmm_strerror(int code)
     switch (code) {
     case QMM_OK: return "success";
     case QMM_ERR_NULL: return "a required pointer is NULL";
-    case QMM_ERR_SHAPE: return "bad shape: need M, K, N >= 1, K a multiple of G, sizes in range";
+    case QMM_ERR_SHAPE: return "bad shape: need M, K, N >= 1, K a multiple of G, sizes in range; between the products: every "
+                               "size at least 1 and in the range that the entry point lists";
     case QMM_ERR_BITS: return "unsupported bit width (supported: 2, 3, 4, 5, 6, 8)";
     case QMM_ERR_GROUP: return "unsupported group size (supported: 32, 64, 128)";
     case QMM_ERR_SPLIT: return "bad split_k: need 1 <= split_k <= K/G";
-    case QMM_ERR_WORKSPACE: return "workspace smaller than the entry point's *_workspace_bytes";
-    case QMM_ERR_ALIGN: return "buffers must be 16-byte aligned (per-row parameters 4), row strides multiples of 8";
+    case QMM_ERR_WORKSPACE: return "workspace smaller than qmm_splitk_workspace_bytes(M, N, split_k), or another entry point's "
+                                   "*_workspace_bytes";
+    case QMM_ERR_ALIGN: return "x, wq, scales, biases, y and workspace must be 16-byte aligned; between the products: tensors "
+                               "16 bytes, per-row parameters 4, row strides multiples of 8 elements";
     case QMM_ERR_LAUNCH: return "the HIP runtime rejected a kernel launch";
     case QMM_ERR_UNSUPPORTED: return "the requested kernel cannot run this shape";
     case QMM_ERR_SCRATCH: return "split_k * M * N * 4 bytes exceed the static scratch (QMM_NOALLOC_SCRATCH_BYTES)";

@@ -71,7 +71,8 @@ extern "C" {
 #define QMM_ERR_GROUP (-4)         /* G not in {32, 64, 128} */
 #define QMM_ERR_SPLIT (-5)         /* split_k < 1 or split_k > K/G */
 #define QMM_ERR_WORKSPACE (-6)     /* workspace smaller than the entry point's *_workspace_bytes */
-#define QMM_ERR_ALIGN (-7)         /* x, wq, scales, biases, y or workspace not 16-byte aligned */
+#define QMM_ERR_ALIGN (-7)         /* x, wq, scales, biases, y or workspace not 16-byte aligned;
+                                    * between the products: as the entry point lists */
 #define QMM_ERR_LAUNCH (-8)        /* the HIP runtime rejected a kernel launch */
 #define QMM_ERR_UNSUPPORTED (-9)   /* qmm_forward_kernel: that kernel cannot run this shape */
 #define QMM_ERR_SCRATCH (-10)      /* qmm_forward_splitk_noalloc: partials exceed the static scratch */
