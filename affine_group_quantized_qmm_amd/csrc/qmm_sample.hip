@@ -8,9 +8,9 @@
 //
 //   1. histogram  One pass over the logits. With z = x / T, bin b = rint(8 z)
 //                 holds the elements' number and their mass relative to the
-//                 bin's centre, e^(z - b/8) = 1 + q with |q| < 0.065, so that a
-//                 small polynomial in fp32 gives a weight to 2^-29 and neither
-//                 the row's maximum nor a range reduction is needed first.
+//                 bin's centre, e^(z - b/8) = 1 + q with |q| < 0.065, so that an
+//                 integer and a small polynomial in fp32 give a weight to 2^-30
+//                 and neither the row's maximum nor a range reduction is needed first.
 //                 Weights are integers (2^31 (1 + q)): sums do not depend on
 //                 their order. Number and mass share one 64-bit LDS atomic.
 //                 Only the 384 bins below the maximum's count: e^-48 of the
@@ -23,9 +23,9 @@
 //                 ones), which are ranked by comparing all pairs.
 //
 // Tokens have to be equal to what 64-bit arithmetic gives, whatever the order of
-// the sums: the weights' relative errors (below 2^-28, of either sign) shift a
-// cumulative sum of n similar tokens by 2^-28 / sqrt(n) of itself, which moves
-// a token only if u falls within that of a border.
+// the sums: the weights' relative errors (below 2^-30) move a border between two
+// tokens by at most a quarter of the difference of two of them, 2^-31 of the kept
+// mass, and a token only if u falls within that.
 //
 // Rows of bf16 logits take another way, by their values (see there).
 //
@@ -57,9 +57,10 @@ constexpr int kRange = 8192;         // bins of the histogram: z of -512 .. 512
 constexpr int kBins = 384;           // bins that count, from the maximum's down
 constexpr int kSlots = 512;          // of a slice's histogram: bin b lies in slot b mod 512
 constexpr double kPerUnit = 8.0;     // bins per unit of z
-constexpr int kSumBits = 46;         // low field of a packed bin: the sum of q
+constexpr int kSumBits = 46;         // low field of a packed bin: the sum of its weights over kLeast
 constexpr float kUnit = 2147483648.0f;   // 2^31: the weight of a bin's centre
-constexpr int kMaxSlice = 1 << 17;   // elements of a slice: the packed number has 18 bits, the sum 45 and a sign
+constexpr uint32_t kLeast = (1u << 31) - (1u << 27);  // what every weight passes (2^31 e^(-1/16) is above it)
+constexpr int kMaxSlice = 1 << 17;   // elements of a slice: the packed number has 18 bits, the sum 46
 // Rows up to this long are gathered by the workgroup that finishes them: 32000
 // logits 17.6 us a call against 20.4 with a launch of its own for the gather,
 // 65000 20.9 and 20.5, 131072 24.1 and 20.5 (one row, top-k and top-p).
@@ -76,7 +77,7 @@ constexpr int kRanked = 1024;        // elements that are ranked by pairs
 // 1000 and min-p 24.0 us a call, with 64 24.6; with 192 16 rows of 131072 take 30
 // instead of 28).
 constexpr int kWhole = 128;
-constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it leaves the nearest integer in the low word
+constexpr double kMagic = 25165824.5;  // 1.5 * 2^24: adding it leaves a number in steps of 2^-28 in the low bits; and half a bin
 
 // What a slice leaves behind, and a row (cut into slices).
 struct SliceHead {
@@ -97,6 +98,7 @@ struct RowSums {
 };
 __host__ __device__ constexpr size_t slice_bytes() { return sizeof(SliceHead) + kSlots * 8 + kSliceList * sizeof(Entry); }
 __host__ __device__ constexpr size_t row_bytes(int S) { return sizeof(RowSums) + S * slice_bytes(); }
+static_assert(kParts == 1 << 9, "binned's parts");
 static_assert(sizeof(RowSums) % 16 == 0 && slice_bytes() % 16 == 0, "aligned parts");
 __device__ __forceinline__ RowSums *sums_of(const SampleArgs &a, int row, int S)
 {
@@ -153,25 +155,33 @@ __device__ __forceinline__ double scaled(float x, double per_unit, float ref)
         return (double)x * per_unit;
 }
 
-// Bin and weight (2^31 (1 + q)) of a scaled logit within the range, and the part
+// Bin and weight (2^31 (1 + q) = kLeast + over) of a scaled logit within the range, and the part
 // of the bin (0: its upper end) that it lies in.
 struct Binned {
     int bin;
-    int q;
+    uint32_t over;
     int part;
+    __device__ __forceinline__ uint32_t weight() const { return kLeast + over; }
 };
+// d + 1/2 in steps of 2^-28 bins is an integer (kMagic's last bit is one): its upper bits are the
+// bin, the lower 28 (`above` the bin's lower end), over 2^31 and less 1/16, are x = ln(1 + q), and
+// so as they stand the first term of 2^31 (e^x - 1). The others, below 2^22, are summed in fp32;
+// the first one left out is below 2^-33 of the weight. Together 2^-30 at most, where the whole
+// series in fp32 is off by 2^-26.7.
 __device__ __forceinline__ Binned binned(double d)
 {
 #pragma clang fp contract(off)
-    const double t = d + kMagic;
+    const uint64_t u = __builtin_bit_cast(uint64_t, d + kMagic);
+    constexpr uint32_t none = (uint32_t)(__builtin_bit_cast(uint64_t, kMagic) >> 28);  // of bin 0
+    constexpr uint32_t low = (1u << 28) - 1;
+    const uint32_t above = (uint32_t)u & low;
     Binned b;
-    b.bin = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
-    const float r = (float)(d - (t - kMagic));  // -1/2 .. 1/2, in bins
-    b.part = (int)((0.5f - r) * (float)kParts);  // exact but for the cut
-    b.part = b.part < kParts ? b.part : kParts - 1;
-    // 2^31 (e^(r/8) - 1) by its series: the first term left out is below 2^-33 of the weight
-    constexpr float c1 = kUnit / 8.f, c2 = c1 / 16.f, c3 = c2 / 24.f, c4 = c3 / 32.f, c5 = c4 / 40.f;
-    b.q = (int)(r * __builtin_fmaf(r, __builtin_fmaf(r, __builtin_fmaf(r, __builtin_fmaf(r, c5, c4), c3), c2), c1));
+    b.bin = (int)((uint32_t)(u >> 28) - none);
+    b.part = (int)((low - above) >> 19);  // 2^28 / kParts each
+    constexpr float c2 = kUnit / 2.f, c3 = kUnit / 6.f, c4 = kUnit / 24.f, c5 = kUnit / 120.f;
+    const float x = __builtin_fmaf((float)above, 0x1p-31f, -0x1p-4f);
+    const float rest = __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, c5, c4), c3), c2);
+    b.over = above + (uint32_t)__builtin_fmaf(x * x, rest, 0.5f);
     return b;
 }
 
@@ -284,7 +294,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_histogram_kernel(const Sa
                                const Binned b = binned(d);
                                // the mask bounds the address of rows above the range, whose bins are not used
                                atomicAdd(reinterpret_cast<unsigned long long *>(&bins[(b.bin + kRange / 2) & (kRange - 1)]),
-                                         ((unsigned long long)1 << kSumBits) + (long long)b.q);
+                                         ((unsigned long long)1 << kSumBits) + b.over);
                            }
                        });
 #pragma unroll
@@ -437,14 +447,15 @@ __device__ __forceinline__ void store_sums(RowSums &sums, uint32_t c, double m, 
 // row gets the same numbers.
 struct Joined {
     uint32_t count[kSlots];
-    int64_t sum[kSlots];
+    uint64_t sum[kSlots];
 };
-__device__ __forceinline__ void unpack(uint64_t v, uint32_t &count, int64_t &sum)
+__device__ __forceinline__ void unpack(uint64_t v, uint32_t &count, uint64_t &sum)
 {
-    const int64_t q = (int64_t)(v << (64 - kSumBits)) >> (64 - kSumBits);
-    sum += q;
-    count += (uint32_t)((v - (uint64_t)q) >> kSumBits);
+    sum += v & (((uint64_t)1 << kSumBits) - 1);
+    count += (uint32_t)(v >> kSumBits);
 }
+// Mass of elements whose weights over kLeast have this sum.
+__device__ __forceinline__ uint64_t mass_of(uint32_t count, uint64_t sum) { return (uint64_t)count * kLeast + sum; }
 template <int THREADS, int AT_ONCE>
 __device__ __forceinline__ void join_slices(const SampleArgs &a, int row, int S, double per_unit, RowSums &sums,
                                             WaveSums<double> &w, Joined &joined)
@@ -472,9 +483,8 @@ __device__ __forceinline__ void join_slices(const SampleArgs &a, int row, int S,
     const int top_bin = binned(fine ? (double)top * per_unit : 0.0).bin;
     const int t = (top_bin - slot) & (kSlots - 1);  // the slot's bin, from the maximum's down
     uint32_t count = 0;
-    int64_t sum = 0;
-    uint64_t packed = 0;
-    // Up to this many elements fit the packed fields of one bin.
+    uint64_t sum = 0, packed = 0;
+    // Up to this many elements fit the packed fields of one bin (each adds less than 2^28 + 2^23).
     const bool together = a.V <= 250000;
     for (int s0 = 0; fine && s0 < S; s0 += AT_ONCE * GROUPS) {
         if (s0 > 0) {
@@ -513,7 +523,7 @@ __device__ __forceinline__ void join_slices(const SampleArgs &a, int row, int S,
         __syncthreads();
     }
     count = threadIdx.x < kBins ? joined.count[threadIdx.x] : 0;
-    const double mass = threadIdx.x < kBins ? ((double)count * (double)kUnit + (double)joined.sum[threadIdx.x]) * factor : 0.0;
+    const double mass = threadIdx.x < kBins ? (double)mass_of(count, joined.sum[threadIdx.x]) * factor : 0.0;
     store_sums<THREADS>(sums, count, mass, w);
 }
 
@@ -842,7 +852,7 @@ __device__ __forceinline__ bool find_listed(Finish<THREADS> &f, int t, int top_b
             const double d = scaled<false>(e.x, per_unit, 0.f);
             const Binned b = binned(d);
             if (d > top_scaled - kBins - 1 && top_bin - b.bin == t)  // not NaN either
-                g(e, b.part, (uint32_t)(2147483648u + (uint32_t)b.q), d);
+                g(e, b.part, b.weight(), d);
         }
     };
     if (threadIdx.x == 0) {
@@ -869,14 +879,14 @@ __device__ __forceinline__ bool find_listed(Finish<THREADS> &f, int t, int top_b
             f.part_sum[threadIdx.x] = 0;
         __syncthreads();
         each([&](const Entry &, int part, uint32_t w, double) {  // packed as in the histogram
-            atomicAdd(&f.part_sum[part], ((unsigned long long)1 << kSumBits) + (long long)(int32_t)(w - 2147483648u));
+            atomicAdd(&f.part_sum[part], ((unsigned long long)1 << kSumBits) + (w - kLeast));
         });
         __syncthreads();
         uint32_t mine = 0;
-        int64_t q = 0;
+        uint64_t over = 0;
         if (threadIdx.x < kParts)
-            unpack(f.part_sum[threadIdx.x], mine, q);
-        const long long my_mass = (long long)mine * 2147483648LL + q;
+            unpack(f.part_sum[threadIdx.x], mine, over);
+        const long long my_mass = (long long)mass_of(mine, over);
         uint32_t c = mine;
         long long m = my_mass;
         block_sums<THREADS>(c, m, f.part_waves);
@@ -972,7 +982,7 @@ __device__ __forceinline__ void search_few(Finish<THREADS> &f, const RowParams &
     const Binned b = binned(scale);
     const int below = mine && scale > top_scaled - kBins - 1 ? top_bin - b.bin : -1;
     const uint64_t place = (uint64_t)order_key(e.x) << 32 | (uint32_t)~e.index;
-    const uint32_t weight = 2147483648u + (uint32_t)b.q;
+    const uint32_t weight = b.weight();
     double limit = kept;
 #pragma unroll 1
     for (int query = kTopK; query <= kToken; ++query) {
@@ -1094,12 +1104,12 @@ __device__ __forceinline__ void narrow(Finish<THREADS> &f, const T *row, int V, 
                 const Binned b = binned(d);
                 const uint32_t k = order_key(x), v = indexes ? ~(uint32_t)i : k;
                 if (top_bin - b.bin == t && (!indexes || k == key) && v >= low && v <= high)
-                    g(v, b.q);
+                    g(v, b.weight());
             }
         });
     };
     for (;;) {  // every turn narrows [low, high] by a factor of 512 or ends
-        range_of(f, [&](auto add) { each([&](uint32_t v, int) { add(v); }); });
+        range_of(f, [&](auto add) { each([&](uint32_t v, uint32_t) { add(v); }); });
         low = f.low_key;
         high = f.high_key;
         const uint32_t number = f.number;
@@ -1110,7 +1120,7 @@ __device__ __forceinline__ void narrow(Finish<THREADS> &f, const T *row, int V, 
                     f.nth = ~low;
                 } else {
                     const double d = scaled<REL>(key_value(low), per_unit, ref);
-                    const unsigned long long w = (unsigned long long)(2147483648LL + binned(d).q);
+                    const unsigned long long w = binned(d).weight();
                     uint32_t j = number;
                     if (query == kTopK) {
                         j = count - before;
@@ -1136,10 +1146,10 @@ __device__ __forceinline__ void narrow(Finish<THREADS> &f, const T *row, int V, 
         if (threadIdx.x == 0)
             f.found = 0xFFFFFFFFu;
         __syncthreads();
-        each([&](uint32_t v, int q) {
+        each([&](uint32_t v, uint32_t w) {
             const uint32_t part = (high - v) >> shift;
             atomicAdd(&f.part_count[part], 1u);
-            atomicAdd(&f.part_sum[part], (unsigned long long)(2147483648LL + q));
+            atomicAdd(&f.part_sum[part], (unsigned long long)w);
         });
         __syncthreads();
         const uint32_t mine = threadIdx.x < kParts ? f.part_count[threadIdx.x] : 0;
@@ -1184,7 +1194,7 @@ __device__ __forceinline__ void find_in_row(Finish<THREADS> &f, const T *row, in
             if (d > top_scaled - kBins - 1) {
                 const Binned b = binned(d);
                 if (top_bin - b.bin == t && (d - top_scaled) / kPerUnit >= log_min_p)
-                    sum += (unsigned long long)(2147483648LL + b.q);
+                    sum += b.weight();
             }
         });
 #pragma unroll
@@ -1277,14 +1287,14 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
             if (d > -(kBins - 1)) {
                 const Binned b = binned(d);
                 atomicAdd(&f.part_count[-b.bin & (kParts - 1)], 1u);
-                atomicAdd(&f.part_sum[-b.bin & (kParts - 1)], (unsigned long long)(long long)b.q);
+                atomicAdd(&f.part_sum[-b.bin & (kParts - 1)], (unsigned long long)b.over);
             }
         });
         __syncthreads();
         const int t = threadIdx.x;
         const uint32_t c = t < kBins ? f.part_count[t] : 0;
         const double m =
-            t < kBins ? ((double)c * (double)kUnit + (double)(long long)f.part_sum[t]) * f.factor[t] : 0.0;
+            t < kBins ? (double)mass_of(c, f.part_sum[t]) * f.factor[t] : 0.0;
         __syncthreads();
         store_sums<THREADS>(f.sums, c, m, f.waves);
     }
@@ -1355,8 +1365,8 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
         if (a.logprobs) {
             // the weight as the sums hold it, so that a token kept alone has share 1
             const float v = key_value(f.key);
-            const int q = binned(fine ? scaled<false>(v, p.per_unit, 0.f) : scaled<true>(v, p.per_unit, top)).q;
-            const double lp = log((double)(2147483648LL + q) * f.factor[t] / kept);
+            const Binned b = binned(fine ? scaled<false>(v, p.per_unit, 0.f) : scaled<true>(v, p.per_unit, top));
+            const double lp = log((double)b.weight() * f.factor[t] / kept);
             a.logprobs[row] = lp < 0.0 ? (float)lp : 0.f;
         }
     }
