@@ -1480,8 +1480,8 @@ __device__ __forceinline__ void count_values(Values &f, const uint16_t *bits, in
     }
 }
 
-// For rows with a logit of more than 65535 elements (two at most): which they are,
-// by their high and then their low bytes, and the counts without them.
+// For rows with a logit of more than 65535 elements (two at most, see kMostByValues): which
+// they are, by their high and then their low bytes, and the counts without them.
 __device__ __forceinline__ void count_without_heavy(Values &f, const uint16_t *row, int V)
 {
     uint32_t high[2] = {0, 0};
@@ -1838,7 +1838,13 @@ int slices_of(int M, int V)
 //   8 x 16000     19 : 18,  23 : 17       64 x 131072   30 : 33,  46 : 32
 //   32 x 65000    23 : 23,  29 : 23       128 x 131072  39 : 33,  75 : 32
 //   256 x 32000   26 : 21,  31 : 20       256 x 131072  48 : 36,  59 : 35
-bool by_values(int M, int V) { return V >= 1 << 13 && V <= (M >= 64 ? kMaxSlice : 1 << 16); }
+//   64 x 152064   32 : 34,  44 : 32       64 x 196607   34 : 39,  45 : 37
+//   128 x 152064  43 : 34,  65 : 32       128 x 196607  49 : 39,  73 : 37
+//   256 x 152064  59 : 37,  79 : 36       256 x 196607  70 : 43,  99 : 42
+// The longest row is the counts': with one element more, three logits could have more
+// than 65535 each.
+constexpr int kMostByValues = 3 * 65536 - 1;
+bool by_values(int M, int V) { return V >= 1 << 13 && V <= (M >= 64 ? kMostByValues : 1 << 16); }
 
 template <typename T>
 hipError_t launch(const SampleArgs &a, hipStream_t stream)
