@@ -569,6 +569,19 @@ struct Search {
 };
 __device__ __forceinline__ double mass_before(const RowSums &s, int t) { return t > 0 ? s.mass[t - 1] : 0.0; }
 __device__ __forceinline__ uint32_t count_before(const RowSums &s, int t) { return t > 0 ? s.count[t - 1] : 0u; }
+// The sums of mass are rounded in another order for each bin, so that one may
+// rise by a rounding at a bin without elements. A crossing found there lies at the
+// end of the last bin with elements, whose last element it is: the value becomes
+// one that no sum in the bin reaches. (That bin is listed: wanted ranges are
+// wider than roundings.)
+__device__ __forceinline__ void leave_empty_bin(const RowSums &s, const Search &find, int &t, double &value)
+{
+    const uint32_t count = s.count[t];
+    if (__builtin_expect(count == count_before(s, t), 0)) {
+        t = find.first_count(count);
+        value = 1e300;
+    }
+}
 
 // The bins whose elements decide. A crossing's value is only known to lie
 // between bounds until the crossing before it is resolved, so it brings a range
@@ -1016,7 +1029,11 @@ __device__ __forceinline__ void search_few(Finish<THREADS> &f, const RowParams &
             mass = below == t && (scale - top_scaled) / kPerUnit >= p.log_min_p ? weight : 0u;
             mass = of_lane(wave_sums(mass), kWave - 1);
         } else {
-            const uint64_t bin = __ballot(below == t);
+            uint64_t bin = __ballot(below == t);
+            if (__builtin_expect(bin == 0, 0)) {
+                leave_empty_bin(f.sums, find, t, value);
+                bin = __ballot(below == t);
+            }
             const uint32_t n = __popcll(bin);
             uint32_t c = 0;
             unsigned long long from = 0;
@@ -1337,6 +1354,7 @@ __global__ __launch_bounds__(THREADS) void sample_finish_kernel(const SampleArgs
             value = (target - mass_before(f.sums, t)) / f.factor[t];
             const double least = query == kTopP ? 0.5 : 0.0;
             value = value > least ? value : least;
+            leave_empty_bin(f.sums, find, t, value);
         }
         if (one_by_one) {
             if (threadIdx.x == 0)
