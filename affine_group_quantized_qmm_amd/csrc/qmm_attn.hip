@@ -29,7 +29,7 @@
 // nontemporal hint, straight past the barriers into registers: the next tile's
 // are in flight while this one is computed.
 //
-// What bounds it is that stream: 6.2 TB/s of 1.61 GB (64 sequences of 4k to 8k
+// What bounds it is that stream: 6.6 TB/s of 1.61 GB (64 sequences of 4k to 8k
 // tokens, 8 heads of 128) where a kernel that does nothing but read such pages
 // reaches 6.75; a fixed 10 to 12 us (the plan, the first pages, the join)
 // where there is little to read.
@@ -50,9 +50,10 @@ constexpr int kJoinThreads = 1024;
 // thousand instructions one after the other, which only another wave of the
 // same SIMD can hide. Heads of 192 and 256, whose registers and LDS leave room
 // for one workgroup on a CU, take two waves a SIMD (131071 tokens of 4 heads of
-// 256: 96 us against 110 with four waves); narrower ones get them from a second
-// workgroup (64 sequences, 8 heads of 128: 260 us with two of four waves, 262
-// with one of eight; 32 sequences of 1000 tokens 28.6 against 31.6).
+// 256: 92 us against 98 with four waves; 8 sequences of 8 rows 41 against 60);
+// narrower ones get them from a second workgroup (64 sequences, 8 heads of 128:
+// 250 us with two of four waves, 252 with one of eight; 32 sequences of 1000
+// tokens 27.9 against 31.4, 256 of 600 85 against 111).
 // So do the most columns (6 tiles of heads of 128), whose accumulators would
 // spill with four.
 constexpr int waves_of(int D, int NT) { return D >= 192 || (D == 128 && NT == 6) ? 8 : 4; }

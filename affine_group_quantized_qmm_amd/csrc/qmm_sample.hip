@@ -43,9 +43,9 @@
 // slices so that few rows still fill the GPU.
 //
 // What bounds it. Few rows: two or three launches one after the other, each with
-// its code to fetch: one row of 131072 fp32 logits takes 20 us (histogram 5,
-// gather 8, finish 5), 16 rows of 151001 with top-k and top-p 24, 32 rows of 32003
-// fp16 logits 24. 256 rows of 131072 fp32 logits take 58 us with top-k 50 and top-p
+// its code to fetch: one row of 131072 fp32 logits takes 18 to 20 us (histogram 5,
+// gather 8, finish 5), 16 rows of 151001 with top-k and top-p 25, 32 rows of 32003
+// fp16 logits 24. 256 rows of 131072 fp32 logits take 57 us with top-k 50 and top-p
 // 0.9, without top-k 66: two passes over 134 MB (27 each at the rate of a copy), and
 // the searches, up to 9 each. With 16-bit logits the histogram still takes 25: a
 // CU issues 20 instructions and one LDS atomic for every element.
