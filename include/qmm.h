@@ -426,8 +426,8 @@ int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stri
  *     s_j = scale * q . k_j,   out = sum_j e^(s_j) v_j / sum_j e^(s_j),
  *     lse = log(sum_j e^(s_j))
  *
- * over the tokens that the row sees; a row that sees none gets zeros and an
- * lse of -infinity. What lies in places that no row sees is not used, whatever
+ * over the tokens that the row sees; a row that sees none, or whose scores are
+ * all -infinity, gets zeros and an lse of -infinity. What lies in places that no row sees is not used, whatever
  * it is; infinities and NaN of a token reach the rows that see it and no
  * others. Products are accumulated in fp32, e^(s) and its sums are fp32, and
  * e^(s) enters the second product as the sum of two 16-bit numbers (good to

@@ -111,3 +111,25 @@ def test_infinities_in_runs_of_many_items():
     out, lse = p.run(max_context=400)
     assert torch.equal(lse, clean_lse)
     same(out, want)
+
+
+@pytest.mark.parametrize("max_context", [1, 300])
+def test_scores_that_are_all_minus_infinity(max_context):
+    """A row whose every score is -infinity is as one that sees nothing; one finite score is enough."""
+    p = Problem([300, 200], [1, 1], 2, 2, 128, 16, BF16, seed=8)
+    p.q[:] = p.q.abs() + 0.5
+    p.kc[torch.isfinite(p.kc)] = 1.0
+    clean, clean_lse = p.run(max_context=max_context)
+    for j in range(300):
+        pg, at = place(p, 0, j, 16)
+        p.kc[pg, 0, at, 3] = -INF
+    out, lse = p.run(max_context=max_context)
+    want, want_lse = clean.clone(), clean_lse.clone()
+    want[0, :2], want_lse[0, :2] = 0.0, -INF
+    same(out, want)
+    same(lse, want_lse)
+    pg, at = place(p, 0, 77, 16)
+    p.kc[pg, 0, at, 3] = 1.0
+    out, lse = p.run(max_context=max_context)
+    v = p.vc[pg, 0, at].to(out.device)
+    assert torch.equal(out[0, 0], v) and torch.equal(out[0, 1], v) and torch.isfinite(lse[0]).all()

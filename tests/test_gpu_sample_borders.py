@@ -67,3 +67,17 @@ def test_log_probabilities():
     share = np.where(got == 1, 1 / (1 + np.exp(d)), np.exp(d) / (1 + np.exp(d)))
     want = np.log(share)
     assert (np.abs(lp.double().cpu().numpy() - want) <= np.abs(want) * 2.0 ** -24 + 2.0 ** -29).all()
+
+
+@pytest.mark.parametrize("V", [131072, 250000, 250001])
+@pytest.mark.parametrize("z", [0.4999, -0.4999])
+def test_bins_full_of_their_heaviest_and_lightest_weights(V, z):
+    """A whole row at the upper or lower end of one bin, up to where counts and
+    sums of weights fill the fields that they share."""
+    dev, qmm = _gpu.dev(), _gpu.lib()
+    u = np.float32(np.random.default_rng(V).random(12, dtype=np.float32))
+    x = torch.full((12, V), z / 8, device=dev)
+    lp = torch.empty(12, device=dev)
+    got = qmm.qmm_sample(x, torch.tensor(u, device=dev), logprobs=lp).cpu().numpy()
+    assert np.array_equal(got, np.floor(u.astype(np.float64) * V).astype(int))
+    assert np.abs(lp.double().cpu().numpy() + np.log(V)).max() <= 2.0 ** -28 + np.log(V) * 2.0 ** -24
