@@ -79,6 +79,13 @@ _lib.qmm_paged_attention_workspace_bytes.argtypes = [_i] * 9
 _lib.qmm_paged_attention_workspace_bytes.restype = _sz
 _lib.qmm_paged_attention.argtypes = [_p, _l, _p, _p, _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
                                      _f32, _i, _i, _p, _sz, _p]
+_lib.qmm_qk_norm_rope_quant.argtypes = [_p, _p, _p, _l, _l, _l, _i, _p, _p, _f32, _f32, _p, _p, _i, _i, _p, _p, _p, _p,
+                                        _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _p]
+_lib.qmm_quant_cache_read.argtypes = [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _p]
+_lib.qmm_paged_attention_quant_workspace_bytes.argtypes = [_i] * 11
+_lib.qmm_paged_attention_quant_workspace_bytes.restype = _sz
+_lib.qmm_paged_attention_quant.argtypes = [_p, _l, _p, _p, _p, _p, _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
+                                           _i, _i, _i, _i, _i, _f32, _i, _i, _p, _sz, _p]
 _lib.qmm_sample_workspace_bytes.argtypes = [_i, _i]
 _lib.qmm_sample_workspace_bytes.restype = _sz
 _lib.qmm_sample.argtypes = [_p, _l, _i, _p, _p, _p, _p, _p, _p, _p, _i, _i, _p, _sz, _p]
@@ -93,7 +100,8 @@ for _f in (_lib.qmm_pack, _lib.qmm_forward, _lib.qmm_forward_rowexact, _lib.qmm_
            _lib.qmm_forward_splitk, _lib.qmm_forward_splitk_noalloc,
            _lib.qmm_forward_kernel, _lib.qmm_forward_fused, _lib.qmm_repack_tiled,
            _lib.qmm_forward_tiled, _lib.qmm_validate, _lib.qmm_stream_read, _lib.qmm_admit,
-           _lib.qmm_admission, _lib.qmm_qk_norm_rope, _lib.qmm_paged_attention, _lib.qmm_sample):
+           _lib.qmm_admission, _lib.qmm_qk_norm_rope, _lib.qmm_paged_attention, _lib.qmm_sample,
+           _lib.qmm_qk_norm_rope_quant, _lib.qmm_quant_cache_read, _lib.qmm_paged_attention_quant):
     _f.restype = _i
 
 EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16", "qmm_forward_splitk",
@@ -103,7 +111,9 @@ EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16
             "qmm_forward_tiled", "qmm_stream_read", "qmm_stream_read_sink_words",
             "qmm_admit_workspace_bytes", "qmm_admit", "qmm_admission", "qmm_admission_clear",
             "qmm_qk_norm_rope", "qmm_paged_attention_workspace_bytes", "qmm_paged_attention",
-            "qmm_sample_workspace_bytes", "qmm_sample")
+            "qmm_sample_workspace_bytes", "qmm_sample",
+            "qmm_qk_norm_rope_quant", "qmm_quant_cache_read", "qmm_paged_attention_quant_workspace_bytes",
+            "qmm_paged_attention_quant")
 
 QMM_MAX_FUSED = 4  # projections per qmm_forward_fused call
 
@@ -467,6 +477,45 @@ def qmm_paged_attention(q, k_cache, v_cache, block_table, context_lens, row_star
     return _step_result(_binding.paged_attention(q, k_cache, v_cache, block_table, context_lens, row_starts, max_rows,
                                                  max_context, scale, window, sinks, out, lse, workspace,
                                                  _step_stream(q)), "qmm_paged_attention")
+
+
+# A quantized cache is four int32 (or uint32) tensors: codes [num_pages, Hkv,
+# page_size, D*bits/32] and (scale | bias << 16) words [.., D/G], for keys and for
+# values.
+def qmm_qk_norm_rope_quant(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_codes, k_sb, v_codes, v_sb,
+                           bits: int, G: int, *, eps: float = 1e-6, weight_offset: float = 0.0,
+                           interleaved: bool = False, dtype: torch.dtype = torch.float16, out=None) -> torch.Tensor:
+    """qmm_qk_norm_rope with k and v quantized as they are written to `slots`;
+    returns the queries, in `out` or a new tensor of `dtype` (float16 or bfloat16)."""
+    return _step_result(_binding.qk_norm_rope_quant(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_codes,
+                                                    k_sb, v_codes, v_sb, bits, G, out, dtype, eps, weight_offset,
+                                                    interleaved, _step_stream(q)), "qmm_qk_norm_rope_quant")
+
+
+def qmm_quant_cache_read(k_codes, k_sb, v_codes, v_sb, bits: int, G: int, slots, *,
+                         dtype: torch.dtype = torch.float16, k_out=None, v_out=None):
+    """(k, v) [M, Hkv, D] of the tokens at `slots` (int32 [M]) of a quantized
+    cache, as float16 (the numbers that the codes stand for) or bfloat16; zeros
+    for slots outside the cache."""
+    return _step_result(_binding.quant_cache_read(k_codes, k_sb, v_codes, v_sb, bits, G, slots, k_out, v_out, dtype,
+                                                  _step_stream(k_codes)), "qmm_quant_cache_read")
+
+
+def qmm_paged_attention_quant_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int, max_rows: int,
+                                              max_context: int, window: int, sinks: int, bits: int, G: int) -> int:
+    return int(_lib.qmm_paged_attention_quant_workspace_bytes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks,
+                                                              bits, G))
+
+
+def qmm_paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits: int, G: int, block_table, context_lens, row_starts,
+                              max_rows: int, max_context: int, *, scale: float | None = None, window: int = 0,
+                              sinks: int = 0, out=None, lse=None, workspace=None) -> torch.Tensor:
+    """qmm_paged_attention over a quantized cache; q and the result are float16 or
+    bfloat16."""
+    return _step_result(_binding.paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits, G, block_table,
+                                                       context_lens, row_starts, max_rows, max_context, scale, window,
+                                                       sinks, out, lse, workspace, _step_stream(q)),
+                        "qmm_paged_attention_quant")
 
 
 def qmm_sample_workspace_bytes(M: int, V: int) -> int:

@@ -38,184 +38,10 @@
 // to fill the GPU as they are, and their lengths are known on the GPU alone.
 // Every workgroup sums up the lengths and finds its own equal share (see
 // "How they are dealt out" below); a second kernel joins pieces of one item.
-#include "qmm_device.hpp"
-#include "qmm_kernels.hpp"
-#include "qmm_step.hpp"
+#include "qmm_attn.hpp"
 
 namespace qmm {
 namespace {
-
-constexpr int kJoinThreads = 1024;
-// Waves of a workgroup; each has 16 tokens of a tile. A turn of a wave is some
-// thousand instructions one after the other, which only another wave of the
-// same SIMD can hide. Heads of 192 and 256, whose registers and LDS leave room
-// for one workgroup on a CU, take two waves a SIMD (131071 tokens of 4 heads of
-// 256: 92 us against 98 with four waves; 8 sequences of 8 rows 41 against 60);
-// narrower ones get them from a second workgroup (64 sequences, 8 heads of 128:
-// 250 us with two of four waves, 252 with one of eight; 32 sequences of 1000
-// tokens 27.9 against 31.4, 256 of 600 85 against 111).
-// So do the most columns (6 tiles of heads of 128), whose accumulators would
-// spill with four.
-constexpr int waves_of(int D, int NT) { return D >= 192 || (D == 128 && NT == 6) ? 8 : 4; }
-constexpr int tile_of(int D, int NT) { return 16 * waves_of(D, NT); }
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;   // token without a row in the cache
-
-typedef float float2_t __attribute__((ext_vector_type(2)));
-typedef short short4_t __attribute__((ext_vector_type(4)));
-
-// A type's matrix instructions and how its weights are scaled: p = 2^(s - m +
-// kLift), where a score may pass the running maximum m by kRaise (both log2);
-// kUnlift is 2^-kLift.
-template <typename T>
-struct Elem;
-template <>
-struct Elem<_Float16> {
-    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
-    typedef _Float16 x4 __attribute__((ext_vector_type(4)));
-    static constexpr uint32_t exponent = 0x7C00u;
-    // p is at most 2^15.5, below the type's largest, and 2^15 at the maximum: the
-    // second part's steps of 2^-24 then hold a weight to 2^-40 of the largest one.
-    static constexpr float kLift = 15.0f, kUnlift = 0x1p-15f, kRaise = 0.5f;
-    static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-    }
-};
-template <>
-struct Elem<__bf16> {
-    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
-    typedef __bf16 x4 __attribute__((ext_vector_type(4)));
-    static constexpr uint32_t exponent = 0x7F80u;
-    static constexpr float kLift = 0.0f, kUnlift = 1.0f, kRaise = 8.0f;  // fp32's range: no floor to keep away from
-    static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-    }
-};
-
-template <int CTRL>
-__device__ __forceinline__ int dpp_or_zero(int v)
-{
-    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
-}
-// Inclusive sums over the lanes of a wave: within rows of 16 by shifts, then
-// the rows before.
-__device__ __forceinline__ int wave_scan(int v)
-{
-    v += dpp_or_zero<0x111>(v);  // row_shr:1
-    v += dpp_or_zero<0x112>(v);
-    v += dpp_or_zero<0x114>(v);
-    v += dpp_or_zero<0x118>(v);
-    const int r0 = __builtin_amdgcn_readlane(v, 15), r1 = __builtin_amdgcn_readlane(v, 31),
-              r2 = __builtin_amdgcn_readlane(v, 47);
-    const int row = threadIdx.x % kWave / 16;
-    return v + (row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0);
-}
-
-// A 32-bit word with its non-finite halves set to zero.
-template <typename T>
-__device__ __forceinline__ uint32_t finite_halves(uint32_t w)
-{
-    constexpr uint32_t e = Elem<T>::exponent;
-    if ((w & e) == e)
-        w &= 0xFFFF0000u;
-    if ((w >> 16 & e) == e)
-        w &= 0x0000FFFFu;
-    return w;
-}
-
-__device__ __forceinline__ int row_of_column(const AttnArgs &a, int x)
-{
-    return divide(x, a.group_magic, a.group_shift);
-}
-
-// The rows and tiles of (sequence b, column chunk): what a workgroup and the
-// join agree on.
-struct Span {
-    int start, n;        // first row in q, number of rows
-    int first_pos;       // position of row 0
-    int pmin, pmax;      // positions of the chunk's first and last row
-    int sink_tiles, low; // tiles [0, sink_tiles) and from `low` on
-    int count;           // tiles in all
-};
-
-template <int TILE>
-__device__ __forceinline__ Span span_of(const AttnArgs &a, int begin, int end, int len, int x0, int cols)
-{
-    Span s;
-    const bool sound = begin >= 0 && begin <= end && end <= a.T;
-    s.start = sound ? begin : 0;
-    s.n = sound ? end - begin : 0;
-    const int G = a.G;
-    len = len < 0 ? 0 : len;
-    s.first_pos = len - s.n;
-    s.sink_tiles = s.low = s.count = 0;
-    s.pmin = s.pmax = -1;
-    if (x0 >= s.n * G)
-        return s;
-    const int last = x0 + cols < s.n * G ? x0 + cols : s.n * G;
-    s.pmin = s.first_pos + row_of_column(a, x0);
-    s.pmax = s.first_pos + row_of_column(a, last - 1);
-    // tokens past the table have no page
-    const int capacity = a.max_pages * a.page_size;
-    const int high = s.pmax + 1 < capacity ? s.pmax + 1 : capacity;
-    if (high <= 0)
-        return s;
-    const int high_tile = (high + TILE - 1) / TILE;
-    if (a.window > 0) {
-        const int first = s.pmin - a.window + 1;
-        s.low = first > 0 ? first / TILE : 0;
-        s.low = s.low < high_tile ? s.low : high_tile;
-        const int sink_tiles = a.sinks / TILE + (a.sinks % TILE != 0);
-        s.sink_tiles = sink_tiles < s.low ? sink_tiles : s.low;
-    }
-    s.count = s.sink_tiles + high_tile - s.low;
-    return s;
-}
-
-template <int TILE>
-__device__ __forceinline__ Span span_of(const AttnArgs &a, int b, int x0, int cols)
-{
-    return span_of<TILE>(a, a.row_starts[b], a.row_starts[b + 1], a.context_lens[b], x0, cols);
-}
-
-// An item is one kv head of one column chunk of one sequence; its tiles are
-// at least one, so that rows that see nothing are written too. Items are
-// numbered by sequence, chunk and head. How they are dealt out:
-//   whole    one workgroup an item; no join.
-//   pieces   (few items) each item in equal pieces of at most `size` tiles, one
-//            a workgroup, with the smallest size that gives at most as many
-//            pieces as workgroups.
-//   runs     (about as many items as workgroups) the tiles of all items one after
-//            the other, in equal runs: a run may hold the end of one item and
-//            the beginning of another, and no workgroup has more than its share
-//            whatever the lengths are.
-__device__ __forceinline__ int tiles_of(const Span &s) { return s.count > 1 ? s.count : 1; }
-
-// Run w takes `each` tiles, one more for the first `more` runs.
-struct Runs {
-    int each, more;
-};
-__device__ __forceinline__ int first_tile(Runs r, int w) { return w * r.each + (w < r.more ? w : r.more); }
-__device__ __forceinline__ int owner_of(Runs r, int tile)
-{
-    const int longer = r.more * (r.each + 1);
-    return tile < longer ? (uint32_t)tile / (uint32_t)(r.each + 1)
-                         : r.more + (uint32_t)(tile - longer) / (uint32_t)r.each;
-}
-
-// A run's partial results: of an item that it begins (but does not finish), and
-// of one that it does not begin (its first).
-__device__ __forceinline__ int slot_of(int w, bool begins) { return 2 * w + (begins ? 1 : 0); }
-
-// What a barrier has to order here is LDS only: loads of the next tile stay in
-// flight across it.
-__device__ __forceinline__ void lds_barrier()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 template <typename T, int D, int NT>
 __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const AttnArgs a)
@@ -249,127 +75,14 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
     const int G = a.G;
     constexpr int kColumns = 16 * NT;
 
-    // Where the run starts: (sequence, chunk, head, tile), and its length.
-    int b, chunk, h, tile = 0, w = 0, left, item_unit = 0, here = 1;
-    int run_begin, run_end, run_len;  // of sequence b
-    Runs runs{1, 0};
-    if (a.whole) {
-        // One item a workgroup; the chunks of a head are 8 apart, that is on one
-        // XCD, behind one L2.
-        const int grp = blockIdx.x / (8 * a.chunks), rem = blockIdx.x % (8 * a.chunks);
-        chunk = rem / 8;
-        const int item = grp * 8 + rem % 8;
-        h = item % a.Hkv;
-        b = item / a.Hkv;
-        if (b >= a.B)
-            return;
-        run_begin = a.row_starts[b];
-        run_end = a.row_starts[b + 1];
-        run_len = a.context_lens[b];
-        const Span s = span_of<kTile>(a, run_begin, run_end, run_len, chunk * kColumns, kColumns);
-        if (chunk * kColumns >= s.n * G)
-            return;
-        left = tiles_of(s);
-    } else {
-        w = blockIdx.x;
-        // Sequences are shared out to the lanes in order; the waves do the same.
-        // The host has checked that the sum of tiles has 31 bits. Up to 64
-        // sequences of one chunk stay in the lanes' registers.
-        const bool small = a.B <= kWave && a.chunks == 1;
-        const int each = (a.B + kWave - 1) / kWave;
-        const int b0 = lane * each, b1 = b0 + each < a.B ? b0 + each : a.B;
-        int lane_begin = 0, lane_end = 0, lane_len = 0, lane_tiles = 0;
-        if (__builtin_expect(small, 1)) {
-            if (lane < a.B) {
-                lane_begin = a.row_starts[lane];
-                lane_end = a.row_starts[lane + 1];
-                lane_len = a.context_lens[lane];
-            }
-            const Span s = span_of<kTile>(a, lane_begin, lane_end, lane_len, 0, kColumns);
-            lane_tiles = s.n > 0 ? tiles_of(s) : 0;
-        }
-        // Tiles of this lane's items, or pieces of `size` tiles.
-        auto sum_of = [&](int size) {
-            int sum = 0;
-            if (__builtin_expect(small, 1))
-                sum = size == 1 ? lane_tiles : (uint32_t)(lane_tiles + size - 1) / (uint32_t)size;
-            else
-                for (int i = b0; i < b1; ++i)
-                    for (int k = 0; k < a.chunks; ++k) {
-                        const Span s = span_of<kTile>(a, i, k * kColumns, kColumns);
-                        if (k * kColumns >= s.n * G)
-                            break;
-                        sum += size == 1 ? tiles_of(s) : (uint32_t)(tiles_of(s) + size - 1) / (uint32_t)size;
-                    }
-            return sum * a.Hkv;
-        };
-        int mine = sum_of(1), upto = wave_scan(mine), size = 1, from = w;
-        int units = __builtin_amdgcn_readlane(upto, kWave - 1);  // runs are dealt in tiles, pieces one by one
-        left = 1;
-        if (a.pieces) {
-            size = (units + a.groups - 1) / (uint32_t)a.groups;
-            for (;;) {  // ends: with a size of the longest item every item is one piece
-                size = size > 1 ? size : 1;
-                mine = sum_of(size);
-                upto = wave_scan(mine);
-                units = __builtin_amdgcn_readlane(upto, kWave - 1);
-                if (units <= a.groups)
-                    break;
-                size += (size + 7) / 8;
-            }
-            if (w >= units)
-                return;
-        } else {
-            const uint32_t groups = units < a.groups ? units : a.groups;
-            if (w >= (int)groups)
-                return;
-            runs.each = units / groups;
-            runs.more = units - runs.each * groups;
-            from = first_tile(runs, w);
-            left = first_tile(runs, w + 1) - from;
-        }
-        // The lane whose share holds the run's first unit, then the item in it.
-        const int in = __builtin_ctzll(__ballot(from < upto));
-        int at = __builtin_amdgcn_readlane(upto - mine, in);
-        b = in * each;
-        chunk = 0;
-        int count;
-        if (__builtin_expect(small, 1)) {
-            count = __builtin_amdgcn_readlane(lane_tiles, in);
-            here = (uint32_t)(count + size - 1) / (uint32_t)size;
-            run_begin = __builtin_amdgcn_readlane(lane_begin, in);
-            run_end = __builtin_amdgcn_readlane(lane_end, in);
-            run_len = __builtin_amdgcn_readlane(lane_len, in);
-        } else {
-            for (;;) {
-                if (b >= a.B)
-                    return;  // not reached: the sums above found the unit
-                const Span s = span_of<kTile>(a, b, chunk * kColumns, kColumns);
-                if (chunk == a.chunks || chunk * kColumns >= s.n * G) {
-                    chunk = 0;
-                    ++b;
-                    continue;
-                }
-                count = tiles_of(s);
-                here = (uint32_t)(count + size - 1) / (uint32_t)size;
-                if (from < at + here * a.Hkv)
-                    break;
-                at += here * a.Hkv;
-                ++chunk;
-            }
-            run_begin = a.row_starts[b];
-            run_end = a.row_starts[b + 1];
-            run_len = a.context_lens[b];
-        }
-        h = (uint32_t)(from - at) / (uint32_t)here;
-        item_unit = at + h * here;
-        tile = from - item_unit;
-        if (a.pieces) {  // piece `tile` of `here` equal ones
-            const int q = (uint32_t)count / (uint32_t)here, more = count - q * here, piece = tile;
-            tile = first_tile(Runs{q, more}, piece);
-            left = first_tile(Runs{q, more}, piece + 1) - tile;
-        }
-    }
+    Start at_first;
+    if (!find_start<kTile, kColumns>(a, at_first))
+        return;
+    int b = at_first.b, chunk = at_first.chunk, h = at_first.h, tile = at_first.tile, left = at_first.left;
+    int item_unit = at_first.item_unit;
+    int run_begin = at_first.run_begin, run_end = at_first.run_end, run_len = at_first.run_len;  // of sequence b
+    const int w = at_first.w, here = at_first.here;
+    const Runs runs = at_first.runs;
     const int tr_offset = (4 * c + n / 4) * kPitch + n % 4 * 8;
 
     // Infinities and NaN in V of a tile that every row sees whole go through both
@@ -792,74 +505,6 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_kernel(const 
     }
 }
 
-// Join of the pieces of an item that several runs share:
-// sum_z acc_z 2^(m_z - M) over sum_z l_z 2^(m_z - M) for each column. A
-// workgroup's threads are D/4 values wide and the rest of them share the
-// pieces, so that their loads are in flight together.
-template <typename T, int D>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a, int columns)
-{
-    using E = Elem<T>;
-    constexpr int W = D / 4;                // threads of one piece's values
-    const int P = blockDim.x / W;           // pieces read at a time
-    __shared__ float4_t part[kJoinThreads / W][W];
-    __shared__ float sums[kJoinThreads / W];
-    const int G = a.G;
-    const int h = blockIdx.x % a.Hkv, k = blockIdx.x / a.Hkv % a.chunks, b = blockIdx.x / a.Hkv / a.chunks;
-    const int x0 = k * columns;
-    const int begin = a.row_starts[b], end = a.row_starts[b + 1];
-    const int2 join = a.joins[blockIdx.x];  // of items that exist
-    const int rows = begin >= 0 && begin <= end && end <= a.T ? end - begin : 0;
-    const int live = x0 + columns < rows * G ? columns : rows * G - x0;
-    if (live <= 0 || join.x == join.y)
-        return;
-    const int pieces = join.y - join.x + 1;
-    auto slot = [&](int z) { return (int64_t)slot_of(join.x + z, z == 0) * columns; };
-    for (int col = blockIdx.y; col < live; col += gridDim.y) {
-        const int x = x0 + col, r = row_of_column(a, x);
-        const int64_t at_row = (int64_t)(begin + r) * a.Hq + h * G + (x - r * G);
-        const float2_t *ml = reinterpret_cast<const float2_t *>(a.part_ml) + col;
-        float top = -__builtin_inff();
-        for (int z = threadIdx.x % kWave; z < pieces; z += kWave)
-            top = fmaxf(top, ml[slot(z)].x);
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2)
-            top = fmaxf(top, __shfl_xor(top, d));
-        const int d4 = threadIdx.x % W, first = threadIdx.x / W;
-        float4_t o{0.f, 0.f, 0.f, 0.f};
-        float total = 0.f;
-        if (first < P) {
-#pragma unroll 8
-            for (int z = first; z < pieces; z += P) {
-                const float2_t v = ml[slot(z)];
-                const float f = top == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(v.x - top);
-                total += v.y * f;
-                o += *reinterpret_cast<const float4_t *>(a.part_acc + (slot(z) + col) * D + d4 * 4) * f;
-            }
-            part[first][d4] = o;
-            if (d4 == 0)
-                sums[first] = total;
-        }
-        __syncthreads();
-        if (first == 0) {
-            for (int p = 1; p < P && p < pieces; ++p) {
-                o += part[p][d4];
-                total += sums[p];
-            }
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-            typename E::x4 y;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                y[k] = (T)(o[k] * inv);
-            *reinterpret_cast<typename E::x4 *>(static_cast<T *>(a.out) + at_row * D + d4 * 4) = y;
-            if (a.lse && d4 == 0)
-                a.lse[at_row] = total == 0.f ? -__builtin_inff()
-                                             : (top + __builtin_amdgcn_logf(total * E::kUnlift)) * 0.69314718055994530942f;
-        }
-        __syncthreads();
-    }
-}
-
 template <typename T, int D, int NT>
 hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
@@ -867,14 +512,9 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.whole)
         return e;
-    attn_join_kernel<T, D><<<dim3((uint32_t)p.items, p.join_columns), p.join_threads, 0, stream>>>(a, 16 * NT);
+    attn_join_kernel<Elem<T>, T, D><<<dim3((uint32_t)p.items, p.join_columns), p.join_threads, 0, stream>>>(a, 16 * NT);
     return hipGetLastError();
 }
-
-// Column tiles that a workgroup takes at most: with more, the accumulators
-// (D / 16 registers a tile) and the queries in LDS would leave room for one
-// workgroup on a CU instead of two.
-constexpr int most_col_tiles(int D) { return D == 64 || D == 128 ? 6 : D == 96 ? 4 : 3; }
 
 template <typename T, int D>
 hipError_t launch_cols(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
@@ -913,12 +553,12 @@ hipError_t launch_dim(const AttnArgs &a, const AttnPlan &p, int D, hipStream_t s
 bool attn_head_dim_supported(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 
 AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks,
-                   int page_size, int max_pages)
+                   int page_size, int max_pages, int bits)
 {
     AttnPlan p;
     const int64_t columns = (int64_t)max_rows * (Hq / Hkv);
     const int64_t col_tiles = (columns + 15) / 16;
-    const int64_t chunks = (col_tiles + most_col_tiles(D) - 1) / most_col_tiles(D);
+    const int64_t chunks = (col_tiles + most_col_tiles(D, bits != 0) - 1) / most_col_tiles(D, bits != 0);
     p.col_tiles = (int)((col_tiles + chunks - 1) / chunks);
     p.col_tiles += p.col_tiles == 5;
     p.chunks = (int)((col_tiles + p.col_tiles - 1) / p.col_tiles);
@@ -964,8 +604,10 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context,
     return p;
 }
 
-hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, void *workspace, hipStream_t stream)
+hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, int bits, void *workspace,
+                                  hipStream_t stream)
 {
+    a.io_bf16 = bf16;
     a.chunks = p.chunks;
     a.groups = p.groups;
     a.whole = p.whole;
@@ -981,7 +623,12 @@ hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf1
         a.part_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.join_bytes);
         a.part_ml = a.part_acc + columns * D;
     }
-    return bf16 ? launch_dim<__bf16>(a, p, D, stream) : launch_dim<_Float16>(a, p, D, stream);
+    switch (bits) {
+    case 0: return bf16 ? launch_dim<__bf16>(a, p, D, stream) : launch_dim<_Float16>(a, p, D, stream);
+    case 4: return launch_attention_codes4(a, p, D, stream);
+    case 8: return launch_attention_codes8(a, p, D, stream);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace qmm

@@ -1,0 +1,400 @@
+// What the attention kernels over the paged cache share: the matrix
+// instructions of an element type, how a call's work is dealt out to workgroups,
+// and the join of what was cut. The kernels are in qmm_attn.hip (16-bit rows) and
+// qmm_attn_codes.hpp (quantized caches).
+#pragma once
+
+#include "qmm_device.hpp"
+#include "qmm_kernels.hpp"
+#include "qmm_step.hpp"
+
+namespace qmm {
+namespace {
+
+constexpr int kJoinThreads = 1024;
+// Waves of a workgroup; each has 16 tokens of a tile. A turn of a wave is some
+// thousand instructions one after the other, which only another wave of the
+// same SIMD can hide. Heads of 192 and 256, whose registers and LDS leave room
+// for one workgroup on a CU, take two waves a SIMD (131071 tokens of 4 heads of
+// 256: 92 us against 98 with four waves; 8 sequences of 8 rows 41 against 60);
+// narrower ones get them from a second workgroup (64 sequences, 8 heads of 128:
+// 250 us with two of four waves, 252 with one of eight; 32 sequences of 1000
+// tokens 27.9 against 31.4, 256 of 600 85 against 111).
+// So do the most columns (6 tiles of heads of 128), whose accumulators would
+// spill with four.
+constexpr int waves_of(int D, int NT) { return D >= 192 || (D == 128 && NT == 6) ? 8 : 4; }
+constexpr int tile_of(int D, int NT) { return 16 * waves_of(D, NT); }
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;   // token without a row in the cache
+
+typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
+
+// A type's matrix instructions and how its weights are scaled: p = 2^(s - m +
+// kLift), where a score may pass the running maximum m by kRaise (both log2);
+// kUnlift is 2^-kLift.
+template <typename T>
+struct Elem;
+template <>
+struct Elem<_Float16> {
+    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+    typedef _Float16 x4 __attribute__((ext_vector_type(4)));
+    static constexpr uint32_t exponent = 0x7C00u;
+    // p is at most 2^15.5, below the type's largest, and 2^15 at the maximum: the
+    // second part's steps of 2^-24 then hold a weight to 2^-40 of the largest one.
+    static constexpr float kLift = 15.0f, kUnlift = 0x1p-15f, kRaise = 0.5f;
+    static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Elem<__bf16> {
+    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+    typedef __bf16 x4 __attribute__((ext_vector_type(4)));
+    static constexpr uint32_t exponent = 0x7F80u;
+    static constexpr float kLift = 0.0f, kUnlift = 1.0f, kRaise = 8.0f;  // fp32's range: no floor to keep away from
+    static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_or_zero(int v)
+{
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+// Inclusive sums over the lanes of a wave: within rows of 16 by shifts, then
+// the rows before.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += dpp_or_zero<0x111>(v);  // row_shr:1
+    v += dpp_or_zero<0x112>(v);
+    v += dpp_or_zero<0x114>(v);
+    v += dpp_or_zero<0x118>(v);
+    const int r0 = __builtin_amdgcn_readlane(v, 15), r1 = __builtin_amdgcn_readlane(v, 31),
+              r2 = __builtin_amdgcn_readlane(v, 47);
+    const int row = threadIdx.x % kWave / 16;
+    return v + (row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0);
+}
+
+// A 32-bit word with its non-finite halves set to zero.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w)
+{
+    constexpr uint32_t e = Elem<T>::exponent;
+    if ((w & e) == e)
+        w &= 0xFFFF0000u;
+    if ((w >> 16 & e) == e)
+        w &= 0x0000FFFFu;
+    return w;
+}
+
+__device__ __forceinline__ int row_of_column(const AttnArgs &a, int x)
+{
+    return divide(x, a.group_magic, a.group_shift);
+}
+
+// The rows and tiles of (sequence b, column chunk): what a workgroup and the
+// join agree on.
+struct Span {
+    int start, n;        // first row in q, number of rows
+    int first_pos;       // position of row 0
+    int pmin, pmax;      // positions of the chunk's first and last row
+    int sink_tiles, low; // tiles [0, sink_tiles) and from `low` on
+    int count;           // tiles in all
+};
+
+template <int TILE>
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int begin, int end, int len, int x0, int cols)
+{
+    Span s;
+    const bool sound = begin >= 0 && begin <= end && end <= a.T;
+    s.start = sound ? begin : 0;
+    s.n = sound ? end - begin : 0;
+    const int G = a.G;
+    len = len < 0 ? 0 : len;
+    s.first_pos = len - s.n;
+    s.sink_tiles = s.low = s.count = 0;
+    s.pmin = s.pmax = -1;
+    if (x0 >= s.n * G)
+        return s;
+    const int last = x0 + cols < s.n * G ? x0 + cols : s.n * G;
+    s.pmin = s.first_pos + row_of_column(a, x0);
+    s.pmax = s.first_pos + row_of_column(a, last - 1);
+    // tokens past the table have no page
+    const int capacity = a.max_pages * a.page_size;
+    const int high = s.pmax + 1 < capacity ? s.pmax + 1 : capacity;
+    if (high <= 0)
+        return s;
+    const int high_tile = (high + TILE - 1) / TILE;
+    if (a.window > 0) {
+        const int first = s.pmin - a.window + 1;
+        s.low = first > 0 ? first / TILE : 0;
+        s.low = s.low < high_tile ? s.low : high_tile;
+        const int sink_tiles = a.sinks / TILE + (a.sinks % TILE != 0);
+        s.sink_tiles = sink_tiles < s.low ? sink_tiles : s.low;
+    }
+    s.count = s.sink_tiles + high_tile - s.low;
+    return s;
+}
+
+template <int TILE>
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int b, int x0, int cols)
+{
+    return span_of<TILE>(a, a.row_starts[b], a.row_starts[b + 1], a.context_lens[b], x0, cols);
+}
+
+// An item is one kv head of one column chunk of one sequence; its tiles are
+// at least one, so that rows that see nothing are written too. Items are
+// numbered by sequence, chunk and head. How they are dealt out:
+//   whole    one workgroup an item; no join.
+//   pieces   (few items) each item in equal pieces of at most `size` tiles, one
+//            a workgroup, with the smallest size that gives at most as many
+//            pieces as workgroups.
+//   runs     (about as many items as workgroups) the tiles of all items one after
+//            the other, in equal runs: a run may hold the end of one item and
+//            the beginning of another, and no workgroup has more than its share
+//            whatever the lengths are.
+__device__ __forceinline__ int tiles_of(const Span &s) { return s.count > 1 ? s.count : 1; }
+
+// Run w takes `each` tiles, one more for the first `more` runs.
+struct Runs {
+    int each, more;
+};
+__device__ __forceinline__ int first_tile(Runs r, int w) { return w * r.each + (w < r.more ? w : r.more); }
+__device__ __forceinline__ int owner_of(Runs r, int tile)
+{
+    const int longer = r.more * (r.each + 1);
+    return tile < longer ? (uint32_t)tile / (uint32_t)(r.each + 1)
+                         : r.more + (uint32_t)(tile - longer) / (uint32_t)r.each;
+}
+
+// A run's partial results: of an item that it begins (but does not finish), and
+// of one that it does not begin (its first).
+__device__ __forceinline__ int slot_of(int w, bool begins) { return 2 * w + (begins ? 1 : 0); }
+
+// Where the run of a workgroup starts, and its length in tiles.
+struct Start {
+    int b, chunk, h, tile;
+    int w, left, item_unit, here;
+    int run_begin, run_end, run_len;  // of sequence b
+    Runs runs;
+};
+// false: nothing to do.
+template <int kTile, int kColumns>
+__device__ __forceinline__ bool find_start(const AttnArgs &a, Start &start)
+{
+    const int lane = threadIdx.x % kWave;
+    int b, chunk, h, tile = 0, w = 0, left, item_unit = 0, here = 1;
+    int run_begin, run_end, run_len;
+    Runs runs{1, 0};
+    if (a.whole) {
+        // One item a workgroup; the chunks of a head are 8 apart, that is on one
+        // XCD, behind one L2.
+        const int grp = blockIdx.x / (8 * a.chunks), rem = blockIdx.x % (8 * a.chunks);
+        chunk = rem / 8;
+        const int item = grp * 8 + rem % 8;
+        h = item % a.Hkv;
+        b = item / a.Hkv;
+        if (b >= a.B)
+            return false;
+        run_begin = a.row_starts[b];
+        run_end = a.row_starts[b + 1];
+        run_len = a.context_lens[b];
+        const Span s = span_of<kTile>(a, run_begin, run_end, run_len, chunk * kColumns, kColumns);
+        if (chunk * kColumns >= s.n * a.G)
+            return false;
+        left = tiles_of(s);
+    } else {
+        w = blockIdx.x;
+        // Sequences are shared out to the lanes in order; the waves do the same.
+        // The host has checked that the sum of tiles has 31 bits. Up to 64
+        // sequences of one chunk stay in the lanes' registers.
+        const bool small = a.B <= kWave && a.chunks == 1;
+        const int each = (a.B + kWave - 1) / kWave;
+        const int b0 = lane * each, b1 = b0 + each < a.B ? b0 + each : a.B;
+        int lane_begin = 0, lane_end = 0, lane_len = 0, lane_tiles = 0;
+        if (__builtin_expect(small, 1)) {
+            if (lane < a.B) {
+                lane_begin = a.row_starts[lane];
+                lane_end = a.row_starts[lane + 1];
+                lane_len = a.context_lens[lane];
+            }
+            const Span s = span_of<kTile>(a, lane_begin, lane_end, lane_len, 0, kColumns);
+            lane_tiles = s.n > 0 ? tiles_of(s) : 0;
+        }
+        // Tiles of this lane's items, or pieces of `size` tiles.
+        auto sum_of = [&](int size) {
+            int sum = 0;
+            if (__builtin_expect(small, 1))
+                sum = size == 1 ? lane_tiles : (uint32_t)(lane_tiles + size - 1) / (uint32_t)size;
+            else
+                for (int i = b0; i < b1; ++i)
+                    for (int k = 0; k < a.chunks; ++k) {
+                        const Span s = span_of<kTile>(a, i, k * kColumns, kColumns);
+                        if (k * kColumns >= s.n * a.G)
+                            break;
+                        sum += size == 1 ? tiles_of(s) : (uint32_t)(tiles_of(s) + size - 1) / (uint32_t)size;
+                    }
+            return sum * a.Hkv;
+        };
+        int mine = sum_of(1), upto = wave_scan(mine), size = 1, from = w;
+        int units = __builtin_amdgcn_readlane(upto, kWave - 1);  // runs are dealt in tiles, pieces one by one
+        left = 1;
+        if (a.pieces) {
+            size = (units + a.groups - 1) / (uint32_t)a.groups;
+            for (;;) {  // ends: with a size of the longest item every item is one piece
+                size = size > 1 ? size : 1;
+                mine = sum_of(size);
+                upto = wave_scan(mine);
+                units = __builtin_amdgcn_readlane(upto, kWave - 1);
+                if (units <= a.groups)
+                    break;
+                size += (size + 7) / 8;
+            }
+            if (w >= units)
+                return false;
+        } else {
+            const uint32_t groups = units < a.groups ? units : a.groups;
+            if (w >= (int)groups)
+                return false;
+            runs.each = units / groups;
+            runs.more = units - runs.each * groups;
+            from = first_tile(runs, w);
+            left = first_tile(runs, w + 1) - from;
+        }
+        // The lane whose share holds the run's first unit, then the item in it.
+        const int in = __builtin_ctzll(__ballot(from < upto));
+        int at = __builtin_amdgcn_readlane(upto - mine, in);
+        b = in * each;
+        chunk = 0;
+        int count;
+        if (__builtin_expect(small, 1)) {
+            count = __builtin_amdgcn_readlane(lane_tiles, in);
+            here = (uint32_t)(count + size - 1) / (uint32_t)size;
+            run_begin = __builtin_amdgcn_readlane(lane_begin, in);
+            run_end = __builtin_amdgcn_readlane(lane_end, in);
+            run_len = __builtin_amdgcn_readlane(lane_len, in);
+        } else {
+            for (;;) {
+                if (b >= a.B)
+                    return false;  // not reached: the sums above found the unit
+                const Span s = span_of<kTile>(a, b, chunk * kColumns, kColumns);
+                if (chunk == a.chunks || chunk * kColumns >= s.n * a.G) {
+                    chunk = 0;
+                    ++b;
+                    continue;
+                }
+                count = tiles_of(s);
+                here = (uint32_t)(count + size - 1) / (uint32_t)size;
+                if (from < at + here * a.Hkv)
+                    break;
+                at += here * a.Hkv;
+                ++chunk;
+            }
+            run_begin = a.row_starts[b];
+            run_end = a.row_starts[b + 1];
+            run_len = a.context_lens[b];
+        }
+        h = (uint32_t)(from - at) / (uint32_t)here;
+        item_unit = at + h * here;
+        tile = from - item_unit;
+        if (a.pieces) {  // piece `tile` of `here` equal ones
+            const int q = (uint32_t)count / (uint32_t)here, more = count - q * here, piece = tile;
+            tile = first_tile(Runs{q, more}, piece);
+            left = first_tile(Runs{q, more}, piece + 1) - tile;
+        }
+    }
+    start = Start{b, chunk, h, tile, w, left, item_unit, here, run_begin, run_end, run_len, runs};
+    return true;
+}
+
+// What a barrier has to order here is LDS only: loads of the next tile stay in
+// flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Column tiles that a workgroup takes at most: with more, the accumulators
+// (D / 16 registers a tile) and the queries in LDS would leave room for one
+// workgroup on a CU instead of two. Codes of heads of 128 leave no registers for
+// six.
+constexpr int most_col_tiles(int D, bool codes = false)
+{
+    return D == 64 || (D == 128 && !codes) ? 6 : D == 96 || D == 128 ? 4 : 3;
+}
+
+// Join of the pieces of an item that several runs share:
+// sum_z acc_z 2^(m_z - M) over sum_z l_z 2^(m_z - M) for each column. A
+// workgroup's threads are D/4 values wide and the rest of them share the
+// pieces, so that their loads are in flight together.
+// E: the matrix instructions' type, T: the output's.
+template <class E, typename T, int D>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a, int columns)
+{
+    constexpr int W = D / 4;                // threads of one piece's values
+    const int P = blockDim.x / W;           // pieces read at a time
+    __shared__ float4_t part[kJoinThreads / W][W];
+    __shared__ float sums[kJoinThreads / W];
+    const int G = a.G;
+    const int h = blockIdx.x % a.Hkv, k = blockIdx.x / a.Hkv % a.chunks, b = blockIdx.x / a.Hkv / a.chunks;
+    const int x0 = k * columns;
+    const int begin = a.row_starts[b], end = a.row_starts[b + 1];
+    const int2 join = a.joins[blockIdx.x];  // of items that exist
+    const int rows = begin >= 0 && begin <= end && end <= a.T ? end - begin : 0;
+    const int live = x0 + columns < rows * G ? columns : rows * G - x0;
+    if (live <= 0 || join.x == join.y)
+        return;
+    const int pieces = join.y - join.x + 1;
+    auto slot = [&](int z) { return (int64_t)slot_of(join.x + z, z == 0) * columns; };
+    for (int col = blockIdx.y; col < live; col += gridDim.y) {
+        const int x = x0 + col, r = row_of_column(a, x);
+        const int64_t at_row = (int64_t)(begin + r) * a.Hq + h * G + (x - r * G);
+        const float2_t *ml = reinterpret_cast<const float2_t *>(a.part_ml) + col;
+        float top = -__builtin_inff();
+        for (int z = threadIdx.x % kWave; z < pieces; z += kWave)
+            top = fmaxf(top, ml[slot(z)].x);
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2)
+            top = fmaxf(top, __shfl_xor(top, d));
+        const int d4 = threadIdx.x % W, first = threadIdx.x / W;
+        float4_t o{0.f, 0.f, 0.f, 0.f};
+        float total = 0.f;
+        if (first < P) {
+#pragma unroll 8
+            for (int z = first; z < pieces; z += P) {
+                const float2_t v = ml[slot(z)];
+                const float f = top == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(v.x - top);
+                total += v.y * f;
+                o += *reinterpret_cast<const float4_t *>(a.part_acc + (slot(z) + col) * D + d4 * 4) * f;
+            }
+            part[first][d4] = o;
+            if (d4 == 0)
+                sums[first] = total;
+        }
+        __syncthreads();
+        if (first == 0) {
+            for (int p = 1; p < P && p < pieces; ++p) {
+                o += part[p][d4];
+                total += sums[p];
+            }
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            typename Elem<T>::x4 y;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                y[k] = (T)(o[k] * inv);
+            *reinterpret_cast<typename Elem<T>::x4 *>(static_cast<T *>(a.out) + at_row * D + d4 * 4) = y;
+            if (a.lse && d4 == 0)
+                a.lse[at_row] = total == 0.f ? -__builtin_inff()
+                                             : (top + __builtin_amdgcn_logf(total * E::kUnlift)) * 0.69314718055994530942f;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+}  // namespace qmm

@@ -1,0 +1,66 @@
+// Rows of a quantized cache read back as 16-bit numbers.
+//
+// A thread turns 8 codes of one group into 16 bytes; neighbouring threads take
+// neighbouring codes of a row, then the next head, then the values' cache. Bound
+// by memory (reads 8 or 4 bytes and writes 16 for each 8 values), or for a few
+// rows by the launch.
+#include "qmm_kernels.hpp"
+#include "qmm_quant.hpp"
+#include "qmm_step.hpp"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int BITS, bool BF16>
+__global__ __launch_bounds__(kThreads) void quant_cache_read_kernel(const ReadArgs a, int units, int rows)
+{
+    // `units` threads for a row; `rows` rows in a workgroup where they fit.
+    const int in = threadIdx.x / units, row = blockIdx.x * rows + in;
+    const int unit = rows > 1 ? threadIdx.x - in * units : blockIdx.y * kThreads + threadIdx.x;
+    if (row >= a.M || (rows > 1 && in >= rows) || unit >= units)
+        return;
+    const int per_head = a.D / 8;
+    int head = unit / per_head;
+    const int u = unit - head * per_head;
+    const int cache = head >= a.Hkv;
+    head -= cache ? a.Hkv : 0;
+    const int slot = a.slots[row];
+    u32x4 v{0, 0, 0, 0};
+    if (slot >= 0 && slot < a.slot_count) {
+        const uint32_t page = divide(slot, a.page_magic, a.page_shift), offset = slot - page * a.page_size;
+        const int64_t at = ((int64_t)page * a.Hkv + head) * a.page_size + offset;
+        const uint32_t *codes = a.codes[cache] + at * (a.D * BITS / 32) + u * (BITS / 4);
+        v = eight_numbers(*reinterpret_cast<const typename Eight<BITS>::raw *>(codes),
+                          a.sb[cache][at * (a.D / a.group) + u * 8 / a.group]);
+    }
+    if constexpr (BF16) {
+        typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+        const half8_t h = __builtin_bit_cast(half8_t, v);
+        b8 w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = (__bf16)(float)h[i];
+        v = __builtin_bit_cast(u32x4, w);
+    }
+    reinterpret_cast<u32x4 *>(a.out[cache])[((int64_t)row * a.Hkv + head) * per_head + u] = v;
+}
+
+}  // namespace
+
+hipError_t launch_quant_cache_read(const ReadArgs &a, bool bf16_out, hipStream_t stream)
+{
+    const int units = 2 * a.Hkv * (a.D / 8);
+    const int rows = units < kThreads ? kThreads / units : 1;
+    const dim3 grid((a.M + rows - 1) / rows, (units + kThreads - 1) / kThreads);
+    if (a.bits == 8)
+        bf16_out ? quant_cache_read_kernel<8, true><<<grid, kThreads, 0, stream>>>(a, units, rows)
+                 : quant_cache_read_kernel<8, false><<<grid, kThreads, 0, stream>>>(a, units, rows);
+    else
+        bf16_out ? quant_cache_read_kernel<4, true><<<grid, kThreads, 0, stream>>>(a, units, rows)
+                 : quant_cache_read_kernel<4, false><<<grid, kThreads, 0, stream>>>(a, units, rows);
+    return hipGetLastError();
+}
+
+}  // namespace qmm

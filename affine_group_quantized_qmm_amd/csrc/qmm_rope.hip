@@ -15,6 +15,11 @@
 // while it walks over heads, so that the four angles are computed once per
 // row and thread.
 //
+// With a quantized cache the keys' and values' 8 values a lane leave as codes: a
+// group of 32, 64 or 128 values is 4, 8 or 16 neighbouring lanes, which find its
+// least and largest value with lane permutations. Rotated halves pass through
+// LDS first, so that a lane holds 8 values in the head's order.
+//
 // 8192 rows (24 query and 4 + 4 key and value heads of 256, fp32 in, bf16 out:
 // 403 MB) take 76 us, 5.3 TB/s where a copy of 1 GiB reaches 5.0; 123 rows of 64
 // heads of 128 take 3.9 us, one row 3.0, which is a launch with its cold code.
@@ -76,10 +81,95 @@ __device__ __forceinline__ float head_sum(float v)
     return v;
 }
 
-template <int L, typename TIN, typename TOUT, bool INTER>
+// Least and largest value of a group over the `lanes` (4, 8 or 16) aligned lanes
+// that hold it.
+__device__ __forceinline__ void group_range(float &lo, float &hi, int lanes)
+{
+    lo = fminf(lo, dpp_f32<0xB1>(lo));
+    hi = fmaxf(hi, dpp_f32<0xB1>(hi));
+    lo = fminf(lo, dpp_f32<0x4E>(lo));
+    hi = fmaxf(hi, dpp_f32<0x4E>(hi));
+    if (lanes >= 8) {
+        lo = fminf(lo, dpp_f32<0x141>(lo));
+        hi = fmaxf(hi, dpp_f32<0x141>(hi));
+    }
+    if (lanes >= 16) {
+        lo = fminf(lo, dpp_f32<0x140>(lo));
+        hi = fmaxf(hi, dpp_f32<0x140>(hi));
+    }
+}
+
+// A group's bias and scale: the largest fp16 number not above its least value,
+// and the smallest with which the last level reaches its largest one, so that
+// every value lies between two levels and its nearest one is within half a step.
+// The span and the comparison are in 64 bits, where both are exact.
+struct Levels {
+    _Float16 scale, bias;
+};
+__device__ __forceinline__ Levels levels_of(float lo, float hi, int levels)
+{
+    _Float16 b = (_Float16)lo;
+    if ((float)b > lo) {
+        const uint16_t bits = __builtin_bit_cast(uint16_t, b);
+        b = __builtin_bit_cast(_Float16, (uint16_t)((bits & 0x7FFF) == 0 ? 0x8001 : bits & 0x8000 ? bits + 1 : bits - 1));
+    }
+    const double span = (double)hi - (double)(float)b;
+    _Float16 s = (_Float16)(float)(span / levels);
+    if ((double)((float)s * (float)levels) < span)  // (11 + 8 bits: the product is exact)
+        s = __builtin_bit_cast(_Float16, (uint16_t)(__builtin_bit_cast(uint16_t, s) + 1));
+    return Levels{s, b};
+}
+
+// The codes of 8 values of row `row` of a cache, the u-th 8 of the head, and
+// from the first lane of a group its scale and bias. Called by whole heads.
+__device__ __forceinline__ void store_codes(const RopeArgs &a, float4_t y0, float4_t y1, int u, bool in_head, bool kept,
+                                            bool is_v, int64_t row)
+{
+    const int lanes = a.group / 8, levels = (1 << a.bits) - 1;
+    bool odd = false;
+    float lo = __builtin_inff(), hi = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        odd |= y0[j] != y0[j] || y1[j] != y1[j];
+        y0[j] = __builtin_amdgcn_fmed3f(y0[j], -kQuantMost, kQuantMost);
+        y1[j] = __builtin_amdgcn_fmed3f(y1[j], -kQuantMost, kQuantMost);
+        lo = fminf(lo, fminf(y0[j], y1[j]));
+        hi = fmaxf(hi, fmaxf(y0[j], y1[j]));
+    }
+    group_range(lo, hi, lanes);
+    const uint64_t all_odd = __ballot(odd && in_head);
+    const int first = threadIdx.x % kWave & -lanes;
+    odd = (all_odd >> first & ((1u << lanes) - 1u)) != 0;
+    if (!in_head || !kept)
+        return;
+    const Levels g = levels_of(lo, hi, levels);
+    // v_rcp_f32 is good to 2^-23: a code's place is off by at most 2^-14 of a step.
+    const float b = (float)g.bias, inv = g.scale > (_Float16)0 ? __builtin_amdgcn_rcpf((float)g.scale) : 0.f;
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float y = j < 4 ? y0[j % 4] : y1[j % 4];
+        c[j] = odd ? 0u : (uint32_t)__builtin_amdgcn_fmed3f(rintf((y - b) * inv), 0.f, (float)levels);
+    }
+    uint32_t *to = static_cast<uint32_t *>(is_v ? a.v_cache : a.k_cache) + row * (a.D * a.bits / 32);
+    if (a.bits == 8) {
+        *reinterpret_cast<u32x2 *>(to + 2 * u) = u32x2{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+                                                       c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
+    } else {
+        to[u] = c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12 | c[4] << 16 | c[5] << 20 | c[6] << 24 | c[7] << 28;
+    }
+    if (u % lanes == 0) {
+        const uint32_t s = odd ? 0x7E00u : __builtin_bit_cast(uint16_t, g.scale);  // NaN for the whole group
+        (is_v ? a.v_sb : a.k_sb)[row * (a.D / a.group) + u / lanes] =
+            s | (uint32_t)__builtin_bit_cast(uint16_t, g.bias) << 16;
+    }
+}
+
+template <int L, typename TIN, typename TOUT, bool INTER, bool QUANT>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a)
 {
     constexpr int HP = kThreads / L;  // heads that a workgroup handles at a time
+    __shared__ float4_t turned[QUANT && !INTER ? kThreads * 2 : 1];  // a rotated key, 8 values for each of its lanes
     const int row = blockIdx.x;
     const int u = threadIdx.x % L;
     const int heads = a.Hq + 2 * a.Hkv;
@@ -96,11 +186,14 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
             return static_cast<const TIN *>(a.k) + row * a.k_stride + (int64_t)(head - a.Hq) * a.D;
         return static_cast<const TIN *>(a.v) + row * a.v_stride + (int64_t)(head - a.Hq - a.Hkv) * a.D;
     };
+    // Values are not turned: with codes their lanes take them in order.
+    auto first_of = [&](int head) { return QUANT && head >= a.Hq + a.Hkv ? 8 * u : d0; };
+    auto second_of = [&](int head) { return QUANT && head >= a.Hq + a.Hkv ? 8 * u + 4 : d1; };
     float4_t x0{0.f, 0.f, 0.f, 0.f}, x1{0.f, 0.f, 0.f, 0.f};
     if (h < heads && in_head) {  // ahead of the angles, whose arithmetic hides it
         const TIN *s = source(h);
-        x0 = Load4<TIN>::at(s + d0);
-        x1 = Load4<TIN>::at(s + d1);
+        x0 = Load4<TIN>::at(s + first_of(h));
+        x1 = Load4<TIN>::at(s + second_of(h));
     }
 
     // Four angles, in turns: the product in 64 bits (position 262143 times a
@@ -127,8 +220,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
         float4_t n0{0.f, 0.f, 0.f, 0.f}, n1{0.f, 0.f, 0.f, 0.f};
         if (more) {  // the next head's values are on their way during this one's arithmetic
             const TIN *s = source(h + step);
-            n0 = Load4<TIN>::at(s + d0);
-            n1 = Load4<TIN>::at(s + d1);
+            n0 = Load4<TIN>::at(s + first_of(h + step));
+            n1 = Load4<TIN>::at(s + second_of(h + step));
         }
         const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
         float ss = 0.f;
@@ -136,8 +229,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
         for (int j = 0; j < 4; ++j)
             ss += x0[j] * x0[j] + x1[j] * x1[j];
         const float r = rsqrtf(head_sum<L>(ss) * (1.0f / (float)a.D) + a.eps);
+        float4_t y0 = x0, y1 = x1;
         if (in_head) {
-            float4_t y0 = x0, y1 = x1;
             if (!is_v) {
                 const float *w = is_q ? a.q_weight : a.k_weight;
                 const float4_t w0 = *reinterpret_cast<const float4_t *>(w + d0);
@@ -169,13 +262,32 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
                 TOUT *o = static_cast<TOUT *>(a.q_out) + ((int64_t)row * a.Hq + h) * a.D;
                 store4(o + d0, y0);
                 store4(o + d1, y1);
-            } else if (kept) {
+            } else if (!QUANT && kept) {
                 const int hk = h - a.Hq - (is_v ? a.Hkv : 0);
                 TOUT *o = static_cast<TOUT *>(is_v ? a.v_cache : a.k_cache) +
                           (((int64_t)page * a.Hkv + hk) * a.page_size + offset) * a.D;
                 store4(o + d0, y0);
                 store4(o + d1, y1);
             }
+        }
+        if constexpr (QUANT) {
+            const bool turn = !INTER && !is_q && !is_v;
+            float4_t *const mine = turned + (QUANT && !INTER ? threadIdx.x / L * L * 2 : 0);
+            if (turn && in_head) {
+                mine[d0 / 4] = y0;
+                mine[d1 / 4] = y1;
+            }
+            if constexpr (!INTER)
+                wave_lds_sync();  // a head's lanes are of one wave
+            if (turn && in_head) {
+                y0 = mine[2 * u];
+                y1 = mine[2 * u + 1];
+            }
+            if constexpr (!INTER)
+                wave_lds_sync();
+            if (!is_q)
+                store_codes(a, y0, y1, u, in_head, kept, is_v, ((int64_t)page * a.Hkv + h - a.Hq - (is_v ? a.Hkv : 0)) *
+                                                                   a.page_size + offset);
         }
         x0 = n0;
         x1 = n1;
@@ -194,10 +306,12 @@ hipError_t launch(const RopeArgs &a, bool interleaved, hipStream_t stream)
     const int passes = (a.Hq + 2 * a.Hkv + HP - 1) / HP;
     const int want = (4 * device_cu_count() + a.M - 1) / a.M;  // workgroups per row that fill the GPU
     const dim3 grid(a.M, want < passes ? want : passes);
-    if (interleaved)
-        qk_norm_rope_kernel<L, TIN, TOUT, true><<<grid, kThreads, 0, stream>>>(a);
+    if (a.bits != 0)
+        interleaved ? qk_norm_rope_kernel<L, TIN, TOUT, true, true><<<grid, kThreads, 0, stream>>>(a)
+                    : qk_norm_rope_kernel<L, TIN, TOUT, false, true><<<grid, kThreads, 0, stream>>>(a);
     else
-        qk_norm_rope_kernel<L, TIN, TOUT, false><<<grid, kThreads, 0, stream>>>(a);
+        interleaved ? qk_norm_rope_kernel<L, TIN, TOUT, true, false><<<grid, kThreads, 0, stream>>>(a)
+                    : qk_norm_rope_kernel<L, TIN, TOUT, false, false><<<grid, kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -42,42 +42,17 @@ int check_attention_sizes(int T, int B, int Hq, int Hkv, int D, int max_rows, in
 constexpr int kFar = 1 << 30;  // positions minus the window stay in 32 bits
 
 qmm::AttnPlan plan_of(int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks,
-                      int page_size, int max_pages)
+                      int page_size, int max_pages, int bits)
 {
     return qmm::attn_plan(B, Hq, Hkv, D, max_rows, max_context, window < kFar ? window : 0, sinks, page_size,
-                          max_pages);
+                          max_pages, bits);
 }
 
-}  // namespace
-
-extern "C" {
-
-int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
-                     int in_type, const float *q_weight, const float *k_weight, float eps, float weight_offset,
-                     const int32_t *positions, const float *inv_freq, int R, int interleaved, const int32_t *slots,
-                     void *q_out, void *k_cache, void *v_cache, int out_type, int M, int Hq, int Hkv, int D,
-                     int num_pages, int page_size, hipStream_t stream)
+qmm::RopeArgs rope_args(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                        const float *q_weight, const float *k_weight, float eps, float weight_offset,
+                        const int32_t *positions, const float *inv_freq, int R, const int32_t *slots, void *q_out,
+                        void *k_cache, void *v_cache, int M, int Hq, int Hkv, int D, int page_size)
 {
-    if (!q || !k || !v || !q_weight || !k_weight || !positions || !slots || !q_out || !k_cache || !v_cache ||
-        (R > 0 && !inv_freq))
-        return QMM_ERR_NULL;
-    if (!any_type(in_type) || !output_type(out_type))
-        return QMM_ERR_TYPE;
-    // a workgroup of 256 threads for each row: the runtime counts a launch's threads in 32 bits
-    if (M < 1 || Hq < 1 || M > (int)(UINT32_MAX / 256) || Hq > 65535 || Hkv > 65535)
-        return QMM_ERR_SHAPE;
-    const int rc = check_cache(num_pages, page_size, Hkv);
-    if (rc != QMM_OK)
-        return rc;
-    if (D < 8 || D > 256 || D % 8 != 0 || R < 0 || R > D || R % 8 != 0)
-        return QMM_ERR_HEAD;
-    if (q_stride < (int64_t)Hq * D || k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D)
-        return QMM_ERR_SHAPE;
-    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(q, 16) || !aligned(k, 16) ||
-        !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(inv_freq, 16) ||
-        !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(positions, 4) ||
-        !aligned(slots, 4))
-        return QMM_ERR_ALIGN;
     qmm::RopeArgs a{};
     a.q = q;
     a.k = k;
@@ -99,15 +74,181 @@ int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stri
     a.D = D;
     a.R = R;
     a.page_size = page_size;
-    const qmm::MagicDiv d = qmm::magic_div(page_size);
-    a.page_magic = d.magic;
-    a.page_shift = d.shift;
-    a.slot_count = num_pages * page_size;
     a.eps = eps;
     a.weight_offset = weight_offset;
+    return a;
+}
+
+// Checks of the norm and rotation that do not depend on what the cache holds.
+int check_rope(const qmm::RopeArgs &a, int in_type, int out_type, int num_pages)
+{
+    if (!a.q || !a.k || !a.v || !a.q_weight || !a.k_weight || !a.positions || !a.slots || !a.q_out || !a.k_cache ||
+        !a.v_cache || (a.R > 0 && !a.inv_freq))
+        return QMM_ERR_NULL;
+    if (!any_type(in_type) || !output_type(out_type))
+        return QMM_ERR_TYPE;
+    // a workgroup of 256 threads for each row: the runtime counts a launch's threads in 32 bits
+    if (a.M < 1 || a.Hq < 1 || a.M > (int)(UINT32_MAX / 256) || a.Hq > 65535 || a.Hkv > 65535)
+        return QMM_ERR_SHAPE;
+    const int rc = check_cache(num_pages, a.page_size, a.Hkv);
+    if (rc != QMM_OK)
+        return rc;
+    if (a.D < 8 || a.D > 256 || a.D % 8 != 0 || a.R < 0 || a.R > a.D || a.R % 8 != 0)
+        return QMM_ERR_HEAD;
+    if (a.q_stride < (int64_t)a.Hq * a.D || a.k_stride < (int64_t)a.Hkv * a.D || a.v_stride < (int64_t)a.Hkv * a.D)
+        return QMM_ERR_SHAPE;
+    if (a.q_stride % 8 != 0 || a.k_stride % 8 != 0 || a.v_stride % 8 != 0 || !aligned(a.q, 16) || !aligned(a.k, 16) ||
+        !aligned(a.v, 16) || !aligned(a.q_weight, 16) || !aligned(a.k_weight, 16) || !aligned(a.inv_freq, 16) ||
+        !aligned(a.q_out, 16) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.positions, 4) ||
+        !aligned(a.slots, 4))
+        return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+int run_rope(qmm::RopeArgs &a, int in_type, int out_type, int interleaved, int num_pages, hipStream_t stream)
+{
+    const qmm::MagicDiv d = qmm::magic_div(a.page_size);
+    a.page_magic = d.magic;
+    a.page_shift = d.shift;
+    a.slot_count = num_pages * a.page_size;
     return qmm::launch_qk_norm_rope(a, in_type, out_type == QMM_BF16, interleaved != 0, stream) == hipSuccess
                ? QMM_OK
                : QMM_ERR_LAUNCH;
+}
+
+// A quantized cache's format.
+int check_format(int D, int bits, int G)
+{
+    if (bits != 4 && bits != 8)
+        return QMM_ERR_BITS;
+    if (G != 32 && G != 64 && G != 128)
+        return QMM_ERR_GROUP;
+    return D % G == 0 ? QMM_OK : QMM_ERR_HEAD;
+}
+
+// Checks and launch of attention over either kind of cache (bits 0: 16-bit rows).
+// `a` holds the pointers, sizes and the format's words; the rest is set here.
+int run_attention(qmm::AttnArgs &a, int type, int D, int bits, int max_rows, int max_context, float scale, int window,
+                  int sinks, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!a.q || !a.k_cache || !a.v_cache || !a.block_table || !a.context_lens || !a.row_starts || !a.out)
+        return QMM_ERR_NULL;
+    if (!output_type(type))
+        return QMM_ERR_TYPE;
+    int rc = check_attention_sizes(a.T, a.B, a.Hq, a.Hkv, D, max_rows, max_context, window, sinks);
+    if (rc == QMM_OK)
+        rc = check_cache(a.num_pages, a.page_size, a.Hkv);
+    if (rc != QMM_OK)
+        return rc;
+    // Token numbers have 32 bits up to the end of a tile that begins at the
+    // table's end, and loads run two tiles ahead.
+    if (a.max_pages < 1 || (int64_t)a.max_pages * a.page_size > INT32_MAX - 4 * qmm::kAttnMostTile ||
+        a.q_stride < (int64_t)a.Hq * D || !isfinite(scale))
+        return QMM_ERR_SHAPE;
+    const qmm::AttnPlan plan =
+        plan_of(a.B, a.Hq, a.Hkv, D, max_rows, max_context, window, sinks, a.page_size, a.max_pages, bits);
+    if (plan.workspace_bytes > 0 && !workspace)
+        return QMM_ERR_NULL;
+    if (workspace_bytes < plan.workspace_bytes)
+        return QMM_ERR_WORKSPACE;
+    if (plan.blocks > INT32_MAX / 256 || plan.items > INT32_MAX / 256)  // the runtime's limit on threads of a launch
+        return QMM_ERR_SHAPE;
+    if (a.q_stride % 8 != 0 || !aligned(a.q, 16) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) ||
+        !aligned(a.out, 16) || (plan.workspace_bytes > 0 && !aligned(workspace, 16)) || !aligned(a.block_table, 4) ||
+        !aligned(a.context_lens, 4) || !aligned(a.row_starts, 4) || !aligned(a.lse, 4) || !aligned(a.k_sb, 4) ||
+        !aligned(a.v_sb, 4))
+        return QMM_ERR_ALIGN;
+    a.window = window < kFar ? window : 0;
+    a.sinks = a.window > 0 ? (sinks < kFar ? sinks : kFar) : 0;
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    const qmm::MagicDiv d = qmm::magic_div(a.page_size);
+    a.page_magic = d.magic;
+    a.page_shift = d.shift;
+    return qmm::launch_paged_attention(a, plan, D, type == QMM_BF16, bits, workspace, stream) == hipSuccess
+               ? QMM_OK
+               : QMM_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qmm_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                     int in_type, const float *q_weight, const float *k_weight, float eps, float weight_offset,
+                     const int32_t *positions, const float *inv_freq, int R, int interleaved, const int32_t *slots,
+                     void *q_out, void *k_cache, void *v_cache, int out_type, int M, int Hq, int Hkv, int D,
+                     int num_pages, int page_size, hipStream_t stream)
+{
+    qmm::RopeArgs a = rope_args(q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, weight_offset, positions,
+                                inv_freq, R, slots, q_out, k_cache, v_cache, M, Hq, Hkv, D, page_size);
+    const int rc = check_rope(a, in_type, out_type, num_pages);
+    return rc != QMM_OK ? rc : run_rope(a, in_type, out_type, interleaved, num_pages, stream);
+}
+
+int qmm_qk_norm_rope_quant(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, int in_type, const float *q_weight, const float *k_weight, float eps,
+                           float weight_offset, const int32_t *positions, const float *inv_freq, int R, int interleaved,
+                           const int32_t *slots, void *q_out, uint32_t *k_codes, uint32_t *k_sb, uint32_t *v_codes,
+                           uint32_t *v_sb, int out_type, int M, int Hq, int Hkv, int D, int bits, int G, int num_pages,
+                           int page_size, hipStream_t stream)
+{
+    qmm::RopeArgs a = rope_args(q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, weight_offset, positions,
+                                inv_freq, R, slots, q_out, k_codes, v_codes, M, Hq, Hkv, D, page_size);
+    if (!k_sb || !v_sb)
+        return QMM_ERR_NULL;
+    int rc = check_rope(a, in_type, out_type, num_pages);
+    if (rc == QMM_OK)
+        rc = check_format(D, bits, G);
+    if (rc != QMM_OK)
+        return rc;
+    if (!aligned(k_sb, 4) || !aligned(v_sb, 4))
+        return QMM_ERR_ALIGN;
+    a.k_sb = k_sb;
+    a.v_sb = v_sb;
+    a.bits = bits;
+    a.group = G;
+    return run_rope(a, in_type, out_type, interleaved, num_pages, stream);
+}
+
+int qmm_quant_cache_read(const uint32_t *k_codes, const uint32_t *k_sb, const uint32_t *v_codes, const uint32_t *v_sb,
+                         const int32_t *slots, void *k_out, void *v_out, int out_type, int M, int Hkv, int D, int bits,
+                         int G, int num_pages, int page_size, hipStream_t stream)
+{
+    if (!k_codes || !k_sb || !v_codes || !v_sb || !slots || !k_out || !v_out)
+        return QMM_ERR_NULL;
+    if (!output_type(out_type))
+        return QMM_ERR_TYPE;
+    int rc = M < 1 || Hkv > 65535 ? QMM_ERR_SHAPE : check_cache(num_pages, page_size, Hkv);
+    if (rc == QMM_OK)
+        rc = D < 32 || D > 256 ? QMM_ERR_HEAD : check_format(D, bits, G);
+    if (rc != QMM_OK)
+        return rc;
+    // a thread for 8 codes of a row, at least a workgroup of 256 a row: the runtime counts a launch's threads in 32 bits
+    const int64_t row_blocks = ((int64_t)2 * Hkv * (D / 8) + 255) / 256;
+    if ((int64_t)M * row_blocks > UINT32_MAX / 256)
+        return QMM_ERR_SHAPE;
+    if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+        !aligned(k_sb, 4) || !aligned(v_sb, 4) || !aligned(slots, 4))
+        return QMM_ERR_ALIGN;
+    qmm::ReadArgs a{};
+    a.codes[0] = k_codes;
+    a.codes[1] = v_codes;
+    a.sb[0] = k_sb;
+    a.sb[1] = v_sb;
+    a.out[0] = k_out;
+    a.out[1] = v_out;
+    a.slots = slots;
+    a.M = M;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.bits = bits;
+    a.group = G;
+    a.page_size = page_size;
+    a.slot_count = num_pages * page_size;
+    const qmm::MagicDiv d = qmm::magic_div(page_size);
+    a.page_magic = d.magic;
+    a.page_shift = d.shift;
+    return qmm::launch_quant_cache_read(a, out_type == QMM_BF16, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 
 size_t qmm_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_rows, int max_context,
@@ -116,7 +257,7 @@ size_t qmm_paged_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D,
     if (check_attention_sizes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks) != QMM_OK)
         return 0;
     // the largest that any block table needs
-    return plan_of(B, Hq, Hkv, D, max_rows, max_context, window, sinks, 1, 1).workspace_bytes;
+    return plan_of(B, Hq, Hkv, D, max_rows, max_context, window, sinks, 1, 1, 0).workspace_bytes;
 }
 
 int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache, int type,
@@ -125,32 +266,6 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
                         int max_rows, int max_context, float scale, int window, int sinks, void *workspace,
                         size_t workspace_bytes, hipStream_t stream)
 {
-    if (!q || !k_cache || !v_cache || !block_table || !context_lens || !row_starts || !out)
-        return QMM_ERR_NULL;
-    if (!output_type(type))
-        return QMM_ERR_TYPE;
-    int rc = check_attention_sizes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks);
-    if (rc == QMM_OK)
-        rc = check_cache(num_pages, page_size, Hkv);
-    if (rc != QMM_OK)
-        return rc;
-    // Token numbers have 32 bits up to the end of a tile that begins at the
-    // table's end, and loads run two tiles ahead.
-    if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX - 4 * qmm::kAttnMostTile ||
-        q_stride < (int64_t)Hq * D || !isfinite(scale))
-        return QMM_ERR_SHAPE;
-    const qmm::AttnPlan plan =
-        plan_of(B, Hq, Hkv, D, max_rows, max_context, window, sinks, page_size, max_pages);
-    if (plan.workspace_bytes > 0 && !workspace)
-        return QMM_ERR_NULL;
-    if (workspace_bytes < plan.workspace_bytes)
-        return QMM_ERR_WORKSPACE;
-    if (plan.blocks > INT32_MAX / 256 || plan.items > INT32_MAX / 256)  // the runtime's limit on threads of a launch
-        return QMM_ERR_SHAPE;
-    if (q_stride % 8 != 0 || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
-        (plan.workspace_bytes > 0 && !aligned(workspace, 16)) || !aligned(block_table, 4) ||
-        !aligned(context_lens, 4) || !aligned(row_starts, 4) || !aligned(lse, 4))
-        return QMM_ERR_ALIGN;
     qmm::AttnArgs a{};
     a.q = q;
     a.k_cache = k_cache;
@@ -168,13 +283,54 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
     a.page_size = page_size;
     a.num_pages = num_pages;
     a.max_pages = max_pages;
-    a.window = window < kFar ? window : 0;
-    a.sinks = a.window > 0 ? (sinks < kFar ? sinks : kFar) : 0;
-    a.scale_log2 = scale * 1.44269504088896340736f;
-    const qmm::MagicDiv d = qmm::magic_div(page_size);
-    a.page_magic = d.magic;
-    a.page_shift = d.shift;
-    return qmm::launch_paged_attention(a, plan, D, type == QMM_BF16, workspace, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+    return run_attention(a, type, D, 0, max_rows, max_context, scale, window, sinks, workspace, workspace_bytes, stream);
+}
+
+size_t qmm_paged_attention_quant_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_rows, int max_context,
+                                                 int window, int sinks, int bits, int G)
+{
+    if (check_attention_sizes(T, B, Hq, Hkv, D, max_rows, max_context, window, sinks) != QMM_OK ||
+        check_format(D, bits, G) != QMM_OK)
+        return 0;
+    return plan_of(B, Hq, Hkv, D, max_rows, max_context, window, sinks, 1, 1, bits).workspace_bytes;
+}
+
+int qmm_paged_attention_quant(const void *q, int64_t q_stride, const uint32_t *k_codes, const uint32_t *k_sb,
+                              const uint32_t *v_codes, const uint32_t *v_sb, int type, const int32_t *block_table,
+                              const int32_t *context_lens, const int32_t *row_starts, void *out, float *lse, int T,
+                              int B, int Hq, int Hkv, int D, int bits, int G, int num_pages, int page_size,
+                              int max_pages, int max_rows, int max_context, float scale, int window, int sinks,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!k_sb || !v_sb)
+        return QMM_ERR_NULL;
+    const int rc = check_format(D, bits, G);
+    if (rc != QMM_OK)
+        return rc;
+    qmm::AttnArgs a{};
+    a.q = q;
+    a.k_cache = k_codes;
+    a.v_cache = v_codes;
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.row_starts = row_starts;
+    a.out = out;
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.T = T;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.max_pages = max_pages;
+    a.k_sb = k_sb;
+    a.v_sb = v_sb;
+    a.code_shift = G == 32 ? 5 : G == 64 ? 6 : 7;
+    for (int groups = D % 96 == 0 ? D / G / 3 : D / G; groups > 1; groups /= 2)
+        ++a.words_shift;
+    return run_attention(a, type, D, bits, max_rows, max_context, scale, window, sinks, workspace, workspace_bytes,
+                         stream);
 }
 
 size_t qmm_sample_workspace_bytes(int M, int V)

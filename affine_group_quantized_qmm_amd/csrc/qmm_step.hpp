@@ -24,8 +24,22 @@ struct RopeArgs {
     int page_shift;
     int slot_count;                           // num_pages * page_size
     float eps, weight_offset;
+    uint32_t *k_sb, *v_sb;                    // quantized caches: (scale, bias) words, [.., D / group]
+    int bits, group;                          // of a quantized cache; bits 0: caches of q_out's type
 };
+constexpr float kQuantMost = 65280.0f;        // the largest magnitude that a quantized cache stores
 hipError_t launch_qk_norm_rope(const RopeArgs &a, int in_type, bool bf16_out, bool interleaved, hipStream_t stream);
+
+// Rows of a quantized cache as 16-bit numbers (qmm_quant.hip).
+struct ReadArgs {
+    const uint32_t *codes[2], *sb[2];         // keys' and values' caches: [num_pages, Hkv, page_size, D * bits / 32], [.., D / group]
+    void *out[2];                             // [M, Hkv, D]
+    const int32_t *slots;                     // [M]
+    int M, Hkv, D, bits, group, page_size, slot_count;
+    uint64_t page_magic;
+    int page_shift;
+};
+hipError_t launch_quant_cache_read(const ReadArgs &a, bool bf16_out, hipStream_t stream);
 
 // Attention over the paged cache (qmm_attn.hip).
 struct AttnArgs {
@@ -50,6 +64,11 @@ struct AttnArgs {
     int groups;                               // runs
     int whole, pieces;                        // how items are dealt out (qmm_attn.hip)
     int one_page;                             // page_size is a multiple of 16
+    // Quantized caches: codes in the caches' place, [.., D * bits / 32] words.
+    const uint32_t *k_sb, *v_sb;              // (scale, bias) words, [num_pages, Hkv, page_size, D / group]
+    int code_shift;                           // log2 of the group
+    int words_shift;                          // log2 of D / group, of a third of it where D is a multiple of 96
+    int io_bf16;                              // q and out are bf16, else fp16
 };
 // How a call is laid out on the GPU; a function of host arguments only.
 struct AttnPlan {
@@ -62,8 +81,12 @@ struct AttnPlan {
 constexpr int kAttnMostTile = 128;  // tokens of the largest tile
 bool attn_head_dim_supported(int D);
 AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context, int window, int sinks,
-                   int page_size, int max_pages);
-hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, void *workspace, hipStream_t stream);
+                   int page_size, int max_pages, int bits);
+// bits: 0 for caches of 16-bit rows, 4 or 8 for codes.
+hipError_t launch_paged_attention(AttnArgs a, const AttnPlan &p, int D, bool bf16, int bits, void *workspace,
+                                  hipStream_t stream);
+hipError_t launch_attention_codes4(const AttnArgs &a, const AttnPlan &p, int D, hipStream_t stream);
+hipError_t launch_attention_codes8(const AttnArgs &a, const AttnPlan &p, int D, hipStream_t stream);
 
 // Sampling (qmm_sample.hip).
 struct SampleArgs {

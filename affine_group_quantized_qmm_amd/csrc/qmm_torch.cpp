@@ -9,9 +9,11 @@
 // that does not fit, and returns the output (the caller's, or a new tensor) or,
 // where the C function refuses the call, its code.
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/Dtype.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 
 #include <cmath>
 #include <initializer_list>
@@ -326,10 +328,190 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// A quantized cache's four tensors; `code` where bits or G are none of the format's.
+struct QuantCaches {
+    uint32_t *words[4];  // k codes, k (scale, bias), v codes, v (scale, bias)
+    int pages, Hkv, page_size, D, code;
+};
+QuantCaches quant_caches(const Call &c, PyObject *const *o, int bits, int G)
+{
+    static const char *const names[4] = {"k_codes", "k_sb", "v_codes", "v_sb"};
+    QuantCaches q{};
+    if (bits != 4 && bits != 8) {
+        q.code = QMM_ERR_BITS;
+        return q;
+    }
+    if (G != 32 && G != 64 && G != 128) {
+        q.code = QMM_ERR_GROUP;
+        return q;
+    }
+    const at::Tensor &k = tensor(o[0], names[0]);
+    if (k.dim() != 4)
+        throw Refused(PyExc_ValueError, "the caches must be 4-D [num_pages, Hkv, page_size, D * bits / 32]");
+    for (int i = 0; i < 4; ++i)
+        if (k.size(i) > (i < 3 ? INT32_MAX : INT32_MAX / 8))
+            throw Refused(PyExc_ValueError, "the caches' sizes do not fit 32 bits");
+    q.pages = (int)k.size(0);
+    q.Hkv = (int)k.size(1);
+    q.page_size = (int)k.size(2);
+    q.D = (int)k.size(3) * (32 / bits);
+    if (q.D < 1 || q.D % G != 0) {
+        q.code = QMM_ERR_HEAD;
+        return q;
+    }
+    const int64_t pairs[4] = {k.size(0), k.size(1), k.size(2), q.D / G};
+    for (int i = 0; i < 4; ++i) {
+        const at::Tensor &t = tensor(o[i], names[i]);
+        const at::ScalarType type = t.scalar_type() == at::kUInt32 ? at::kUInt32 : at::kInt;
+        q.words[i] = static_cast<uint32_t *>(c.whole(t, names[i], type, i % 2 ? at::IntArrayRef(pairs) : k.sizes()));
+    }
+    return q;
+}
+
+// A 16-bit output's type: the one that is given, or the dtype argument's.
+at::ScalarType output_type(PyObject *out, PyObject *dtype)
+{
+    if (out != Py_None) {
+        const at::ScalarType t = tensor(out, "out").scalar_type();
+        if (t != at::kHalf && t != at::kBFloat16)
+            throw Refused(PyExc_TypeError, std::string("out must be float16 or bfloat16, got ") + c10::toString(t));
+        return t;
+    }
+    if (THPDtype_Check(dtype)) {
+        const at::ScalarType t = reinterpret_cast<THPDtype *>(dtype)->scalar_type;
+        if (t == at::kHalf || t == at::kBFloat16)
+            return t;
+    }
+    throw Refused(PyExc_TypeError, "dtype must be torch.float16 or torch.bfloat16");
+}
+
+// (q, k, v, q_weight, k_weight, positions, inv_freq or None, slots, k_codes, k_sb, v_codes, v_sb, bits, G, out or None,
+//  dtype, eps, weight_offset, interleaved, stream)
+PyObject *qk_norm_rope_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        args(n, 20);
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+        if (q.dim() != 3 || k.dim() != 3 || v.dim() != 3)
+            throw Refused(PyExc_ValueError, "q, k and v must be 3-D [M, heads, D]");
+        const Call c = on_gpu(q, "q");
+        const c10::DeviceGuard guard(c.device);
+        const at::ScalarType type = q.scalar_type();
+        if (type_code(type) < 0)
+            throw Refused(PyExc_TypeError, std::string("q must be float32, float16 or bfloat16, got ") + c10::toString(type));
+        const int64_t M = q.size(0), Hq = q.size(1), D = q.size(2);
+        if (M > INT32_MAX || Hq > INT32_MAX || D > INT32_MAX)
+            throw Refused(PyExc_ValueError, "q's sizes do not fit 32 bits");
+        const int bits = as_int(a[12], "bits"), G = as_int(a[13], "G");
+        const QuantCaches kv = quant_caches(c, a + 8, bits, G);
+        if (kv.code)
+            return PyLong_FromLong(kv.code);
+        if (kv.D != D)
+            throw Refused(PyExc_ValueError, "the caches' D is " + std::to_string(kv.D) + ", the queries' " + std::to_string(D));
+        const int64_t qs = c.rows(q, "q", type, q.sizes());
+        const int64_t keys[3] = {M, kv.Hkv, D};
+        const int64_t ks = c.rows(k, "k", type, keys), vs = c.rows(v, "v", type, keys);
+        int R = 0;
+        const float *freq = nullptr;
+        if (a[6] != Py_None) {
+            const int64_t half = tensor(a[6], "inv_freq").numel();
+            R = (int)(half < 4096 ? 2 * half : 8192);
+            freq = static_cast<const float *>(c.whole(a[6], "inv_freq", at::kFloat, {half}));
+        }
+        const at::ScalarType out_type = output_type(a[14], a[15]);
+        const Output out(c, a[14], "out", out_type, {M, Hq, D});
+        const int code = qmm_qk_norm_rope_quant(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, type_code(type),
+            static_cast<const float *>(c.whole(a[3], "q_weight", at::kFloat, {D})),
+            static_cast<const float *>(c.whole(a[4], "k_weight", at::kFloat, {D})), as_float(a[16]), as_float(a[17]),
+            static_cast<const int32_t *>(c.whole(a[5], "positions", at::kInt, {M})), freq, R, PyObject_IsTrue(a[18]),
+            static_cast<const int32_t *>(c.whole(a[7], "slots", at::kInt, {M})), out.data, kv.words[0], kv.words[1],
+            kv.words[2], kv.words[3], type_code(out_type), (int)M, (int)Hq, kv.Hkv, (int)D, bits, G, kv.pages,
+            kv.page_size, as_stream(a[19]));
+        return out.result(code);
+    });
+}
+
+// (k_codes, k_sb, v_codes, v_sb, bits, G, slots, k_out or None, v_out or None, dtype, stream)
+PyObject *quant_cache_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        args(n, 11);
+        const Call c = on_gpu(tensor(a[0], "k_codes"), "k_codes");
+        const c10::DeviceGuard guard(c.device);
+        const int bits = as_int(a[4], "bits"), G = as_int(a[5], "G");
+        const QuantCaches kv = quant_caches(c, a, bits, G);
+        if (kv.code)
+            return PyLong_FromLong(kv.code);
+        const int64_t M = tensor(a[6], "slots").numel();
+        if (M > INT32_MAX)
+            throw Refused(PyExc_ValueError, "the number of slots does not fit 32 bits");
+        const int32_t *slots = static_cast<const int32_t *>(c.whole(a[6], "slots", at::kInt, {M}));
+        const at::ScalarType type = output_type(a[7] != Py_None ? a[7] : a[8], a[9]);
+        const Output k(c, a[7], "k_out", type, {M, kv.Hkv, kv.D}), v(c, a[8], "v_out", type, {M, kv.Hkv, kv.D});
+        const int code = qmm_quant_cache_read(kv.words[0], kv.words[1], kv.words[2], kv.words[3], slots, k.data, v.data,
+                                              type_code(type), (int)M, kv.Hkv, kv.D, bits, G, kv.pages, kv.page_size,
+                                              as_stream(a[10]));
+        if (code)
+            return PyLong_FromLong(code);
+        return Py_BuildValue("(NN)", k.result(0), v.result(0));
+    });
+}
+
+// (q, k_codes, k_sb, v_codes, v_sb, bits, G, block_table, context_lens, row_starts, max_rows, max_context, scale or
+//  None, window, sinks, out or None, lse or None, workspace or None, stream)
+PyObject *paged_attention_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        args(n, 19);
+        const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[7], "block_table");
+        if (q.dim() != 3 || table.dim() != 2)
+            throw Refused(PyExc_ValueError, "q must be 3-D [T, Hq, D] and block_table 2-D [B, max_pages]");
+        const Call c = on_gpu(q, "q");
+        const c10::DeviceGuard guard(c.device);
+        const at::ScalarType type = q.scalar_type();
+        if (type != at::kHalf && type != at::kBFloat16)
+            throw Refused(PyExc_TypeError, std::string("q must be float16 or bfloat16, got ") + c10::toString(type));
+        const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2), B = table.size(0), max_pages = table.size(1);
+        if (T > INT32_MAX || Hq > INT32_MAX || D > INT32_MAX || B > INT32_MAX || max_pages > INT32_MAX)
+            throw Refused(PyExc_ValueError, "sizes of q or block_table do not fit 32 bits");
+        const int bits = as_int(a[5], "bits"), G = as_int(a[6], "G");
+        const QuantCaches kv = quant_caches(c, a + 1, bits, G);
+        if (kv.code)
+            return PyLong_FromLong(kv.code);
+        if (kv.D != D)
+            throw Refused(PyExc_ValueError, "the caches' D is " + std::to_string(kv.D) + ", the queries' " + std::to_string(D));
+        const int64_t qs = c.rows(q, "q", type, q.sizes());
+        const int max_rows = as_int(a[10], "max_rows"), max_context = as_int(a[11], "max_context");
+        const int window = as_int(a[13], "window"), sinks = as_int(a[14], "sinks");
+        const int32_t *blocks = static_cast<const int32_t *>(c.whole(table, "block_table", at::kInt, table.sizes()));
+        const int32_t *lens = static_cast<const int32_t *>(c.whole(a[8], "context_lens", at::kInt, {B}));
+        const int32_t *starts = static_cast<const int32_t *>(c.whole(a[9], "row_starts", at::kInt, {B + 1}));
+        const Output out(c, a[15], "out", type, {T, Hq, D});
+        float *lse = static_cast<float *>(c.whole_or_null(a[16], "lse", at::kFloat, {T, Hq}));
+        const float scale = a[12] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : as_float(a[12]);
+        const hipStream_t stream = as_stream(a[18]);
+        const Workspace ws(a[17],
+                           qmm_paged_attention_quant_workspace_bytes((int)T, (int)B, (int)Hq, kv.Hkv, (int)D, max_rows,
+                                                                     max_context, window, sinks, bits, G),
+                           c.device);
+        return out.result(qmm_paged_attention_quant(
+            q.data_ptr(), qs, kv.words[0], kv.words[1], kv.words[2], kv.words[3], type_code(type), blocks, lens, starts,
+            out.data, lse, (int)T, (int)B, (int)Hq, kv.Hkv, (int)D, bits, G, kv.pages, kv.page_size, (int)max_pages,
+            max_rows, max_context, scale, window, sinks, ws.data, ws.bytes, stream));
+    });
+}
+
 PyMethodDef methods[] = {
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)), METH_FASTCALL,
      nullptr},
+    {"qk_norm_rope_quant", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope_quant)),
+     METH_FASTCALL, nullptr},
+    {"quant_cache_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quant_cache_read)), METH_FASTCALL,
+     nullptr},
+    {"paged_attention_quant", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention_quant)),
+     METH_FASTCALL, nullptr},
     {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sample)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -67,7 +67,7 @@ extern "C" {
 #define QMM_OK 0
 #define QMM_ERR_NULL (-1)          /* a required pointer is NULL */
 #define QMM_ERR_SHAPE (-2)         /* M < 1, K < 1, N < 1, K % G != 0 or a size overflows */
-#define QMM_ERR_BITS (-3)          /* bits not in {2, 3, 4, 5, 6, 8} */
+#define QMM_ERR_BITS (-3)          /* bits not in {2, 3, 4, 5, 6, 8} (quantized cache: {4, 8}) */
 #define QMM_ERR_GROUP (-4)         /* G not in {32, 64, 128} */
 #define QMM_ERR_SPLIT (-5)         /* split_k < 1 or split_k > K/G */
 #define QMM_ERR_WORKSPACE (-6)     /* workspace smaller than the entry point's *_workspace_bytes */
@@ -456,6 +456,76 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
                         int Hkv, int D, int num_pages, int page_size, int max_pages, int max_rows,
                         int max_context, float scale, int window, int sinks, void *workspace,
                         size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The quantized paged cache: keys and values as 8- or 4-bit codes with a scale
+ * and a bias for each group of G values of one token and head. codes are uint32
+ * [num_pages, Hkv, page_size, D*bits/32], a row being the least-significant-bit-
+ * first stream of its D codes; sb are uint32 [num_pages, Hkv, page_size, D/G],
+ * words of a group's fp16 scale and, in the upper half, fp16 bias. A code c
+ * stands for the fp16 number nearest to scale * c + bias. bits is 4 or 8, G 32,
+ * 64 or 128, D a multiple of G; sizes as for the cache above. codes are 16-byte
+ * aligned, sb 4.
+ *
+ * qmm_qk_norm_rope_quant - qmm_qk_norm_rope with keys and values quantized as
+ * they are written. In a group of values y (fp32, after norm and rotation; values
+ * past 65280 in magnitude are taken as 65280): bias is the largest fp16 number
+ * not above min y, scale the smallest with bias + scale * (2^bits - 1) >= max y,
+ * and the code is the integer nearest to (y - bias) / scale (to 2^-14 of a step),
+ * so that a value is stored to within half a step, and the fp16 rounding of the
+ * number. A group that holds a NaN stands for NaN in all its places. Arguments as
+ * for qmm_qk_norm_rope; slots that are negative or past the cache write nothing.
+ * Errors: those of qmm_qk_norm_rope, QMM_ERR_BITS, QMM_ERR_GROUP, QMM_ERR_HEAD
+ * also for D % G != 0.
+ */
+int qmm_qk_norm_rope_quant(const void *q, const void *k, const void *v, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, int in_type,
+                           const float *q_weight, const float *k_weight, float eps,
+                           float weight_offset, const int32_t *positions, const float *inv_freq,
+                           int R, int interleaved, const int32_t *slots, void *q_out,
+                           uint32_t *k_codes, uint32_t *k_sb, uint32_t *v_codes, uint32_t *v_sb,
+                           int out_type, int M, int Hq, int Hkv, int D, int bits, int G,
+                           int num_pages, int page_size, hipStream_t stream);
+
+/*
+ * qmm_quant_cache_read - rows of a quantized cache as 16-bit numbers: k_out and
+ * v_out [M, Hkv, D] of out_type (fp16: the numbers that the codes stand for; bf16:
+ * these rounded) of the tokens at slots int32 [M]; rows whose slot is negative or
+ * past the cache are zeros. The same slot may be read twice. Outputs are 16-byte
+ * aligned. D up to 256; M times the workgroups of a row (2 * Hkv * D / 2048,
+ * rounded up) below 2^24.
+ * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_HEAD, QMM_ERR_BITS,
+ * QMM_ERR_GROUP, QMM_ERR_ALIGN, QMM_ERR_LAUNCH.
+ */
+int qmm_quant_cache_read(const uint32_t *k_codes, const uint32_t *k_sb, const uint32_t *v_codes,
+                         const uint32_t *v_sb, const int32_t *slots, void *k_out, void *v_out,
+                         int out_type, int M, int Hkv, int D, int bits, int G, int num_pages,
+                         int page_size, hipStream_t stream);
+
+/*
+ * qmm_paged_attention_quant - qmm_paged_attention over a quantized cache: the
+ * result is that of the formula for the fp16 numbers that the codes stand for,
+ * whatever the type of q and out (fp16 or bf16). Products are accumulated in
+ * fp32; e^(s) enters the second product as the sum of two fp16 numbers (good to
+ * 2^-22 of itself, or 2^-40 of the row's largest where that is more); bf16
+ * queries keep their bits down to 2^-28 of their row's largest value. Arguments,
+ * visibility, rows that see nothing, non-finite values and workspace as for
+ * qmm_paged_attention, the workspace's size from
+ * qmm_paged_attention_quant_workspace_bytes.
+ * Errors: those of qmm_paged_attention, QMM_ERR_BITS, QMM_ERR_GROUP, QMM_ERR_HEAD
+ * also for D % G != 0.
+ */
+size_t qmm_paged_attention_quant_workspace_bytes(int T, int B, int Hq, int Hkv, int D,
+                                                 int max_rows, int max_context, int window,
+                                                 int sinks, int bits, int G);
+int qmm_paged_attention_quant(const void *q, int64_t q_stride, const uint32_t *k_codes,
+                              const uint32_t *k_sb, const uint32_t *v_codes,
+                              const uint32_t *v_sb, int type, const int32_t *block_table,
+                              const int32_t *context_lens, const int32_t *row_starts, void *out,
+                              float *lse, int T, int B, int Hq, int Hkv, int D, int bits, int G,
+                              int num_pages, int page_size, int max_pages, int max_rows,
+                              int max_context, float scale, int window, int sinks,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * qmm_sample - a token for each row of logits from a given uniform number.
