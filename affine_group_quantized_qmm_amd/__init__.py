@@ -89,6 +89,9 @@ _lib.qmm_paged_attention_quant.argtypes = [_p, _l, _p, _p, _p, _p, _i, _p, _p, _
 _lib.qmm_sample_workspace_bytes.argtypes = [_i, _i]
 _lib.qmm_sample_workspace_bytes.restype = _sz
 _lib.qmm_sample.argtypes = [_p, _l, _i, _p, _p, _p, _p, _p, _p, _p, _i, _i, _p, _sz, _p]
+_lib.qmm_logprobs_workspace_bytes.argtypes = [_i, _i, _i]
+_lib.qmm_logprobs_workspace_bytes.restype = _sz
+_lib.qmm_logprobs.argtypes = [_p, _l, _i, _p, _p, _p, _p, _i, _p, _p, _i, _i, _p, _sz, _p]
 _lib.qmm_splitk_workspace_bytes.argtypes = [_i, _i, _i]
 _lib.qmm_splitk_workspace_bytes.restype = _sz
 _lib.qmm_validate.argtypes = [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _sz]
@@ -101,7 +104,8 @@ for _f in (_lib.qmm_pack, _lib.qmm_forward, _lib.qmm_forward_rowexact, _lib.qmm_
            _lib.qmm_forward_kernel, _lib.qmm_forward_fused, _lib.qmm_repack_tiled,
            _lib.qmm_forward_tiled, _lib.qmm_validate, _lib.qmm_stream_read, _lib.qmm_admit,
            _lib.qmm_admission, _lib.qmm_qk_norm_rope, _lib.qmm_paged_attention, _lib.qmm_sample,
-           _lib.qmm_qk_norm_rope_quant, _lib.qmm_quant_cache_read, _lib.qmm_paged_attention_quant):
+           _lib.qmm_qk_norm_rope_quant, _lib.qmm_quant_cache_read, _lib.qmm_paged_attention_quant,
+           _lib.qmm_logprobs):
     _f.restype = _i
 
 EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16", "qmm_forward_splitk",
@@ -113,7 +117,7 @@ EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16
             "qmm_qk_norm_rope", "qmm_paged_attention_workspace_bytes", "qmm_paged_attention",
             "qmm_sample_workspace_bytes", "qmm_sample",
             "qmm_qk_norm_rope_quant", "qmm_quant_cache_read", "qmm_paged_attention_quant_workspace_bytes",
-            "qmm_paged_attention_quant")
+            "qmm_paged_attention_quant", "qmm_logprobs_workspace_bytes", "qmm_logprobs")
 
 QMM_MAX_FUSED = 4  # projections per qmm_forward_fused call
 
@@ -515,7 +519,7 @@ def qmm_paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits: int, G: int
     return _step_result(_binding.paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits, G, block_table,
                                                        context_lens, row_starts, max_rows, max_context, scale, window,
                                                        sinks, out, lse, workspace, _step_stream(q)),
-                        "qmm_paged_attention_quant")
+                        "qmm_paged_attention_quant", "qmm_logprobs_workspace_bytes", "qmm_logprobs")
 
 
 def qmm_sample_workspace_bytes(M: int, V: int) -> int:
@@ -530,3 +534,17 @@ def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
     token's share of the kept mass."""
     return _step_result(_binding.sample(logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, workspace,
                                         _step_stream(logits)), "qmm_sample")
+
+
+def qmm_logprobs_workspace_bytes(M: int, V: int, top_n: int) -> int:
+    return int(_lib.qmm_logprobs_workspace_bytes(M, V, top_n))
+
+
+def qmm_logprobs(logits, tokens, top_n: int = 0, *, logprobs=None, ranks=None, entropy=None, top_tokens=None,
+                 top_logprobs=None, workspace=None):
+    """(logprobs, ranks, entropy, top_tokens, top_logprobs) of rows of logits [M, V]:
+    the logarithm of the share of tokens[m] (int32) in row m's softmax and its
+    place in falling order (0: the largest), the row's entropy, and its top_n
+    (up to 64) most probable tokens [M, top_n] with their logarithms."""
+    return _step_result(_binding.logprobs(logits, tokens, top_n, logprobs, ranks, entropy, top_tokens, top_logprobs,
+                                          workspace, _step_stream(logits)), "qmm_logprobs")

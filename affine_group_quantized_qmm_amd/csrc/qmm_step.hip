@@ -48,6 +48,14 @@ qmm::AttnPlan plan_of(int B, int Hq, int Hkv, int D, int max_rows, int max_conte
                           max_pages, bits);
 }
 
+int check_logprobs_sizes(int M, int V, int n)
+{
+    if (M < 1 || V < 1 || V > (1 << 23) || n < 0 || n > 64)
+        return QMM_ERR_SHAPE;
+    // the runtime counts a launch's threads in 32 bits
+    return M > (1 << 24) - 1 || qmm::logprobs_plan(M, V, n, 7).threads > (int64_t)UINT32_MAX ? QMM_ERR_SHAPE : QMM_OK;
+}
+
 qmm::RopeArgs rope_args(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                         const float *q_weight, const float *k_weight, float eps, float weight_offset,
                         const int32_t *positions, const float *inv_freq, int R, const int32_t *slots, void *q_out,
@@ -368,6 +376,50 @@ int qmm_sample(const void *logits, int64_t row_stride, int type, const float *u,
     a.M = M;
     a.V = V;
     return qmm::launch_sample(a, type, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+size_t qmm_logprobs_workspace_bytes(int M, int V, int n)
+{
+    return check_logprobs_sizes(M, V, n) != QMM_OK ? 0 : qmm::logprobs_plan(M, V, n, 7).workspace_bytes;
+}
+
+int qmm_logprobs(const void *logits, int64_t row_stride, int type, const int32_t *tokens, float *logprobs,
+                 int32_t *ranks, float *entropy, int n, int32_t *top_tokens, float *top_logprobs, int M, int V,
+                 void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!logits || !tokens || !logprobs || (n > 0 && (!top_tokens || !top_logprobs)))
+        return QMM_ERR_NULL;
+    if (!any_type(type))
+        return QMM_ERR_TYPE;
+    const int rc = check_logprobs_sizes(M, V, n);
+    if (rc != QMM_OK)
+        return rc;
+    if (row_stride < V)
+        return QMM_ERR_SHAPE;
+    const int size = type == QMM_F32 ? 4 : 2;
+    const bool even = aligned(logits, 16) && row_stride * size % 16 == 0;
+    const qmm::LogprobPlan plan = qmm::logprobs_plan(M, V, n, even ? 0 : 16 / size - 1);
+    if (plan.workspace_bytes > 0 && !workspace)
+        return QMM_ERR_NULL;
+    if (workspace_bytes < plan.workspace_bytes)
+        return QMM_ERR_WORKSPACE;
+    if (!aligned(logits, type == QMM_F32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprobs, 4) || !aligned(ranks, 4) ||
+        !aligned(entropy, 4) || !aligned(top_tokens, 4) || !aligned(top_logprobs, 4) ||
+        (plan.workspace_bytes > 0 && !aligned(workspace, 16)))
+        return QMM_ERR_ALIGN;
+    qmm::LogprobArgs a{};
+    a.logits = logits;
+    a.row_stride = row_stride;
+    a.tokens = tokens;
+    a.logprobs = logprobs;
+    a.ranks = ranks;
+    a.entropy = entropy;
+    a.top_tokens = top_tokens;
+    a.top_logprobs = top_logprobs;
+    a.M = M;
+    a.V = V;
+    a.n = n;
+    return qmm::launch_logprobs(a, plan, type, workspace, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 
 }  // extern "C"

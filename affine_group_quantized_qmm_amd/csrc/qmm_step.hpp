@@ -103,6 +103,34 @@ bool sample_size_supported(int V);
 size_t sample_workspace_bytes(int M, int V);
 hipError_t launch_sample(const SampleArgs &a, int type, hipStream_t stream);
 
+// Log probabilities (qmm_logprobs.hip).
+struct LogprobPart {                          // of a slice of a row: see there
+    float m;
+    uint32_t ahead;
+    double s, t;
+};
+struct LogprobArgs {
+    const void *logits;                       // [M, V], row_stride elements between rows
+    int64_t row_stride;
+    const int32_t *tokens;                    // [M]
+    float *logprobs, *entropy;                // [M]; entropy may be null
+    int32_t *ranks;                           // [M] or null
+    int32_t *top_tokens;                      // [M, n]
+    float *top_logprobs;                      // [M, n]
+    LogprobPart *parts;                       // [M, slices]
+    float2 *best;                             // [M, slices, n]: logit and index (as bits)
+    int M, V, n, slices;
+    int skew;                                 // elements from a multiple of 16 bytes to the first row
+};
+struct LogprobPlan {
+    int slices;
+    int64_t threads;
+    size_t workspace_bytes;
+};
+// skew: the most elements that lie in front of a row within its first 16 bytes
+LogprobPlan logprobs_plan(int M, int V, int n, int skew);
+hipError_t launch_logprobs(LogprobArgs a, const LogprobPlan &p, int type, void *workspace, hipStream_t stream);
+
 // n / d = (n * magic) >> (32 + shift) for 0 <= n < 2^31, with
 // magic = ceil(2^(32 + shift) / d) and d <= 2^(shift + 1): the magic's excess
 // over the exact quotient is below 2^-(shift + 32) * d <= 2^-31 of a unit per

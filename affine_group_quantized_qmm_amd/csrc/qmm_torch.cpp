@@ -502,7 +502,48 @@ PyObject *paged_attention_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// (logits, tokens, top_n, logprobs or None, ranks or None, entropy or None, top_tokens or None, top_logprobs or None,
+//  workspace or None, stream)
+PyObject *logprobs(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        args(n, 10);
+        const at::Tensor &x = tensor(a[0], "logits");
+        if (x.dim() != 2)
+            throw Refused(PyExc_ValueError, "logits must be 2-D [M, V]");
+        const Call c = on_gpu(x, "logits");
+        const c10::DeviceGuard guard(c.device);
+        const at::ScalarType type = x.scalar_type();
+        if (type_code(type) < 0)
+            throw Refused(PyExc_TypeError,
+                          std::string("logits must be float32, float16 or bfloat16, got ") + c10::toString(type));
+        const int64_t M = x.size(0), V = x.size(1);
+        if (M > INT32_MAX || V > INT32_MAX)
+            throw Refused(PyExc_ValueError, "sizes of logits do not fit 32 bits");
+        const int top = as_int(a[2], "top_n");
+        if (top < 0 || top > 64)
+            return PyLong_FromLong(QMM_ERR_SHAPE);
+        const int64_t stride = c.rows(x, "logits", type, x.sizes());
+        const int32_t *tokens = static_cast<const int32_t *>(c.whole(a[1], "tokens", at::kInt, {M}));
+        const Output lp(c, a[3], "logprobs", at::kFloat, {M}), ranks(c, a[4], "ranks", at::kInt, {M});
+        const Output entropy(c, a[5], "entropy", at::kFloat, {M});
+        const Output best(c, a[6], "top_tokens", at::kInt, {M, top}), best_lp(c, a[7], "top_logprobs", at::kFloat, {M, top});
+        const hipStream_t stream = as_stream(a[9]);
+        const Workspace ws(a[8], qmm_logprobs_workspace_bytes((int)M, (int)V, top), c.device);
+        const int code =
+            qmm_logprobs(x.data_ptr(), stride, type_code(type), tokens, static_cast<float *>(lp.data),
+                         static_cast<int32_t *>(ranks.data), static_cast<float *>(entropy.data), top,
+                         static_cast<int32_t *>(best.data), static_cast<float *>(best_lp.data), (int)M, (int)V, ws.data,
+                         ws.bytes, stream);
+        if (code)
+            return PyLong_FromLong(code);
+        return Py_BuildValue("(NNNNN)", lp.result(0), ranks.result(0), entropy.result(0), best.result(0),
+                             best_lp.result(0));
+    });
+}
+
 PyMethodDef methods[] = {
+    {"logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(logprobs)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)), METH_FASTCALL,
      nullptr},

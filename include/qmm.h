@@ -562,6 +562,38 @@ int qmm_sample(const void *logits, int64_t row_stride, int type, const float *u,
                const float *min_p, int32_t *tokens, float *logprobs, int M, int V, void *workspace,
                size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * qmm_logprobs - log probabilities of given tokens, with their ranks, the entropy
+ * and the most probable tokens of each row.
+ *
+ * logits [M, V] as for qmm_sample. Per row, with p = softmax(x):
+ *   logprobs[m]  log p_j of j = tokens[m] (int32 [M])
+ *   ranks[m]     the number of logits in front of x_j: larger ones, and equal ones
+ *                of lower index (may be NULL)
+ *   entropy[m]   -sum p_i log p_i (may be NULL)
+ *   top_tokens, top_logprobs [M, n]: the first n tokens in falling order, equal
+ *                logits by rising index, and their log p (n = 0: not wanted, both may
+ *                be NULL; n <= 64)
+ * Not the filtered distribution that qmm_sample draws from, but the model's own.
+ * NaN counts as -infinity; +infinity holds all the mass, in equal parts where
+ * there are several. A token that is no index of the row gets logprob -infinity and
+ * rank -1; a row without any logit above -infinity has logprobs of -infinity and entropy
+ * 0. Tokens of logit -infinity are never among the top_tokens: places without one hold
+ * -1 and -infinity.
+ * Sums are fp32 over up to 32 terms and 64 bits over those, results are rounded
+ * once from there: logprobs are good to about 1e-6 absolutely. Reruns are bitwise
+ * identical. V <= 2^23; M times ((V + 7) / 2048 + 1) * 256 below 2^32 is always taken.
+ * workspace: qmm_logprobs_workspace_bytes(M, V, n) bytes (0 for invalid sizes and where
+ * none is needed), 16-byte aligned, contents irrelevant.
+ * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_WORKSPACE,
+ * QMM_ERR_ALIGN (logits their element, workspace 16, the others 4), QMM_ERR_LAUNCH.
+ */
+size_t qmm_logprobs_workspace_bytes(int M, int V, int n);
+int qmm_logprobs(const void *logits, int64_t row_stride, int type, const int32_t *tokens,
+                 float *logprobs, int32_t *ranks, float *entropy, int n, int32_t *top_tokens,
+                 float *top_logprobs, int M, int V, void *workspace, size_t workspace_bytes,
+                 hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
