@@ -89,6 +89,9 @@ _lib.qmm_paged_attention_quant.argtypes = [_p, _l, _p, _p, _p, _p, _i, _p, _p, _
 _lib.qmm_sample_workspace_bytes.argtypes = [_i, _i]
 _lib.qmm_sample_workspace_bytes.restype = _sz
 _lib.qmm_sample.argtypes = [_p, _l, _i, _p, _p, _p, _p, _p, _p, _p, _i, _i, _p, _sz, _p]
+_lib.qmm_lora_workspace_bytes.argtypes = [_i, ctypes.POINTER(_i), _i, _i, _i, _i]
+_lib.qmm_lora_workspace_bytes.restype = _sz
+_lib.qmm_lora.argtypes = [_p, _i, _i, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _sz, _p]
 _lib.qmm_logprobs_workspace_bytes.argtypes = [_i, _i, _i]
 _lib.qmm_logprobs_workspace_bytes.restype = _sz
 _lib.qmm_logprobs.argtypes = [_p, _l, _i, _p, _p, _p, _p, _i, _p, _p, _i, _i, _p, _sz, _p]
@@ -105,7 +108,7 @@ for _f in (_lib.qmm_pack, _lib.qmm_forward, _lib.qmm_forward_rowexact, _lib.qmm_
            _lib.qmm_forward_tiled, _lib.qmm_validate, _lib.qmm_stream_read, _lib.qmm_admit,
            _lib.qmm_admission, _lib.qmm_qk_norm_rope, _lib.qmm_paged_attention, _lib.qmm_sample,
            _lib.qmm_qk_norm_rope_quant, _lib.qmm_quant_cache_read, _lib.qmm_paged_attention_quant,
-           _lib.qmm_logprobs):
+           _lib.qmm_logprobs, _lib.qmm_lora):
     _f.restype = _i
 
 EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16", "qmm_forward_splitk",
@@ -117,7 +120,8 @@ EXPORTED = ("qmm_pack", "qmm_forward", "qmm_forward_rowexact", "qmm_forward_bf16
             "qmm_qk_norm_rope", "qmm_paged_attention_workspace_bytes", "qmm_paged_attention",
             "qmm_sample_workspace_bytes", "qmm_sample",
             "qmm_qk_norm_rope_quant", "qmm_quant_cache_read", "qmm_paged_attention_quant_workspace_bytes",
-            "qmm_paged_attention_quant", "qmm_logprobs_workspace_bytes", "qmm_logprobs")
+            "qmm_paged_attention_quant", "qmm_logprobs_workspace_bytes", "qmm_logprobs",
+            "qmm_lora_workspace_bytes", "qmm_lora")
 
 QMM_MAX_FUSED = 4  # projections per qmm_forward_fused call
 
@@ -519,7 +523,8 @@ def qmm_paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits: int, G: int
     return _step_result(_binding.paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits, G, block_table,
                                                        context_lens, row_starts, max_rows, max_context, scale, window,
                                                        sinks, out, lse, workspace, _step_stream(q)),
-                        "qmm_paged_attention_quant", "qmm_logprobs_workspace_bytes", "qmm_logprobs")
+                        "qmm_paged_attention_quant", "qmm_logprobs_workspace_bytes", "qmm_logprobs",
+            "qmm_lora_workspace_bytes", "qmm_lora")
 
 
 def qmm_sample_workspace_bytes(M: int, V: int) -> int:
@@ -534,6 +539,19 @@ def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
     token's share of the kept mass."""
     return _step_result(_binding.sample(logits, u, temperature, top_k, top_p, min_p, tokens, logprobs, workspace,
                                         _step_stream(logits)), "qmm_sample")
+
+
+def qmm_lora_workspace_bytes(Ns, M: int, K: int, r: int, adapters: int) -> int:
+    """Bytes for projections of Ns columns each."""
+    return int(_lib.qmm_lora_workspace_bytes(len(Ns), (_i * len(Ns))(*Ns), M, K, r, adapters))
+
+
+def qmm_lora(x, adapters, ids, ys, *, scales=None, workspace=None):
+    """Adds to each y_p (float32 [M, N_p]) of `ys` scales[i] * B_p[i] (A_p[i] x[m]) of
+    row m's adapter i = ids[m] (int32; negative: none), and returns `ys`.
+    `adapters` holds a pair (a [n, r, K], b [n, N_p, r]) for each of up to four
+    projections of x [M, K], all float16 or all bfloat16."""
+    return _step_result(_binding.lora(x, adapters, ids, ys, scales, workspace, _step_stream(x)), "qmm_lora")
 
 
 def qmm_logprobs_workspace_bytes(M: int, V: int, top_n: int) -> int:

@@ -1,0 +1,372 @@
+// Low-rank adapters of many requests beside a shared projection:
+//
+//   h_m = scale * A_id(m) x_m   (r values),   y_m += B_id(m) h_m
+//
+// Rows are taken 16 at a time, the columns of the matrix instructions. The adapters
+// that occur among them are found by their leaders: the first row of each. A
+// workgroup takes one leader's adapter and multiplies it with all 16 rows; what
+// belongs to rows of other adapters is dropped. So an adapter is read once for 16 rows,
+// however the rows are ordered, every row has one writer, and nothing is sorted.
+//
+// Down: 16 ranks by 16 rows in 16x16x32 instructions, the four waves of a workgroup
+// taking a quarter of its part of K each and adding up in LDS; parts of K in workgroups
+// of their own (a sum in order in the second kernel) until the GPU is full.
+// Up: 16 columns of the projection by 16 rows. h enters as the sum of 16-bit numbers
+// (two in fp16, three in bf16, whose products are exact), so that no rounding to the inputs'
+// type is added between the two products; in fp16 a row's h is multiplied by a power of two
+// that brings its largest value to 2^14 first. Ranks below 32 leave room in an
+// instruction's 32 places of contraction, which the further numbers take.
+//
+// Bound by the adapters' bytes for many requests, by y (read and written) for
+// prompts, and by two launches for few rows.
+#include "qmm_device.hpp"
+#include "qmm_kernels.hpp"
+#include "qmm_step.hpp"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int kRows = 16;         // rows of a block
+constexpr int kBatch = 8;         // steps of 32 along K whose operands are in flight together
+constexpr int kPass = kWaves * kBatch * 32;  // of K, by a workgroup at a time
+constexpr int kTiles = 4;         // 16-column tiles of a wave in the second product
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<_Float16> {
+    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+    static constexpr int kParts = 2;
+    static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Elem<__bf16> {
+    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+    static constexpr int kParts = 3;
+    static __device__ __forceinline__ float4_t mfma(x8 a, x8 b, float4_t c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+// The adapter of row `block * 16 + lane % 16` (-1: none), and the rows of the block
+// that are the first of theirs, as bits.
+struct Block {
+    int id;
+    uint32_t leaders;
+};
+__device__ __forceinline__ Block block_of(const LoraArgs &a, int block)
+{
+    const int n = threadIdx.x % 16, row = block * kRows + n;
+    int id = row < a.M ? a.ids[row] : -1;
+    id = id >= 0 && id < a.adapters ? id : -1;
+    bool first = id >= 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        first = first && !(i < n && __builtin_amdgcn_readlane(id, i) == id);
+    return Block{id, (uint32_t)__ballot(first) & 0xFFFFu};
+}
+
+// ---------------------------------------------------------------------------
+// h of one adapter: up to 32 ranks, one part of K.
+// ---------------------------------------------------------------------------
+template <typename T, int RT>  // tiles of 16 ranks
+__global__ __launch_bounds__(kThreads) void lora_down_kernel(const LoraArgs a)
+{
+    using E = Elem<T>;
+    using x8 = typename E::x8;
+    __shared__ float4_t sums[kWaves][RT][kWave];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, n = lane % 16, c = lane / 16;
+    const int z = blockIdx.x % a.parts, group = blockIdx.x / a.parts % a.rank_groups, p = blockIdx.x / a.parts / a.rank_groups;
+    const int block = blockIdx.y;
+    const Block rows = block_of(a, block);
+    const int row = block * kRows + n;
+    const T *x = static_cast<const T *>(a.x) + (int64_t)(row < a.M ? row : a.M - 1) * a.K + 8 * c;
+    // This workgroup's steps of 32, then this wave's.
+    const int steps = a.K / 32, per = (steps + a.parts - 1) / a.parts;
+    const int begin = z * per < steps ? z * per : steps, end = begin + per < steps ? begin + per : steps;
+    const int mine = (end - begin + kWaves - 1) / kWaves;
+    const int from = begin + wave * mine < end ? begin + wave * mine : end, to = from + mine < end ? from + mine : end;
+
+    uint32_t leaders = rows.leaders;
+    for (int skip = blockIdx.z; leaders != 0; skip = gridDim.z - 1) {
+        while (skip > 0 && leaders != 0) {
+            leaders &= leaders - 1;
+            --skip;
+        }
+        if (leaders == 0)
+            break;
+        const int id = __builtin_amdgcn_readlane(rows.id, __builtin_ctz(leaders));
+        leaders &= leaders - 1;
+        const T *w[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const int j = (group * RT + t) * 16 + n;
+            w[t] = static_cast<const T *>(a.proj[p].a) + ((int64_t)id * a.r + (j < a.r ? j : a.r - 1)) * a.K + 8 * c;
+        }
+        float4_t acc[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+            acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+        int s = from;
+        for (; s + kBatch <= to; s += kBatch) {
+            x8 xv[kBatch], wv[RT][kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                xv[i] = *reinterpret_cast<const x8 *>(x + (s + i) * 32);
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    wv[t][i] = *reinterpret_cast<const x8 *>(w[t] + (s + i) * 32);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    acc[t] = E::mfma(wv[t][i], xv[i], acc[t]);
+        }
+        for (; s < to; ++s) {
+            const x8 xv = *reinterpret_cast<const x8 *>(x + s * 32);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                acc[t] = E::mfma(*reinterpret_cast<const x8 *>(w[t] + s * 32), xv, acc[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+            sums[wave][t][lane] = acc[t];
+        __syncthreads();
+        if (wave < RT) {  // wave t adds up tile t: ranks 4c .. 4c+3 of row n
+            float4_t h = sums[0][wave][lane];
+#pragma unroll
+            for (int v = 1; v < kWaves; ++v)
+                h += sums[v][wave][lane];
+            const int j = (group * RT + wave) * 16 + 4 * c;
+            if (rows.id == id && j < a.r)
+                *reinterpret_cast<float4_t *>(a.h + (((int64_t)p * a.parts + z) * a.M + row) * a.r + j) = h;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// y += B h of one adapter for 16 rows and 16 * kTiles columns a wave. RP: the rank,
+// filled up to 8, 16 or a multiple of 32.
+// ---------------------------------------------------------------------------
+template <typename T, int RP>
+__global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
+{
+    using E = Elem<T>;
+    using x8 = typename E::x8;
+    constexpr int kSteps = RP < 32 ? 1 : RP / 32;         // operands of B
+    constexpr int kSlots = RP < 32 ? 32 / RP : 1;         // parts of h in one instruction
+    constexpr int kMul = (E::kParts + kSlots - 1) / kSlots;  // instructions for one operand of B
+    constexpr int kPitch = RP + 4;
+    __shared__ __align__(16) float h_lds[kRows * kPitch];
+    __shared__ uint32_t row_top[kRows];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, n = lane % 16, c = lane / 16;
+    int p = 0;
+#pragma unroll
+    for (int q = 1; q < kMaxProj; ++q)
+        p = q < a.count && (int)blockIdx.x >= a.proj[q].first ? q : p;
+    const LoraProj proj = a.proj[p];
+    const int block = blockIdx.y, row = block * kRows + n;
+    const int N = proj.N, n0 = (((int)blockIdx.x - proj.first) * kWaves + wave) * kTiles * 16;
+    const Block rows = block_of(a, block);
+    // Places of a lane's 8 values of the contraction.
+    const int j0 = RP >= 32 ? 8 * c : RP == 16 ? 8 * (c % 2) : 0;
+    const int slot = RP >= 32 ? 0 : RP == 16 ? c / 2 : c;
+    const bool even = N % 4 == 0;
+
+    uint32_t leaders = rows.leaders;
+    for (int skip = blockIdx.z; leaders != 0; skip = gridDim.z - 1) {
+        while (skip > 0 && leaders != 0) {
+            leaders &= leaders - 1;
+            --skip;
+        }
+        if (leaders == 0)
+            break;
+        const int id = __builtin_amdgcn_readlane(rows.id, __builtin_ctz(leaders));
+        leaders &= leaders - 1;
+        const bool own = rows.id == id;  // of this lane's row
+        // B and y are on their way while h is put together.
+        const T *b = static_cast<const T *>(proj.b) + (int64_t)id * N * a.r;
+        x8 bv[kTiles][kSteps];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const int col = n0 + t * 16 + n;
+            const T *from = b + (int64_t)(col < N ? col : N - 1) * a.r;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int j = j0 + 32 * s;
+                bv[t][s] = *reinterpret_cast<const x8 *>(from + (j < a.r ? j : 0));
+                if (j >= a.r)
+                    bv[t][s] = x8{};
+            }
+        }
+        float *y = proj.y + (int64_t)(own ? row : 0) * N;
+        float4_t yv[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const int col = n0 + t * 16 + 4 * c;
+            yv[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+            if (even) {
+                if (own && col < N)
+                    yv[t] = *reinterpret_cast<const float4_t *>(y + col);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (own && col + i < N)
+                        yv[t][i] = y[col + i];
+            }
+        }
+
+        if (threadIdx.x < kRows)
+            row_top[threadIdx.x] = 0;
+        __syncthreads();
+        const float scale = a.scales ? a.scales[id] : 1.f;
+        const int quads = a.r / 4;
+        for (int i = threadIdx.x; i < kRows * quads; i += kThreads) {
+            const int m = i / quads, q = i - m * quads;
+            const int r_id = __shfl(rows.id, m);  // (by whole waves: kRows * quads is a multiple of 32, see below)
+            float4_t h{0.f, 0.f, 0.f, 0.f};
+            if (r_id == id) {
+                const float *from = a.h + ((int64_t)p * a.parts * a.M + block * kRows + m) * a.r + 4 * q;
+#pragma unroll 4
+                for (int z = 0; z < a.parts; ++z)
+                    h += *reinterpret_cast<const float4_t *>(from + (int64_t)z * a.M * a.r);
+                h *= scale;
+            }
+            *reinterpret_cast<float4_t *>(h_lds + m * kPitch + 4 * q) = h;
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = __builtin_fabsf(h[k]);
+                top = f < __builtin_inff() && f > top ? f : top;
+            }
+            atomicMax(&row_top[m], __builtin_bit_cast(uint32_t, top));
+        }
+        __syncthreads();
+        // h of row n as operands: values j0 + 32 s .., part slot + kSlots q.
+        const uint32_t top = row_top[n];
+        const int lift = top == 0 ? 0 : 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
+        x8 hv[kSteps][kMul];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int j = j0 + 32 * s;
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = j < a.r ? __builtin_amdgcn_ldexpf(h_lds[n * kPitch + j + k], lift) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float rest = v[k];
+                T part[4] = {};
+#pragma unroll
+                for (int i = 0; i < E::kParts; ++i) {
+                    part[i] = (T)rest;
+                    const float f = (float)part[i];
+                    rest = __builtin_fabsf(f) == __builtin_inff() ? 0.f : rest - f;  // nothing is left of infinity
+                }
+#pragma unroll
+                for (int q = 0; q < kMul; ++q) {
+                    T pick = part[0];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < kSlots * kMul)
+                            pick = slot + kSlots * q == i ? (i < E::kParts ? part[i] : (T)0.f) : pick;
+                    hv[s][q][k] = pick;
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            float4_t acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int q = 0; q < kMul; ++q)
+                    acc = E::mfma(bv[t][s], hv[s][q], acc);
+            const int col = n0 + t * 16 + 4 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                yv[t][i] += __builtin_amdgcn_ldexpf(acc[i], -lift);
+            if (even) {
+                if (own && col < N)
+                    *reinterpret_cast<float4_t *>(y + col) = yv[t];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (own && col + i < N)
+                        y[col + i] = yv[t][i];
+            }
+        }
+        __syncthreads();  // h_lds is free again
+    }
+}
+
+template <typename T>
+hipError_t launch(const LoraArgs &a, const LoraPlan &p, hipStream_t stream)
+{
+    const dim3 down(p.down_x, p.blocks, p.down_z), up(p.up_x, p.blocks, p.up_z);
+    if (a.r <= 16)
+        lora_down_kernel<T, 1><<<down, kThreads, 0, stream>>>(a);
+    else
+        lora_down_kernel<T, 2><<<down, kThreads, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    if (a.r <= 8)
+        lora_up_kernel<T, 8><<<up, kThreads, 0, stream>>>(a);
+    else if (a.r <= 16)
+        lora_up_kernel<T, 16><<<up, kThreads, 0, stream>>>(a);
+    else if (a.r <= 32)
+        lora_up_kernel<T, 32><<<up, kThreads, 0, stream>>>(a);
+    else if (a.r <= 64)
+        lora_up_kernel<T, 64><<<up, kThreads, 0, stream>>>(a);
+    else
+        lora_up_kernel<T, 128><<<up, kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+int clamped(int64_t v, int lo, int hi) { return (int)(v < lo ? lo : v > hi ? hi : v); }
+
+}  // namespace
+
+LoraPlan lora_plan(int count, const int *N, int M, int K, int r, int adapters)
+{
+    LoraPlan p;
+    p.blocks = (M + kRows - 1) / kRows;
+    p.rank_groups = r <= 16 ? 1 : (r + 31) / 32;
+    const int most = kRows < adapters ? kRows : adapters, slots = M < most ? M : most;
+    // Workgroups: parts of K first, down to one pass of a workgroup (1024 values);
+    // then the adapters of a block. Four on a CU are wanted.
+    const int64_t want = 4 * (int64_t)device_cu_count(), base = (int64_t)p.blocks * p.rank_groups * count;
+    p.parts = clamped((want + base - 1) / base, 1, (K + kPass - 1) / kPass);
+    p.down_x = p.parts * p.rank_groups * count;
+    p.down_z = clamped((want * 4 + base * p.parts - 1) / (base * p.parts), 1, slots);
+    p.up_x = 0;
+    for (int i = 0; i < count; ++i)
+        p.up_x += (N[i] + kWaves * kTiles * 16 - 1) / (kWaves * kTiles * 16);
+    const int64_t ups = (int64_t)p.up_x * p.blocks;
+    p.up_z = clamped((want * 4 + ups - 1) / ups, 1, slots);
+    p.workspace_bytes = sizeof(float) * count * p.parts * (size_t)M * r;
+    return p;
+}
+
+hipError_t launch_lora(LoraArgs a, const LoraPlan &p, bool bf16, void *workspace, hipStream_t stream)
+{
+    a.parts = p.parts;
+    a.rank_groups = p.rank_groups;
+    a.h = static_cast<float *>(workspace);
+    int first = 0;
+    for (int i = 0; i < a.count; ++i) {
+        a.proj[i].first = first;
+        first += (a.proj[i].N + kWaves * kTiles * 16 - 1) / (kWaves * kTiles * 16);
+    }
+    return bf16 ? launch<__bf16>(a, p, stream) : launch<_Float16>(a, p, stream);
+}
+
+}  // namespace qmm

@@ -48,6 +48,23 @@ qmm::AttnPlan plan_of(int B, int Hq, int Hkv, int D, int max_rows, int max_conte
                           max_pages, bits);
 }
 
+int check_lora_sizes(int count, const int *N, int M, int K, int r, int adapters)
+{
+    if (count < 1 || count > QMM_MAX_FUSED || M < 1 || K < 32 || K % 32 != 0 || r < 8 || r > 128 || r % 8 != 0 ||
+        adapters < 1)
+        return QMM_ERR_SHAPE;
+    if (M > 65535 * 16 || K > (1 << 28))  // blocks of 16 rows along a grid's y
+        return QMM_ERR_SHAPE;
+    for (int i = 0; i < count; ++i)
+        if (N[i] < 1 || N[i] > (1 << 28))
+            return QMM_ERR_SHAPE;
+    // the runtime counts a launch's threads in 32 bits
+    const qmm::LoraPlan p = qmm::lora_plan(count, N, M, K, r, adapters);
+    const uint64_t most = UINT32_MAX / 256;
+    return (uint64_t)p.blocks * p.down_x * p.down_z > most || (uint64_t)p.blocks * p.up_x * p.up_z > most ? QMM_ERR_SHAPE
+                                                                                                      : QMM_OK;
+}
+
 int check_logprobs_sizes(int M, int V, int n)
 {
     if (M < 1 || V < 1 || V > (1 << 23) || n < 0 || n > 64)
@@ -376,6 +393,50 @@ int qmm_sample(const void *logits, int64_t row_stride, int type, const float *u,
     a.M = M;
     a.V = V;
     return qmm::launch_sample(a, type, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
+}
+
+size_t qmm_lora_workspace_bytes(int count, const int *N, int M, int K, int r, int adapters)
+{
+    return !N || check_lora_sizes(count, N, M, K, r, adapters) != QMM_OK
+               ? 0
+               : qmm::lora_plan(count, N, M, K, r, adapters).workspace_bytes;
+}
+
+int qmm_lora(const void *x, int type, int count, const void *const *a, const void *const *b, float *const *y,
+             const int *N, const int32_t *ids, const float *scales, int M, int K, int r, int adapters, void *workspace,
+             size_t workspace_bytes, hipStream_t stream)
+{
+    if (!x || !a || !b || !y || !N || !ids)
+        return QMM_ERR_NULL;
+    if (!output_type(type))
+        return QMM_ERR_TYPE;
+    const int rc = check_lora_sizes(count, N, M, K, r, adapters);
+    if (rc != QMM_OK)
+        return rc;
+    const qmm::LoraPlan plan = qmm::lora_plan(count, N, M, K, r, adapters);
+    if (!workspace)
+        return QMM_ERR_NULL;
+    if (workspace_bytes < plan.workspace_bytes)
+        return QMM_ERR_WORKSPACE;
+    qmm::LoraArgs l{};
+    for (int i = 0; i < count; ++i) {
+        if (!a[i] || !b[i] || !y[i])
+            return QMM_ERR_NULL;
+        if (!aligned(a[i], 16) || !aligned(b[i], 16) || !aligned(y[i], 16))
+            return QMM_ERR_ALIGN;
+        l.proj[i] = qmm::LoraProj{a[i], b[i], y[i], N[i], 0};
+    }
+    if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(scales, 4))
+        return QMM_ERR_ALIGN;
+    l.x = x;
+    l.ids = ids;
+    l.scales = scales;
+    l.count = count;
+    l.M = M;
+    l.K = K;
+    l.r = r;
+    l.adapters = adapters;
+    return qmm::launch_lora(l, plan, type == QMM_BF16, workspace, stream) == hipSuccess ? QMM_OK : QMM_ERR_LAUNCH;
 }
 
 size_t qmm_logprobs_workspace_bytes(int M, int V, int n)

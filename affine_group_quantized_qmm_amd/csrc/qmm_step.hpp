@@ -103,6 +103,30 @@ bool sample_size_supported(int V);
 size_t sample_workspace_bytes(int M, int V);
 hipError_t launch_sample(const SampleArgs &a, int type, hipStream_t stream);
 
+// Low-rank adapters beside a projection (qmm_lora.hip).
+struct LoraProj {
+    const void *a, *b;                        // [adapters, r, K], [adapters, N, r]
+    float *y;                                 // [M, N]
+    int N;
+    int first;                                // the first workgroup of its columns
+};
+struct LoraArgs {
+    const void *x;                            // [M, K]
+    const int32_t *ids;                       // [M]
+    const float *scales;                      // [adapters] or null
+    float *h;                                 // [count, parts, M, r]
+    LoraProj proj[4];                         // (kMaxProj)
+    int count, M, K, r, adapters;
+    int parts, rank_groups;                   // of K; of 32 ranks
+};
+struct LoraPlan {
+    int blocks, parts, rank_groups;           // blocks of 16 rows
+    int down_x, down_z, up_x, up_z;           // launches
+    size_t workspace_bytes;
+};
+LoraPlan lora_plan(int count, const int *N, int M, int K, int r, int adapters);
+hipError_t launch_lora(LoraArgs a, const LoraPlan &p, bool bf16, void *workspace, hipStream_t stream);
+
 // Log probabilities (qmm_logprobs.hip).
 struct LogprobPart {                          // of a slice of a row: see there
     float m;

@@ -542,7 +542,77 @@ PyObject *logprobs(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// (x, sequence of (a, b), ids, sequence of y, scales or None, workspace or None, stream)
+PyObject *lora(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject * {
+        args(n, 7);
+        const at::Tensor &x = tensor(o[0], "x");
+        if (x.dim() != 2)
+            throw Refused(PyExc_ValueError, "x must be 2-D [M, K]");
+        const Call c = on_gpu(x, "x");
+        const c10::DeviceGuard guard(c.device);
+        const at::ScalarType type = x.scalar_type();
+        if (type != at::kHalf && type != at::kBFloat16)
+            throw Refused(PyExc_TypeError, std::string("x must be float16 or bfloat16, got ") + c10::toString(type));
+        const int64_t M = x.size(0), K = x.size(1);
+        if (M > INT32_MAX || K > INT32_MAX)
+            throw Refused(PyExc_ValueError, "x's sizes do not fit 32 bits");
+        c.whole(x, "x", type, x.sizes());
+        if (!PySequence_Check(o[1]) || !PySequence_Check(o[3]) || THPVariable_Check(o[1]) || THPVariable_Check(o[3]))
+            throw Refused(PyExc_TypeError, "adapters must be a sequence of (a, b) pairs and ys one of tensors");
+        const Py_ssize_t count = PySequence_Size(o[1]);
+        if (count < 1 || count > QMM_MAX_FUSED || PySequence_Size(o[3]) != count)
+            throw Refused(PyExc_ValueError, "one to " + std::to_string(QMM_MAX_FUSED) + " projections, and a y for each");
+        struct Item {  // a borrowed element: the sequence holds it for the call
+            PyObject *p;
+            Item(PyObject *s, Py_ssize_t i) : p(PySequence_GetItem(s, i))
+            {
+                if (!p)
+                    throw Refused(nullptr, "");
+            }
+            ~Item() { Py_DECREF(p); }
+            Item(const Item &) = delete;
+        };
+        const void *a[QMM_MAX_FUSED], *b[QMM_MAX_FUSED];
+        float *y[QMM_MAX_FUSED];
+        int N[QMM_MAX_FUSED];
+        int64_t adapters = 0, r = 0;
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const Item pair(o[1], i), out(o[3], i);
+            if (!PySequence_Check(pair.p) || THPVariable_Check(pair.p) || PySequence_Size(pair.p) != 2)
+                throw Refused(PyExc_TypeError, "adapters must be a sequence of (a, b) pairs");
+            const Item ao(pair.p, 0), bo(pair.p, 1);
+            const at::Tensor &at = tensor(ao.p, "a"), &bt = tensor(bo.p, "b");
+            if (at.dim() != 3 || bt.dim() != 3)
+                throw Refused(PyExc_ValueError, "a must be 3-D [adapters, r, K] and b 3-D [adapters, N, r]");
+            if (i == 0) {
+                adapters = at.size(0);
+                r = at.size(1);
+            }
+            const int64_t cols = bt.size(1);
+            if (adapters > INT32_MAX || r > INT32_MAX || cols > INT32_MAX)
+                throw Refused(PyExc_ValueError, "the adapters' sizes do not fit 32 bits");
+            a[i] = c.whole(at, "a", type, at::IntArrayRef({adapters, r, K}));
+            b[i] = c.whole(bt, "b", type, at::IntArrayRef({adapters, cols, r}));
+            y[i] = static_cast<float *>(c.whole(out.p, "y", at::kFloat, {M, cols}));
+            N[i] = (int)cols;
+        }
+        const int32_t *ids = static_cast<const int32_t *>(c.whole(o[2], "ids", at::kInt, {M}));
+        const float *scales = static_cast<const float *>(c.whole_or_null(o[4], "scales", at::kFloat, {adapters}));
+        const hipStream_t stream = as_stream(o[6]);
+        const Workspace ws(o[5], qmm_lora_workspace_bytes((int)count, N, (int)M, (int)K, (int)r, (int)adapters), c.device);
+        const int code = qmm_lora(x.data_ptr(), type_code(type), (int)count, a, b, y, N, ids, scales, (int)M, (int)K, (int)r,
+                                  (int)adapters, ws.data, ws.bytes, stream);
+        if (code)
+            return PyLong_FromLong(code);
+        Py_INCREF(o[3]);
+        return o[3];
+    });
+}
+
 PyMethodDef methods[] = {
+    {"lora", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(lora)), METH_FASTCALL, nullptr},
     {"logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(logprobs)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)), METH_FASTCALL,

@@ -563,6 +563,37 @@ int qmm_sample(const void *logits, int64_t row_stride, int type, const float *u,
                size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * qmm_lora - low-rank adapters of many requests beside shared projections of the
+ * same activations: for row m with adapter i = ids[m], and each projection p < count
+ * (count <= QMM_MAX_FUSED),
+ *
+ *     y_p[m] += scales[i] * B_p[i] (A_p[i] x[m])
+ *
+ * on top of what the products (qmm_forward, qmm_forward_bf16, qmm_forward_fused)
+ * left in y. x [M, K] of `type` (fp16 or bf16) is what the products take; a, b, y and
+ * N are host arrays of `count` entries, read during the call only: a[p]
+ * [adapters, r, K] and b[p] [adapters, N[p], r] of `type`, y[p] fp32 [M, N[p]], no two
+ * of them overlapping. ids int32 [M]; a number that is negative or not below `adapters`
+ * means no adapter: that row of y is neither read nor written. scales fp32 [adapters]
+ * may be NULL (1). K a multiple of 32, r a multiple of 8 up to 128 (adapters of a lower
+ * rank are filled up with zeros), M up to 1048560. Rows may come in any order; rows of
+ * one request side by side read its adapter once for 16 of them.
+ * Products are accumulated in fp32. A_p x enters the second product, scaled, as the sum of
+ * two fp16 numbers (good to 2^-22 of itself, or 2^-39 of the row's largest where that
+ * is more) or three bf16 numbers (2^-24). Infinities and NaN reach the rows that they belong
+ * to. Reruns are bitwise identical.
+ * workspace: qmm_lora_workspace_bytes(count, N, M, K, r, adapters) bytes (0 for invalid
+ * sizes), contents irrelevant. x, a, b, y and the workspace are 16-byte aligned, ids
+ * and scales 4.
+ * Errors: QMM_ERR_NULL, QMM_ERR_TYPE, QMM_ERR_SHAPE, QMM_ERR_WORKSPACE,
+ * QMM_ERR_ALIGN, QMM_ERR_LAUNCH.
+ */
+size_t qmm_lora_workspace_bytes(int count, const int *N, int M, int K, int r, int adapters);
+int qmm_lora(const void *x, int type, int count, const void *const *a, const void *const *b,
+             float *const *y, const int *N, const int32_t *ids, const float *scales, int M, int K,
+             int r, int adapters, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * qmm_logprobs - log probabilities of given tokens, with their ranks, the entropy
  * and the most probable tokens of each row.
  *
