@@ -523,8 +523,7 @@ def qmm_paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits: int, G: int
     return _step_result(_binding.paged_attention_quant(q, k_codes, k_sb, v_codes, v_sb, bits, G, block_table,
                                                        context_lens, row_starts, max_rows, max_context, scale, window,
                                                        sinks, out, lse, workspace, _step_stream(q)),
-                        "qmm_paged_attention_quant", "qmm_logprobs_workspace_bytes", "qmm_logprobs",
-            "qmm_lora_workspace_bytes", "qmm_lora")
+                        "qmm_paged_attention_quant")
 
 
 def qmm_sample_workspace_bytes(M: int, V: int) -> int:
