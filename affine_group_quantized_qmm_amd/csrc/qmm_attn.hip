@@ -562,7 +562,7 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context,
     p.col_tiles = (int)((col_tiles + chunks - 1) / chunks);
     p.col_tiles += p.col_tiles == 5;
     p.chunks = (int)((col_tiles + p.col_tiles - 1) / p.col_tiles);
-    const int kTile = tile_of(D, p.col_tiles);
+    const int kTile = bits == 0 ? tile_of(D, p.col_tiles) : kCodesTile;
     int64_t visible = max_context;
     if (window > 0 && (int64_t)window + max_rows + sinks + 2 * kTile < visible)
         visible = (int64_t)window + max_rows + sinks + 2 * kTile;
@@ -572,7 +572,8 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int D, int max_rows, int max_context,
     // on a CU (a workgroup has a tile of each). More only add plans, partial
     // results and joins: 131071 tokens take 96 us with one on a CU and 111 with
     // two, heads of 64 with a window 24.3, 23.8 and 24.3 with two, three and four.
-    const int per_cu = waves_of(D, p.col_tiles) == 8 ? 1 : D >= 96 ? 2 : 3;
+    const int per_cu = bits != 0 ? codes_waves_per_simd(bits, D, p.col_tiles)
+                       : waves_of(D, p.col_tiles) == 8 ? 1 : D >= 96 ? 2 : 3;
     const int64_t full = (int64_t)per_cu * device_cu_count();
     // The runs count tiles in 31 bits, up to the block table's end.
     const int64_t most_tiles = items * ((int64_t)max_pages * page_size / kTile + 1);

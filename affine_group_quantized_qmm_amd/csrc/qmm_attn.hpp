@@ -24,6 +24,7 @@ constexpr int kJoinThreads = 1024;
 // spill with four.
 constexpr int waves_of(int D, int NT) { return D >= 192 || (D == 128 && NT == 6) ? 8 : 4; }
 constexpr int tile_of(int D, int NT) { return 16 * waves_of(D, NT); }
+constexpr int kCodesTile = 128;  // tokens of a tile over codes: 32 for each of four waves
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;   // token without a row in the cache
 
 typedef float float2_t __attribute__((ext_vector_type(2)));
@@ -321,11 +322,19 @@ __device__ __forceinline__ void lds_barrier()
 
 // Column tiles that a workgroup takes at most: with more, the accumulators
 // (D / 16 registers a tile) and the queries in LDS would leave room for one
-// workgroup on a CU instead of two. Codes of heads of 128 leave no registers for
-// six.
+// workgroup on a CU instead of two. Over codes each wave has the whole head's
+// accumulators (D / 4 registers a tile).
 constexpr int most_col_tiles(int D, bool codes = false)
 {
-    return D == 64 || (D == 128 && !codes) ? 6 : D == 96 || D == 128 ? 4 : 3;
+    return codes ? (D <= 96 ? 4 : D == 128 ? 3 : 2) : D == 64 || D == 128 ? 6 : D == 96 ? 4 : 3;
+}
+// Waves of a SIMD over codes: what the accumulators and a tile's codes leave room for.
+constexpr int codes_waves_per_simd(int bits, int D, int NT)
+{
+    return D == 64    ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
+           : D == 96  ? (NT == 1 ? 3 : NT == 4 ? 1 : 2)
+           : D == 128 ? (NT == 1 && bits == 4 ? 3 : NT == 3 && bits == 8 ? 1 : 2)
+                      : (NT == 1 && (D == 192 || bits == 4) ? 2 : 1);
 }
 
 // Join of the pieces of an item that several runs share:

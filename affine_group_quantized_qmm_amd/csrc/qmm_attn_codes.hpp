@@ -1,9 +1,26 @@
 // Attention of the newest rows of each sequence over a paged cache of 8- or 4-bit
-// codes: the same mathematics and layout of a call as over 16-bit rows
-// (qmm_attn.hip). A cache row comes in as codes with the (scale, bias) words of
-// its groups, and its numbers, fp16, are formed between the registers that a
-// tile was loaded to and LDS: one byte permutation, one packed subtraction and one packed
-// multiply-add for two values. From there on the products are those of fp16.
+// codes: the mathematics and the layout of a call of attention over 16-bit rows
+// (qmm_attn.hip), on the fp16 numbers that the codes stand for.
+//
+// Forming the numbers is what the kernel spends most of its instructions on (three
+// for two 8-bit codes, 17 for eight 4-bit ones), with a half or a
+// quarter of the bytes to wait for. So the rest is kept short: a wave is alone with
+// 32 tokens at a time from their loads to its own output, and workgroups meet only
+// at the end of an item.
+//
+//   S^T = K Q^T      A lane loads 16 bytes of the row of one token (n) at a time, and its
+//                    codes are operands as they come: K passes no LDS. The order of
+//                    the contraction is that of the loads, for the queries too.
+//   p = 2^(s - m)    a lane holds tokens 4c .. 4c + 3 of both 16-token halves of one
+//                    column, which are the 8 places of the second product's operand
+//   O^T += V^T P^T   as they lie: P stays in registers. V^T comes out of the wave's own
+//                    part of LDS with transposing reads, up to 128 values of the head at a
+//                    time.
+//
+// P is one fp16 number, scaled by 2^15: its rounding, 2^-11 at most, is below the codes'
+// own (half a step is 2^-9 of a group's range and more), and the largest weight, which is
+// a power of two when it raises the maximum, is exact. Over 16-bit rows it is two.
+// bf16 queries become fp16, brought to a common size by a power of two for each column.
 #pragma once
 
 #include "qmm_attn.hpp"
@@ -12,56 +29,87 @@
 namespace qmm {
 namespace {
 
+constexpr int kCodeWaves = kCodesTile / 32;
+
+// What a lane loads of a row at a time: `codes` codes, within one group.
+template <int BITS, int D>
+struct Piece {
+    static constexpr int codes = D % 128 == 0 && BITS == 4 ? 32 : D % 64 == 0 ? 16 : 8;
+    static constexpr int count = D / 4 / codes;  // of a lane
+    typedef uint32_t raw __attribute__((ext_vector_type(codes * BITS / 32)));
+};
+
+// The queries' operands of one column stay in registers while they are few.
+constexpr bool codes_queries_in_lds(int D, int NT) { return NT * D / 32 > 8; }
+
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+
 // Four outputs in their type.
-__device__ __forceinline__ u32x2 rounded4(const AttnArgs &a, float4_t v)
+__device__ __forceinline__ u32x2 rounded4(float4_t v, bool bf16)
 {
-    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
     typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-    if (a.io_bf16)
+    if (bf16)
         return __builtin_bit_cast(u32x2, b4{(__bf16)v.x, (__bf16)v.y, (__bf16)v.z, (__bf16)v.w});
-    return __builtin_bit_cast(u32x2, h4{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w});
+    return __builtin_bit_cast(u32x2, half4_t{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w});
+}
+
+// Largest magnitude of 8 bf16 values, as an fp32's bits.
+__device__ __forceinline__ uint32_t top_of(u32x4 v)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = v[k] << 16 & 0x7FFF0000u, hi = v[k] & 0x7FFF0000u;
+        top = lo > top ? lo : top;
+        top = hi > top ? hi : top;
+    }
+    return top;
+}
+// The exponent of the power of two that brings it to 2^14 .. 2^15; columns of zeros,
+// or with infinities or NaN, stay.
+__device__ __forceinline__ int lift_of(uint32_t top)
+{
+    return top == 0 || top >= 0x7F800000u ? 0 : 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
+}
+__device__ __forceinline__ half8_t lifted(u32x4 v, int lift)
+{
+    half8_t h;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        h[k] = (_Float16)__builtin_amdgcn_ldexpf(bf16_bits_to_float(v[k / 2] >> 16 * (k % 2) & 0xFFFFu), lift);
+    return h;
 }
 
 template <int BITS, int D, int NT>
-__global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_codes_kernel(const AttnArgs a)
+__global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, NT)) void attn_codes_kernel(const AttnArgs a)
 {
-    using T = _Float16;
-    using E = Elem<T>;
-    using x8 = typename E::x8;
-    using x4 = typename E::x4;
-    constexpr int kWaves = waves_of(D, NT), kTile = tile_of(D, NT);
+    using E = Elem<_Float16>;
+    using P = Piece<BITS, D>;
+    using Raw = typename P::raw;
+    constexpr int kWaves = kCodeWaves, kTile = kCodesTile;
     static_assert(kTile <= kAttnMostTile, "the host's limit on token numbers");
-    constexpr int KS = D / 32;                  // contraction steps of K Q^T; loads of a lane for K and for V
-    constexpr int DT = D / 16;                  // output tiles along the head
-    constexpr int DW = (DT + kWaves - 1) / kWaves;  // of one wave: tiles wave, wave + kWaves, ...
-    // A lane's share of 16 rows of a cache, as it is loaded: units of codes, each
-    // within one group, with their (scale, bias) words.
-    constexpr int kCodes = D % 64 == 0 ? 16 : 8;
-    typedef uint32_t Unit __attribute__((ext_vector_type(kCodes * BITS / 32)));
-    constexpr int U = D / kCodes;               // units of a cache row
-    constexpr int kLoads = U / 4;               // units of a lane
-    constexpr int kParts = kCodes / 8;          // 16 bytes in LDS for each 8 values
-    // LDS row of V: 32 bytes past the data shift consecutive rows by 8 banks,
-    // so that the 8 rows that a transposing read touches at a time do not collide.
-    constexpr int kPitch = 2 * D + 32;
-    constexpr int kColumn = kTile + 8;          // elements of a column of P: 16 bytes of padding for the same reason
-    // The queries' operands stay in registers (4 a step and column tile) while
-    // these are few, else in LDS, where the waves share them.
-    constexpr bool kQueriesInLds = NT * KS > 8;
-    // Each wave's 16 rows hold its K tile up to the first barrier of a turn, then V.
-    __shared__ __align__(16) char kv_lds[kTile * kPitch];
-    __shared__ __align__(16) T p_hi[NT * 16 * kColumn], p_lo[NT * 16 * kColumn];
-    __shared__ u32x4 q_lds[kQueriesInLds ? NT * KS * kWave : 1];
-    __shared__ float col_max[NT * 16], col_sum[kWaves][NT * 16];
-    __shared__ uint32_t query_top[kQueriesInLds ? NT * 16 : 1];  // largest magnitude of a column's queries, as bits
-    __shared__ u32x4 bad_tokens[kWaves / 4];  // a word for each wave; after the last tile whether its sums are not all finite
-    __shared__ uint32_t rows_lds[kTile];
+    constexpr int kColumns = 16 * NT;
+    constexpr int kPieces = P::count, kEights = P::codes / 8;  // of a lane in a row; operands of a piece
+    constexpr int KS = D / 32;                   // contraction steps of K Q^T
+    constexpr int DT = D / 16;                   // output tiles along the head
+    constexpr int kRowBytes = D * BITS / 8, kPieceBytes = P::codes * BITS / 8;
+    // V goes through LDS in parts of the head of whole pieces.
+    constexpr int kParts = D == 256 ? 2 : D == 192 ? 3 : 1, kPartPieces = kPieces / kParts, kPartTiles = DT / kParts;
+    // 32 bytes past the data shift consecutive rows by 8 banks, so that the 8 rows
+    // that a transposing read touches at a time do not collide.
+    constexpr int kPitch = 2 * D / kParts + 32;
+    constexpr int kWaveLds = 32 * kPitch;
+    constexpr bool kQueriesInLds = codes_queries_in_lds(D, NT);
+    // The waves' own parts; at the end of an item, 4 tiles of 16 columns of each wave.
+    constexpr int kJoinBytes = kWaves * 4 * kWave * 16;
+    __shared__ __align__(16) char lds[kWaves * kWaveLds > kJoinBytes ? kWaves * kWaveLds : kJoinBytes];
+    __shared__ half8_t q_lds[kQueriesInLds ? NT * KS * kWave : 1];
+    __shared__ uint32_t query_top[kQueriesInLds ? kColumns : 1];
+    __shared__ float wave_max[kWaves][kColumns], wave_sums[kWaves][kColumns];
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int c = lane / 16, n = lane % 16;
     const int G = a.G;
-    constexpr int kColumns = 16 * NT;
-
     Start at_first;
     if (!find_start<kTile, kColumns>(a, at_first))
         return;
@@ -70,14 +118,14 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_codes_kernel(
     int run_begin = at_first.run_begin, run_end = at_first.run_end, run_len = at_first.run_len;  // of sequence b
     const int w = at_first.w, here = at_first.here;
     const Runs runs = at_first.runs;
+    char *const my_lds = lds + wave * kWaveLds;
     const int tr_offset = (4 * c + n / 4) * kPitch + n % 4 * 8;
+    // Words of a row's groups, and the first piece's.
+    const uint32_t row_words = (D % 96 == 0 ? 3u : 1u) << a.words_shift;
+    const uint32_t lane_word = (uint32_t)(c * P::codes) >> a.code_shift;
+    const bool one_page = a.one_page, bf16 = a.io_bf16;
+    const int capacity = a.max_pages * a.page_size;
 
-    // Infinities and NaN in V of a tile that every row sees whole go through both
-    // products as they are, where infinity times a remainder of 0 or below is not
-    // infinity. They leave no output of the piece finite: then it is computed once
-    // more with every tile treated as partly visible (`careful`), which takes
-    // them one by one. Nothing is looked for in the tiles themselves.
-    bool careful = false;
     for (;; lds_barrier()) {  // the items of the run
     const int x0 = chunk * kColumns;
     const Span span = span_of<kTile>(a, run_begin, run_end, run_len, x0, kColumns);
@@ -88,188 +136,173 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_codes_kernel(
             int2{w, a.pieces ? w + here - 1 : owner_of(runs, item_unit + count - 1)};
 
     const int32_t *table = a.block_table + (int64_t)b * a.max_pages;
-    const int capacity = a.max_pages * a.page_size;
     const int last_token = span.pmax < capacity ? span.pmax : capacity - 1;
     auto first_of = [&](int x) {
-        return (x < span.sink_tiles ? x : span.low + x - span.sink_tiles) * kTile;
+        return (x < span.sink_tiles ? x : span.low + x - span.sink_tiles) * kTile + 32 * wave;
     };
-    // Token (16 * wave + n) of a tile: whether some row of the workgroup sees
-    // it. The others are not read: their pages may be gone, their values anything.
+    // Whether some row of the workgroup sees a token. The others are not read: their pages
+    // may be gone, their values anything.
     auto seen_by_any = [&](int j) {
         return j <= last_token && (a.window == 0 || j > span.pmin - a.window || j < a.sinks);
     };
     // Loads are issued without branches around them (past the end they go to the
-    // cache's first row): where paths with and without a load meet, the compiler
-    // has to wait for all that are in flight.
-    // Pages of whole multiples of 16 tokens: the wave's 16 tokens are in one
+    // cache's first row). Pages of whole multiples of 16 tokens: 16 tokens are in one
     // page, their rows one after the other.
-    const bool one_page = a.one_page;
-    auto look_up = [&](int x) -> int {
-        const int j0 = first_of(x) + 16 * wave, j = one_page ? j0 : j0 + n;
-        const bool seen = x < end && (one_page ? j0 <= last_token && (a.window == 0 || j0 + 15 > span.pmin - a.window ||
-                                                                     j0 < a.sinks)
-                                               : seen_by_any(j));
-        const int page = table[seen ? divide(j, a.page_magic, a.page_shift) : 0u];
-        return seen ? page : -1;
+    struct Pages {
+        int of[2];
     };
-    // The cache row of token 16 * wave + n, and where the wave's rows are one
-    // after the other the first of them.
+    auto look_up = [&](int x) -> Pages {
+        Pages p;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int j0 = first_of(x) + 16 * u, j = one_page ? j0 : j0 + n;
+            const bool seen = x < end && (one_page ? j0 <= last_token && (a.window == 0 || j0 + 15 > span.pmin - a.window ||
+                                                                         j0 < a.sinks)
+                                                   : seen_by_any(j));
+            const int page = table[seen ? divide(j, a.page_magic, a.page_shift) : 0u];
+            p.of[u] = seen ? page : -1;
+        }
+        return p;
+    };
+    // The cache rows of token n of each half, and where they are one after the other
+    // the first of them.
     struct Rows {
-        uint32_t mine, first;
+        uint32_t mine[2], first[2];
     };
-    auto rows_of = [&](int page, int x) -> Rows {
-        const int j0 = first_of(x) + 16 * wave;
-        Rows r{kNoRow, 0u};
-        if (one_page) {
-            const uint32_t p = __builtin_amdgcn_readfirstlane(page);
-            const uint32_t off = j0 - divide(j0, a.page_magic, a.page_shift) * a.page_size;
-            if (p < (uint32_t)a.num_pages) {
-                r.first = (p * a.Hkv + h) * a.page_size + off;
-                r.mine = seen_by_any(j0 + n) ? r.first + n : kNoRow;
+    auto rows_of = [&](Pages pages, int x) -> Rows {
+        Rows r;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int j0 = first_of(x) + 16 * u;
+            r.mine[u] = kNoRow;
+            r.first[u] = 0u;
+            if (one_page) {
+                const uint32_t p = __builtin_amdgcn_readfirstlane(pages.of[u]);
+                const uint32_t off = j0 - divide(j0, a.page_magic, a.page_shift) * a.page_size;
+                if (p < (uint32_t)a.num_pages) {
+                    r.first[u] = (p * a.Hkv + h) * a.page_size + off;
+                    r.mine[u] = seen_by_any(j0 + n) ? r.first[u] + n : kNoRow;
+                }
+            } else if ((uint32_t)pages.of[u] < (uint32_t)a.num_pages) {
+                const uint32_t off = j0 + n - divide(j0 + n, a.page_magic, a.page_shift) * a.page_size;
+                r.mine[u] = ((uint32_t)pages.of[u] * a.Hkv + h) * a.page_size + off;
             }
-        } else if ((uint32_t)page < (uint32_t)a.num_pages) {
-            const uint32_t off = j0 + n - divide(j0 + n, a.page_magic, a.page_shift) * a.page_size;
-            r.mine = ((uint32_t)page * a.Hkv + h) * a.page_size + off;
         }
         return r;
     };
-    // Rows in the cache are below 2^32, byte offsets are not: 64-bit products.
-    constexpr int kRowBytes = D * BITS / 8;
-    auto at = [&](const void *cache, uint32_t row) {
-        return static_cast<const char *>(cache) + (uint64_t)(row == kNoRow ? 0u : row) * kRowBytes;
+    // A lane's pieces of the rows of both halves, with their (scale, bias) words: piece
+    // 4 i + c of row n. Rows in the cache are below 2^32, byte offsets are not: 64-bit products.
+    struct Tile {
+        Raw r[2][kPieces];
+        uint32_t sb[2][kPieces];
     };
-    auto words_at = [&](const uint32_t *sb, uint32_t row) {
-        return sb + ((uint64_t)(row == kNoRow ? 0u : row) << a.words_shift) * (D % 96 == 0 ? 3 : 1);
-    };
-
-    // Whole rows of the wave's 16 tokens; to LDS in the same order.
-    Unit kr[kLoads], vr[kLoads];
-    uint32_t kw[kLoads], vw[kLoads];
-    // They are read once: the nontemporal hint gives 6.75 TB/s of such rows
-    // instead of 6.05.
-    auto load = [&](Unit (&r)[kLoads], uint32_t (&w)[kLoads], const void *cache, const uint32_t *sb, Rows rows) {
-        if (one_page) {
-            const Unit *p = reinterpret_cast<const Unit *>(static_cast<const char *>(cache) + (uint64_t)rows.first * kRowBytes);
+    auto load = [&](Tile &t, const void *cache, const uint32_t *sb, const Rows &rows) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                r[i] = __builtin_nontemporal_load(p + (i * kWave + lane));
-            const uint32_t *s = words_at(sb, rows.first);
+        for (int u = 0; u < 2; ++u) {
+            const char *from;
+            const uint32_t *words;
+            if (one_page) {
+                from = static_cast<const char *>(cache) + (uint64_t)rows.first[u] * kRowBytes + (n * kRowBytes + c * kPieceBytes);
+                words = sb + (uint64_t)rows.first[u] * row_words + (n * row_words + lane_word);
+            } else {
+                const uint32_t row = rows.mine[u] == kNoRow ? 0u : rows.mine[u];
+                from = static_cast<const char *>(cache) + (uint64_t)row * kRowBytes + c * kPieceBytes;
+                words = sb + (uint64_t)row * row_words + lane_word;
+            }
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                w[i] = s[(uint32_t)(i * kWave + lane) * kCodes >> a.code_shift];
-        } else {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int unit = i * kWave + lane;
-                const uint32_t row = __shfl(rows.mine, unit / U);
-                const Unit *p = reinterpret_cast<const Unit *>(at(cache, row)) + unit % U;
-                r[i] = __builtin_nontemporal_load(p);
-                w[i] = words_at(sb, row)[(uint32_t)(unit % U) * kCodes >> a.code_shift];
+            for (int i = 0; i < kPieces; ++i) {
+                // read once: past the caches
+                t.r[u][i] = __builtin_nontemporal_load(reinterpret_cast<const Raw *>(from + i * 4 * kPieceBytes));
+                t.sb[u][i] = words[(uint32_t)(i * 4 * P::codes) >> a.code_shift];
             }
         }
     };
-    // The 16 bytes of LDS that hold 8 values: unit i of the lane, part j.
-    auto place = [&](int i, int j) {
-        const int unit = i * kWave + lane;
-        return reinterpret_cast<u32x4 *>(kv_lds + (16 * wave + unit / U) * kPitch + (unit % U * kParts + j) * 16);
-    };
-    auto numbers = [&](const Unit (&r)[kLoads], const uint32_t (&w)[kLoads], int i, int j) -> u32x4 {
+    auto numbers = [&](Raw r, uint32_t sb, int e) -> u32x4 {  // eight e of a piece
         if constexpr (BITS == 8)
-            return eight_numbers(r[i][2 * j], r[i][2 * j + 1], w[i]);
+            return eight_numbers(r[2 * e], r[2 * e + 1], sb);
         else
-            return eight_numbers(r[i][j], w[i]);
+            return eight_numbers(r[e], sb);
     };
-    auto store = [&](const Unit (&r)[kLoads], const uint32_t (&w)[kLoads]) {
+    // Tokens of which a lane has a group whose last level may pass fp16's largest
+    // number, or whose scale or bias is infinite or NaN already.
+    auto not_finite = [&](const Tile &t, uint32_t present) -> uint32_t {
+        uint32_t tokens = 0;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
+        for (int u = 0; u < 2; ++u) {
+            uint32_t worst = 0;
 #pragma unroll
-            for (int j = 0; j < kParts; ++j)
-                *place(i, j) = numbers(r, w, i, j);
+            for (int i = 0; i < kPieces; ++i) {
+                const half2_t sb = __builtin_bit_cast(half2_t, t.sb[u][i] & 0x7FFF7FFFu);
+                const _Float16 last = __builtin_fmaf16(sb.x, (_Float16)(float)((1 << BITS) - 1), sb.y);
+                const uint32_t bits = __builtin_bit_cast(uint16_t, last);
+                worst = bits > worst ? bits : worst;
+            }
+            const uint64_t odd = __ballot(worst >= E::exponent);
+            const uint32_t two = (uint32_t)odd | (uint32_t)(odd >> 32);
+            tokens |= ((two | two >> 16) & 0xFFFFu) << 16 * u;
+        }
+        return tokens & present;
     };
 
-    int page = look_up(begin);
-    // Queries of column tile t, step q: column n's values 32 q + 8 c ...
+    // Queries of column tile t in the order of the pieces: step i * kEights + e has
+    // values (4 i + c) * codes + 8 e ..
     auto query_at = [&](int t, int q) {
         const int x = x0 + t * 16 + n;
         const bool live = x < span.n * G;
         const int r = live ? row_of_column(a, x) : 0, g = live ? x - r * G : 0;
-        return static_cast<const uint16_t *>(a.q) + (span.start + r) * a.q_stride + (int64_t)(h * G + g) * D + q * 32 + c * 8;
-    };
-    // bf16 queries of a quantized cache become fp16: a column's are multiplied by
-    // the power of two that brings the largest to 2^14 .. 2^15, which keeps their 8
-    // bits down to 2^-28 of it, and its scores are divided by it.
-    const bool convert = a.io_bf16;
-    auto top_of = [&](u32x4 v) {  // largest magnitude of 8 bf16 values, as an fp32's bits
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = v[k] << 16 & 0x7FFF0000u, hi = v[k] & 0x7FFF0000u;
-            top = lo > top ? lo : top;
-            top = hi > top ? hi : top;
-        }
-        return top;
-    };
-    auto lift_of = [&](uint32_t top) {  // exponent of that power; columns of zeros, or with infinities or NaN, stay
-        return top == 0 || top >= 0x7F800000u ? 0 : 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
-    };
-    auto lifted = [&](u32x4 v, int lift) {
-        half8_t h;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            h[k] = (_Float16)__builtin_amdgcn_ldexpf(bf16_bits_to_float(v[k / 2] >> 16 * (k % 2) & 0xFFFFu), lift);
-        return __builtin_bit_cast(u32x4, h);
+        return reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.q) + (span.start + r) * a.q_stride +
+                                               (int64_t)(h * G + g) * D + (4 * (q / kEights) + c) * P::codes + q % kEights * 8);
     };
     float score_scale[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
         score_scale[t] = a.scale_log2;
-    x8 qf[kQueriesInLds ? 1 : NT][KS];
+    half8_t qf[kQueriesInLds ? 1 : NT][KS];
     if constexpr (kQueriesInLds) {
-        constexpr int P = (NT * KS + kWaves - 1) / kWaves;
-        u32x4 v[P];
+        constexpr int kShare = (NT * KS + kWaves - 1) / kWaves;
+        u32x4 v[kShare];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {  // all in flight before the first is stored
-            const int piece = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
-            v[i] = *reinterpret_cast<const u32x4 *>(query_at(piece / KS, piece % KS));
+        for (int i = 0; i < kShare; ++i) {  // all in flight before the first is stored
+            const int one = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
+            v[i] = *query_at(one / KS, one % KS);
         }
-        if (convert) {
-            if (threadIdx.x < NT * 16)
+        if (bf16) {
+            if (threadIdx.x < kColumns)
                 query_top[threadIdx.x] = 0;
             lds_barrier();
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int piece = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
-                __hip_atomic_fetch_max(&query_top[piece / KS * 16 + n], top_of(v[i]), __ATOMIC_RELAXED,
+            for (int i = 0; i < kShare; ++i) {
+                const int one = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
+                __hip_atomic_fetch_max(&query_top[one / KS * 16 + n], top_of(v[i]), __ATOMIC_RELAXED,
                                        __HIP_MEMORY_SCOPE_WORKGROUP);
             }
             lds_barrier();
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int piece = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
-                v[i] = lifted(v[i], lift_of(query_top[piece / KS * 16 + n]));
-            }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
                 score_scale[t] = __builtin_amdgcn_ldexpf(a.scale_log2, -lift_of(query_top[t * 16 + n]));
         }
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int piece = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
-            q_lds[piece * kWave + lane] = v[i];
+        for (int i = 0; i < kShare; ++i) {
+            const int one = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
+            q_lds[one * kWave + lane] =
+                bf16 ? lifted(v[i], lift_of(query_top[one / KS * 16 + n])) : __builtin_bit_cast(half8_t, v[i]);
         }
+        lds_barrier();
     } else {
+        u32x4 v[NT][KS];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int q = 0; q < KS; ++q)
-                qf[t][q] = *reinterpret_cast<const x8 *>(query_at(t, q));
-        if (convert) {
+                v[t][q] = *query_at(t, q);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < NT; ++t) {
+            int lift = 0;
+            if (bf16) {
                 uint32_t top = 0;
 #pragma unroll
                 for (int q = 0; q < KS; ++q) {
-                    const uint32_t x = top_of(__builtin_bit_cast(u32x4, qf[t][q]));
+                    const uint32_t x = top_of(v[t][q]);
                     top = x > top ? x : top;
                 }
 #pragma unroll
@@ -277,12 +310,12 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_codes_kernel(
                     const uint32_t x = __shfl_xor(top, d);
                     top = x > top ? x : top;
                 }
-                const int lift = lift_of(top);
-#pragma unroll
-                for (int q = 0; q < KS; ++q)
-                    qf[t][q] = __builtin_bit_cast(x8, lifted(__builtin_bit_cast(u32x4, qf[t][q]), lift));
+                lift = lift_of(top);
                 score_scale[t] = __builtin_amdgcn_ldexpf(a.scale_log2, -lift);
             }
+#pragma unroll
+            for (int q = 0; q < KS; ++q)
+                qf[t][q] = bf16 ? lifted(v[t][q], lift) : __builtin_bit_cast(half8_t, v[t][q]);
         }
     }
     int pos[NT];  // positions of this lane's columns (-1: no such column)
@@ -291,284 +324,224 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_codes_kernel(
         const int x = x0 + t * 16 + n;
         pos[t] = x < span.n * G ? span.first_pos + row_of_column(a, x) : -1;
     }
-    if (threadIdx.x < NT * 16)
-        col_max[threadIdx.x] = -__builtin_inff();
-    Rows rows = rows_of(page, begin);
-    load(kr, kw, a.k_cache, a.k_sb, rows);
-    page = look_up(begin + 1);
-    load(vr, vw, a.v_cache, a.v_sb, rows);
-    lds_barrier();
 
-    float4_t acc[NT][DW];
+    float4_t acc[NT][DT];
     float m[NT], l[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         m[t] = -__builtin_inff();
         l[t] = 0.f;
 #pragma unroll
-        for (int d = 0; d < DW; ++d)
+        for (int d = 0; d < DT; ++d)
             acc[t][d] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
-    for (int x = begin; x < end; ++x) {
-        const int j0 = first_of(x) + 16 * wave;  // the wave's first token
-        const uint32_t present = (uint32_t)__ballot(rows.mine != kNoRow) & 0xFFFFu;
-        const uint32_t row_now = rows.mine;
+    {
+        Tile kt, vt;
+        Rows rows = rows_of(look_up(begin), begin);
+        load(kt, a.k_cache, a.k_sb, rows);
+        Pages pages = look_up(begin + 1);
+        load(vt, a.v_cache, a.v_sb, rows);
+        for (int x = begin; x < end; ++x) {
+            const int j0 = first_of(x);  // the wave's first token
+            const uint32_t present = ((uint32_t)__ballot(rows.mine[0] != kNoRow) & 0xFFFFu) |
+                                     (uint32_t)__ballot(rows.mine[1] != kNoRow) << 16;
 
-        store(kr, kw);
-        rows = rows_of(page, x + 1);
-        load(kr, kw, a.k_cache, a.k_sb, rows);
-        page = look_up(x + 2);
-        wave_lds_sync();
-        float4_t s[NT];
+            float4_t s[2][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            s[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < NT; ++t)
+                s[0][t] = s[1][t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < KS; ++q) {
-            const x8 kf = *reinterpret_cast<const x8 *>(kv_lds + (16 * wave + n) * kPitch + q * 64 + c * 16);
+            for (int q = 0; q < KS; ++q) {
+                half8_t kf[2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                x8 qv;
-                if constexpr (kQueriesInLds)
-                    qv = __builtin_bit_cast(x8, q_lds[(t * KS + q) * kWave + lane]);
-                else
-                    qv = qf[t][q];
-                s[t] = E::mfma(kf, qv, s[t]);
-            }
-            if (NT * KS >= 16 && q % 2 == 1)  // not all of the operands in registers at once
-                __builtin_amdgcn_sched_barrier(0);
-        }
-
-        // Tiles that not every row sees whole: scores that a row does not see
-        // are -infinity.
-        const bool partial = careful || present != 0xFFFFu || j0 + 15 > span.pmin ||
-                             (a.window > 0 && j0 <= span.pmax - a.window && j0 + 16 > a.sinks);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            s[t] *= score_scale[t];
-            if (partial) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = j0 + 4 * c + i;
-                    const bool sees = j <= pos[t] && (present >> (4 * c + i) & 1u) &&
-                                      (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
-                    s[t][i] = sees ? s[t][i] : -__builtin_inff();
-                }
-            }
-            const float top = fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3]));
-            if (top > m[t] + E::kRaise)
-                __hip_atomic_fetch_max(&col_max[t * 16 + n], top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        }
-        lds_barrier();  // the columns' maxima are in
-
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const float up = col_max[t * 16 + n];
-            if (__any(up > m[t])) {
-                const float f = up > m[t] ? __builtin_amdgcn_exp2f(m[t] - up) : 1.f;
-                m[t] = up;
-                l[t] *= f;
-#pragma unroll
-                for (int d = 0; d < DW; ++d)
-                    acc[t][d] *= f;
-            }
-            const float base = m[t] == -__builtin_inff() ? 0.f : m[t] - E::kLift;
-            x4 hi, lo;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p = __builtin_amdgcn_exp2f(s[t][i] - base);
-                l[t] += p;
-                hi[i] = (T)p;
-                lo[i] = (T)(p - (float)hi[i]);
-            }
-            const int to = (t * 16 + n) * kColumn + 16 * wave + 4 * c;
-            *reinterpret_cast<x4 *>(&p_hi[to]) = hi;
-            *reinterpret_cast<x4 *>(&p_lo[to]) = lo;
-        }
-        // V to LDS. In partly visible tiles, values that could poison a product
-        // with p = 0 are kept out: tokens without a row are cleared, non-finite
-        // values are cleared here and added back below for the rows that see them.
-        uint32_t bad = 0;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            u32x4 v[kParts];
-#pragma unroll
-            for (int j = 0; j < kParts; ++j)
-                v[j] = numbers(vr, vw, i, j);
-            if (partial) {
-                typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-                const int token = (i * kWave + lane) / U;
-                const bool there = present >> token & 1u;
-                u16x2 largest{0, 0};  // of the magnitudes' bits: an exponent of all ones is above every finite one
-#pragma unroll
-                for (int k = 0; k < 4 * kParts; ++k) {
-                    v[k / 4][k % 4] = there ? v[k / 4][k % 4] : 0u;
-                    largest = __builtin_elementwise_max(largest, __builtin_bit_cast(u16x2, v[k / 4][k % 4] & 0x7FFF7FFFu));
-                }
-                const bool odd = largest.x >= E::exponent || largest.y >= E::exponent;
-                if (__builtin_expect(__any(odd), 0)) {
-#pragma unroll
-                    for (int k = 0; k < 4 * kParts; ++k)
-                        v[k / 4][k % 4] = finite_halves<T>(v[k / 4][k % 4]);
-                    uint32_t here_bad = odd ? 1u << token : 0u;
-#pragma unroll
-                    for (int d = 1; d < kWave; d *= 2)
-                        here_bad |= __shfl_xor(here_bad, d);
-                    bad |= here_bad;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kParts; ++j)
-                *place(i, j) = v[j];
-            if constexpr (NT >= 3)  // not all of the numbers in registers at once
-                __builtin_amdgcn_sched_barrier(0);
-        }
-        if (lane < 16) {
-            rows_lds[16 * wave + lane] = row_now;
-            reinterpret_cast<uint32_t *>(bad_tokens)[wave] = bad;
-        }
-        load(vr, vw, a.v_cache, a.v_sb, rows);
-        lds_barrier();  // P and V are in
-
-        // Step q takes tokens 4c .. 4c+3 of waves 2q and 2q+1.
-#pragma unroll
-        for (int q = 0; q < kWaves / 2; ++q) {
-            x8 vt[DW];
-#pragma unroll
-            for (int d = 0; d < DW; ++d) {
-                const int dt = wave + kWaves * d;
-                if (DT % kWaves != 0 && dt >= DT)
-                    break;
-                typedef __attribute__((address_space(3))) short4_t lds4;
-                const char *p = kv_lds + tr_offset + 32 * q * kPitch + dt * 32;
-                const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
-                const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 16 * kPitch));
-                vt[d] = __builtin_bit_cast(x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int from = (t * 16 + n) * kColumn + 32 * q + 4 * c;
-                const x8 hi = __builtin_shufflevector(*reinterpret_cast<const x4 *>(&p_hi[from]),
-                                                      *reinterpret_cast<const x4 *>(&p_hi[from + 16]), 0, 1, 2, 3, 4, 5, 6, 7);
-                const x8 lo = __builtin_shufflevector(*reinterpret_cast<const x4 *>(&p_lo[from]),
-                                                      *reinterpret_cast<const x4 *>(&p_lo[from + 16]), 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-                for (int d = 0; d < DW; ++d) {
-                    if (DT % kWaves != 0 && wave + kWaves * d >= DT)
-                        break;
-                    acc[t][d] = E::mfma(vt[d], hi, acc[t][d]);
-                    acc[t][d] = E::mfma(vt[d], lo, acc[t][d]);
-                }
-                if constexpr (NT >= 3)  // not all of the operands in registers at once
-                    __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-
-        u32x4 any_bad = bad_tokens[0];
-        if constexpr (kWaves == 8)
-            any_bad |= bad_tokens[1];
-        const uint32_t some = __builtin_amdgcn_readfirstlane(any_bad.x | any_bad.y | any_bad.z | any_bad.w);
-        for (int v = 0; __builtin_expect(some != 0, 0) && v < kWaves; ++v) {
-            uint32_t left = __builtin_amdgcn_readfirstlane(reinterpret_cast<const uint32_t *>(bad_tokens)[v]);
-            while (left) {  // a token of a partly visible tile holds infinities or NaN
-                const int tok = 16 * v + __builtin_ctz(left);
-                left &= left - 1;
-                const int j = first_of(x) + tok;
-                const char *vp = at(a.v_cache, rows_lds[tok]);
+                for (int u = 0; u < 2; ++u)
+                    kf[u] = __builtin_bit_cast(half8_t, numbers(kt.r[u][q / kEights], kt.sb[u][q / kEights], q % kEights));
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const int from = (t * 16 + n) * kColumn + tok;
-                    // a weight that was too small for its type is not zero
-                    const float p = (float)p_hi[from] + (float)p_lo[from] + 0x1p-126f;
-                    const bool sees = j <= pos[t] && (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
-#pragma unroll
-                    for (int d = 0; d < DW; ++d) {
-                        const int dt = wave + kWaves * d;
-                        if (DT % kWaves != 0 && dt >= DT)
-                            break;
-                        const int first = dt * 16 + 4 * c;  // of 4 codes
-                        uint32_t bytes;
-                        if constexpr (BITS == 8) {
-                            bytes = *reinterpret_cast<const uint32_t *>(vp + first);
-                        } else {
-                            const uint32_t w = *reinterpret_cast<const uint16_t *>(vp + first / 2);
-                            bytes = (w & 15) | (w & 0xF0) << 4 | (w & 0xF00) << 8 | (w & 0xF000) << 12;
-                        }
-                        const half2_t sb = __builtin_bit_cast(half2_t, words_at(a.v_sb, rows_lds[tok])[first >> a.code_shift]);
-                        const x4 v4 = __builtin_bit_cast(x4, code_numbers(bytes, half2_t{sb.x, sb.x}, half2_t{sb.y, sb.y}));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float f = (float)v4[i];
-                            const bool odd = !(__builtin_fabsf(f) < __builtin_inff());
-                            acc[t][d][i] += odd && sees ? p * f : 0.f;
-                        }
-                        __builtin_amdgcn_sched_barrier(0);  // rare: few registers rather than loads in flight
-                    }
+                    half8_t qv;
+                    if constexpr (kQueriesInLds)
+                        qv = q_lds[(t * KS + q) * kWave + lane];
+                    else
+                        qv = qf[t][q];
+                    s[0][t] = E::mfma(kf[0], qv, s[0][t]);
+                    s[1][t] = E::mfma(kf[1], qv, s[1][t]);
                 }
             }
-        }
-        lds_barrier();  // every wave is past V and P
-    }
+            rows = rows_of(pages, x + 1);
+            load(kt, a.k_cache, a.k_sb, rows);
+            pages = look_up(x + 2);
 
-    // Sums of the columns over the lanes and waves that share them.
-    float zero = 0.f;  // NaN if some sum is not finite
+            // Tiles that not every row sees whole: scores that a row does not see
+            // are -infinity.
+            const bool partial = present != 0xFFFFFFFFu || j0 + 31 > span.pmin ||
+                                 (a.window > 0 && j0 <= span.pmax - a.window && j0 + 32 > a.sinks);
+            half8_t weights[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    p[i] = s[i / 4][t][i % 4] * score_scale[t];
+                if (partial) {
+                    int first = 4 * c;  // (not kept in registers over the loop in eight forms)
+                    pin_register(first);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = first + 16 * (i / 4) + i % 4, j = j0 + at;
+                        const bool sees = j <= pos[t] && (present >> at & 1u) &&
+                                          (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
+                        p[i] = sees ? p[i] : -__builtin_inff();
+                    }
+                }
+                float top = p[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i)
+                    top = __builtin_fmaxf(top, p[i]);
+                // The maxima are raised only when some score passes them by kRaise,
+                // which bounds p and leaves nothing to exchange in most turns.
+                if (__any(top > m[t] + E::kRaise)) {
+                    top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+                    top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+                    const float f = top > m[t] ? __builtin_amdgcn_exp2f(m[t] - top) : 1.f;
+                    m[t] = top > m[t] ? top : m[t];
+                    l[t] *= f;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        acc[t][d] *= f;
+                }
+                const float base = m[t] == -__builtin_inff() ? 0.f : m[t] - E::kLift;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = __builtin_amdgcn_exp2f(p[i] - base);
+                    l[t] += p[i];
+                    weights[t][i] = (_Float16)p[i];
+                }
+            }
+
+            // V to LDS, without tokens that no row sees, whose places may hold anything,
+            // and without those whose numbers may be infinite or NaN, which would reach every
+            // column: a scale and bias of 0 make zeros of them.
+            const uint32_t bad = not_finite(vt, present);
+            auto through_lds = [&](uint32_t tokens, auto use) {
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int k = 0; k < kPartPieces; ++k) {
+                            const int i = part * kPartPieces + k;
+                            const uint32_t sb = tokens >> (16 * u + n) & 1u ? vt.sb[u][i] : 0u;
+#pragma unroll
+                            for (int e = 0; e < kEights; ++e)
+                                *reinterpret_cast<u32x4 *>(my_lds + (16 * u + n) * kPitch +
+                                                           ((4 * k + c) * P::codes + 8 * e) * 2) =
+                                    numbers(vt.r[u][i], sb, e);
+                        }
+                    wave_lds_sync();
+#pragma unroll
+                    for (int d = 0; d < kPartTiles; ++d) {
+                        typedef __attribute__((address_space(3))) short4_t lds4;
+                        const char *from = my_lds + tr_offset + d * 32;
+                        const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)from);
+                        const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(from + 16 * kPitch));
+                        const half8_t vf =
+                            __builtin_bit_cast(half8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            use(vf, t, acc[t][part * kPartTiles + d]);
+                    }
+                    wave_lds_sync();
+                }
+            };
+            through_lds(present & ~bad, [&](half8_t vf, int t, float4_t &o) { o = E::mfma(vf, weights[t], o); });
+            // The others one by one, into the columns that see them alone.
+            for (uint32_t todo = bad; __builtin_expect(todo != 0, 0); todo &= todo - 1) {
+                const int tok = __builtin_amdgcn_readfirstlane(__builtin_ctz(todo)), j = j0 + tok;
+                // The codes are taken apart once more, and not kept for this.
+#pragma unroll
+                for (int i = 0; i < 2 * kPieces; ++i)
+#pragma unroll
+                    for (int k = 0; k < P::codes * BITS / 32; ++k) {
+                        uint32_t word = vt.r[i / kPieces][i % kPieces][k];
+                        pin_register(word);
+                        vt.r[i / kPieces][i % kPieces][k] = word;
+                    }
+                auto sees = [&](int t) {
+                    return j <= pos[t] && (a.window == 0 || j > pos[t] - a.window || j < a.sinks);
+                };
+                through_lds(1u << tok, [&](half8_t vf, int t, float4_t &o) {
+                    half8_t some = weights[t];  // a weight that was too small for its type is not zero
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        some[i] = some[i] == (_Float16)0 ? (_Float16)0x1p-24f : some[i];
+                    const float4_t with = E::mfma(vf, some, o);
+                    o = sees(t) ? with : o;
+                });
+            }
+            load(vt, a.v_cache, a.v_sb, rows);
+        }
+    }
+    // What follows knows its lanes anew: nothing of it stays in registers over the loop.
+    int lane_end = lane;
+    pin_register(lane_end);
+    const int n_end = lane_end % 16, c_end = lane_end / 16;
+    // The waves' sums meet.
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         l[t] += __shfl_xor(l[t], 16);
         l[t] += __shfl_xor(l[t], 32);
-        if (c == 0)
-            col_sum[wave][t * 16 + n] = l[t];
-#pragma unroll
-        for (int d = 0; d < DW; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                zero = __builtin_fmaf(acc[t][d][i], 0.f, zero);
+        if (c_end == 0) {
+            wave_max[wave][t * 16 + n_end] = m[t];
+            wave_sums[wave][t * 16 + n_end] = l[t];
+        }
     }
-    const uint32_t odd = __any(zero != 0.f);
-    if (lane == 0)
-        reinterpret_cast<uint32_t *>(bad_tokens)[wave] = odd;
     lds_barrier();
-    u32x4 any_odd = bad_tokens[0];
-    if constexpr (kWaves == 8)
-        any_odd |= bad_tokens[1];
-    if (!careful && __builtin_amdgcn_readfirstlane(any_odd.x | any_odd.y | any_odd.z | any_odd.w)) {
-        careful = true;
-        continue;
-    }
-    careful = false;
+    float4_t *const meet = reinterpret_cast<float4_t *>(lds);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int x = x0 + t * 16 + n;
-        if (x >= span.n * G)
-            continue;
-        float total = 0.f;
+        float top = -__builtin_inff(), total = 0.f;
 #pragma unroll
         for (int v = 0; v < kWaves; ++v)
-            total += col_sum[v][t * 16 + n];
-        const int r = row_of_column(a, x);
+            top = __builtin_fmaxf(top, wave_max[v][t * 16 + n_end]);
+        auto factor = [&](float of) { return of == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(of - top); };
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v)
+            total += wave_sums[v][t * 16 + n_end] * factor(wave_max[v][t * 16 + n_end]);
+        const float mine = factor(m[t]);
+        const int x = x0 + t * 16 + n_end;
+        const bool live = x < span.n * G;
+        const int r = row_of_column(a, live ? x : x0);
         const int64_t at_row = (int64_t)(span.start + r) * a.Hq + h * G + (x - r * G);
-        const bool first = wave == 0 && c == 0;
-        if (begin == 0 && end == count) {
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-            uint16_t *to = static_cast<uint16_t *>(a.out) + at_row * D + wave * 16 + 4 * c;
-#pragma unroll
-            for (int d = 0; d < DW; ++d) {
-                const u32x2 y = rounded4(a, acc[t][d] * inv);  // the output's one rounding
-                if (DT % kWaves == 0 || wave + kWaves * d < DT)
-                    *reinterpret_cast<u32x2 *>(to + kWaves * d * 16) = y;
-            }
-            if (first && a.lse)
+        const int64_t part = (int64_t)slot_of(w, begin == 0) * kColumns + t * 16 + n_end;
+        const bool all = begin == 0 && end == count;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        if (live && wave == 0 && c_end == 0) {
+            if (!all)
+                *reinterpret_cast<float2_t *>(a.part_ml + part * 2) = float2_t{top, total};
+            else if (a.lse)
                 a.lse[at_row] = total == 0.f ? -__builtin_inff()
-                                             : (m[t] + __builtin_amdgcn_logf(total * E::kUnlift)) * 0.69314718055994530942f;
-        } else {
-            const int64_t part = (int64_t)slot_of(w, begin == 0) * kColumns + t * 16 + n;
-            float *to = a.part_acc + part * D + wave * 16 + 4 * c;
+                                             : (top + __builtin_amdgcn_logf(total * E::kUnlift)) * 0.69314718055994530942f;
+        }
+        // Four tiles of the head at a time, each added up by one wave.
 #pragma unroll
-            for (int d = 0; d < DW; ++d)
-                if (DT % kWaves == 0 || wave + kWaves * d < DT)
-                    *reinterpret_cast<float4_t *>(to + kWaves * d * 16) = acc[t][d];
-            if (first)
-                *reinterpret_cast<float2_t *>(a.part_ml + part * 2) = float2_t{m[t], total};
+        for (int d0 = 0; d0 < DT; d0 += 4) {
+            if (t + d0 > 0)
+                lds_barrier();
+#pragma unroll
+            for (int k = 0; k < 4 && d0 + k < DT; ++k)
+                meet[(wave * 4 + k) * kWave + lane] = acc[t][d0 + k] * mine;
+            lds_barrier();
+            if (d0 + wave < DT) {
+                float4_t o = meet[wave * kWave + lane];
+#pragma unroll
+                for (int v = 1; v < kWaves; ++v)
+                    o += meet[(v * 4 + wave) * kWave + lane];
+                const int d = (d0 + wave) * 16 + 4 * c_end;
+                if (live && all)
+                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at_row * D + d) = rounded4(o * inv, bf16);
+                else if (live)
+                    *reinterpret_cast<float4_t *>(a.part_acc + part * D + d) = o;
+            }
         }
     }
 
@@ -595,7 +568,7 @@ __global__ __launch_bounds__(waves_of(D, NT) * kWave, 2) void attn_codes_kernel(
 template <int BITS, int D, int NT>
 hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
-    attn_codes_kernel<BITS, D, NT><<<dim3((uint32_t)p.blocks), waves_of(D, NT) * kWave, 0, stream>>>(a);
+    attn_codes_kernel<BITS, D, NT><<<dim3((uint32_t)p.blocks), kCodeWaves * kWave, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.whole)
         return e;
@@ -610,17 +583,17 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 template <int BITS, int D>
 hipError_t launch_cols(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
+    constexpr int most = most_col_tiles(D, true);
     switch (p.col_tiles) {
     case 1: return launch<BITS, D, 1>(a, p, stream);
     case 2: return launch<BITS, D, 2>(a, p, stream);
-    case 3: return launch<BITS, D, 3>(a, p, stream);
-    case 4:
-        if constexpr (most_col_tiles(D, true) >= 4)
-            return launch<BITS, D, 4>(a, p, stream);
+    case 3:
+        if constexpr (most >= 3)
+            return launch<BITS, D, 3>(a, p, stream);
         return hipErrorInvalidValue;
-    case 6:
-        if constexpr (most_col_tiles(D, true) >= 6)
-            return launch<BITS, D, 6>(a, p, stream);
+    case 4:
+        if constexpr (most >= 4)
+            return launch<BITS, D, 4>(a, p, stream);
         return hipErrorInvalidValue;
     default: return hipErrorInvalidValue;
     }
