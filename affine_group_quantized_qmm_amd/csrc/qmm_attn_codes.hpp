@@ -8,14 +8,16 @@
 // 32 tokens at a time from their loads to its own output, and workgroups meet only
 // at the end of an item.
 //
-//   S^T = K Q^T      A lane loads 16 bytes of the row of one token (n) at a time, and its
-//                    codes are operands as they come: K passes no LDS. The order of
-//                    the contraction is that of the loads, for the queries too.
+//   S^T = K Q^T      Rows are loaded whole, 16 bytes a lane, and pass the wave's own part
+//                    of LDS as codes, from where a lane has the 16 bytes of the token whose
+//                    operand it holds (loading them so would ask the address unit for
+//                    64 places instead of 16: 64 sequences, 8 heads of 128, 8 bits
+//                    178 us). The order of the contraction is that of the pieces, for
+//                    the queries too.
 //   p = 2^(s - m)    a lane holds tokens 4c .. 4c + 3 of both 16-token halves of one
 //                    column, which are the 8 places of the second product's operand
-//   O^T += V^T P^T   as they lie: P stays in registers. V^T comes out of the wave's own
-//                    part of LDS with transposing reads, up to 128 values of the head at a
-//                    time.
+//   O^T += V^T P^T   as they lie: P stays in registers. V^T comes out of the wave's part of
+//                    LDS with transposing reads.
 //
 // P is one fp16 number, scaled by 2^15: its rounding, 2^-11 at most, is below the codes'
 // own (half a step is 2^-9 of a group's range and more), and the largest weight, which is
@@ -35,12 +37,9 @@ constexpr int kCodeWaves = kCodesTile / 32;
 template <int BITS, int D>
 struct Piece {
     static constexpr int codes = D % 128 == 0 && BITS == 4 ? 32 : D % 64 == 0 ? 16 : 8;
-    static constexpr int count = D / 4 / codes;  // of a lane
+    static constexpr int in_row = D / codes, count = in_row / 4;  // of a lane: pieces of 16 rows
     typedef uint32_t raw __attribute__((ext_vector_type(codes * BITS / 32)));
 };
-
-// The queries' operands of one column stay in registers while they are few.
-constexpr bool codes_queries_in_lds(int D, int NT) { return NT * D / 32 > 8; }
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
@@ -89,22 +88,20 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
     constexpr int kWaves = kCodeWaves, kTile = kCodesTile;
     static_assert(kTile <= kAttnMostTile, "the host's limit on token numbers");
     constexpr int kColumns = 16 * NT;
-    constexpr int kPieces = P::count, kEights = P::codes / 8;  // of a lane in a row; operands of a piece
+    constexpr int kPieces = P::count, U = P::in_row, kEights = P::codes / 8;  // kEights: operands of a piece
     constexpr int KS = D / 32;                   // contraction steps of K Q^T
     constexpr int DT = D / 16;                   // output tiles along the head
     constexpr int kRowBytes = D * BITS / 8, kPieceBytes = P::codes * BITS / 8;
-    // V goes through LDS in parts of the head of whole pieces.
-    constexpr int kParts = D == 256 ? 2 : D == 192 ? 3 : 1, kPartPieces = kPieces / kParts, kPartTiles = DT / kParts;
-    // 32 bytes past the data shift consecutive rows by 8 banks, so that the 8 rows
-    // that a transposing read touches at a time do not collide.
-    constexpr int kPitch = 2 * D / kParts + 32;
+    // A wave's part of LDS holds 32 rows: first K's as codes, then V's as numbers. 32
+    // bytes past the data shift consecutive rows of V by 8 banks, so that the 8 rows
+    // that a transposing read touches at a time do not collide; 16 do it for K's.
+    constexpr int kPitch = 2 * D + 32, kCodePitch = kRowBytes + 16;
     constexpr int kWaveLds = 32 * kPitch;
-    constexpr bool kQueriesInLds = codes_queries_in_lds(D, NT);
-    // The waves' own parts; at the end of an item, 4 tiles of 16 columns of each wave.
+    // At the end of an item: 4 tiles of 16 columns of each wave.
     constexpr int kJoinBytes = kWaves * 4 * kWave * 16;
     __shared__ __align__(16) char lds[kWaves * kWaveLds > kJoinBytes ? kWaves * kWaveLds : kJoinBytes];
-    __shared__ half8_t q_lds[kQueriesInLds ? NT * KS * kWave : 1];
-    __shared__ uint32_t query_top[kQueriesInLds ? kColumns : 1];
+    __shared__ half8_t q_lds[NT * KS * kWave];
+    __shared__ uint32_t query_top[kColumns];
     __shared__ float wave_max[kWaves][kColumns], wave_sums[kWaves][kColumns];
 
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -120,9 +117,11 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
     const Runs runs = at_first.runs;
     char *const my_lds = lds + wave * kWaveLds;
     const int tr_offset = (4 * c + n / 4) * kPitch + n % 4 * 8;
-    // Words of a row's groups, and the first piece's.
-    const uint32_t row_words = (D % 96 == 0 ? 3u : 1u) << a.words_shift;
-    const uint32_t lane_word = (uint32_t)(c * P::codes) >> a.code_shift;
+    const uint32_t row_words = (D % 96 == 0 ? 3u : 1u) << a.words_shift;  // groups of a row
+    // Words of a lane's first piece among those of 16 rows, as values and as keys; the
+    // further ones are whole groups of 4 or 64 pieces behind it.
+    const uint32_t value_word = (uint32_t)(lane * P::codes) >> a.code_shift;
+    const uint32_t key_piece_word = (uint32_t)(c * P::codes) >> a.code_shift;
     const bool one_page = a.one_page, bf16 = a.io_bf16;
     const int capacity = a.max_pages * a.page_size;
 
@@ -190,30 +189,40 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
         }
         return r;
     };
-    // A lane's pieces of the rows of both halves, with their (scale, bias) words: piece
-    // 4 i + c of row n. Rows in the cache are below 2^32, byte offsets are not: 64-bit products.
+    // A lane's pieces of the rows of both halves: pieces i * 64 + lane of 16 rows, whole
+    // rows one after the other. Rows in the cache are below 2^32, byte offsets are
+    // not: 64-bit products.
     struct Tile {
         Raw r[2][kPieces];
-        uint32_t sb[2][kPieces];
+        uint32_t sb[2][kPieces];  // of V: the pieces' (scale, bias) words; of K: of pieces 4 i + c of row n
     };
-    auto load = [&](Tile &t, const void *cache, const uint32_t *sb, const Rows &rows) {
+    auto row_at = [&](const void *cache, uint32_t row) {
+        return static_cast<const char *>(cache) + (uint64_t)(row == kNoRow ? 0u : row) * kRowBytes;
+    };
+    auto words_at = [&](const uint32_t *sb, uint32_t row) { return sb + (uint64_t)(row == kNoRow ? 0u : row) * row_words; };
+    auto load = [&](Tile &t, const void *cache, const uint32_t *sb, const Rows &rows, bool keys) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const char *from;
-            const uint32_t *words;
+            // read once: past the caches
             if (one_page) {
-                from = static_cast<const char *>(cache) + (uint64_t)rows.first[u] * kRowBytes + (n * kRowBytes + c * kPieceBytes);
-                words = sb + (uint64_t)rows.first[u] * row_words + (n * row_words + lane_word);
-            } else {
-                const uint32_t row = rows.mine[u] == kNoRow ? 0u : rows.mine[u];
-                from = static_cast<const char *>(cache) + (uint64_t)row * kRowBytes + c * kPieceBytes;
-                words = sb + (uint64_t)row * row_words + lane_word;
-            }
+                const Raw *from = reinterpret_cast<const Raw *>(row_at(cache, rows.first[u]));
+                const uint32_t *words = words_at(sb, rows.first[u]);
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                // read once: past the caches
-                t.r[u][i] = __builtin_nontemporal_load(reinterpret_cast<const Raw *>(from + i * 4 * kPieceBytes));
-                t.sb[u][i] = words[(uint32_t)(i * 4 * P::codes) >> a.code_shift];
+                for (int i = 0; i < kPieces; ++i) {
+                    t.r[u][i] = __builtin_nontemporal_load(from + (i * kWave + lane));
+                    t.sb[u][i] = keys ? words[n * row_words + key_piece_word + ((uint32_t)(i * 4 * P::codes) >> a.code_shift)]
+                                      : words[value_word + ((uint32_t)(i * kWave * P::codes) >> a.code_shift)];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int piece = i * kWave + lane;
+                    const uint32_t row = __shfl(rows.mine[u], piece / U);
+                    t.r[u][i] = __builtin_nontemporal_load(reinterpret_cast<const Raw *>(row_at(cache, row)) + piece % U);
+                    t.sb[u][i] =
+                        keys ? words_at(sb, rows.mine[u])[key_piece_word + ((uint32_t)(i * 4 * P::codes) >> a.code_shift)]
+                             : words_at(sb, row)[(uint32_t)(piece % U * P::codes) >> a.code_shift];
+                }
             }
         }
     };
@@ -223,25 +232,33 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
         else
             return eight_numbers(r[e], sb);
     };
-    // Tokens of which a lane has a group whose last level may pass fp16's largest
-    // number, or whose scale or bias is infinite or NaN already.
+    // Tokens with a group whose last level may pass fp16's largest number, or whose
+    // scale or bias is infinite or NaN already.
     auto not_finite = [&](const Tile &t, uint32_t present) -> uint32_t {
-        uint32_t tokens = 0;
+        uint32_t worst = 0;
+        auto last_level = [&](int u, int i) -> uint32_t {
+            const half2_t sb = __builtin_bit_cast(half2_t, t.sb[u][i] & 0x7FFF7FFFu);
+            return __builtin_bit_cast(uint16_t, (_Float16)__builtin_fmaf16(sb.x, (_Float16)(float)((1 << BITS) - 1), sb.y));
+        };
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            uint32_t worst = 0;
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const half2_t sb = __builtin_bit_cast(half2_t, t.sb[u][i] & 0x7FFF7FFFu);
-                const _Float16 last = __builtin_fmaf16(sb.x, (_Float16)(float)((1 << BITS) - 1), sb.y);
-                const uint32_t bits = __builtin_bit_cast(uint16_t, last);
-                worst = bits > worst ? bits : worst;
+                const uint32_t last = last_level(u, i);
+                worst = last > worst ? last : worst;
             }
-            const uint64_t odd = __ballot(worst >= E::exponent);
-            const uint32_t two = (uint32_t)odd | (uint32_t)(odd >> 32);
-            tokens |= ((two | two >> 16) & 0xFFFFu) << 16 * u;
-        }
-        return tokens & present;
+        if (__builtin_expect(!__any(worst >= E::exponent), 1))
+            return 0;
+        uint32_t tokens = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                tokens |= last_level(u, i) >= E::exponent ? 1u << (16 * u + (i * kWave + lane) / U) : 0u;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2)
+            tokens |= __shfl_xor(tokens, d);
+        return __builtin_amdgcn_readfirstlane(tokens) & present;
     };
 
     // Queries of column tile t in the order of the pieces: step i * kEights + e has
@@ -257,8 +274,7 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
 #pragma unroll
     for (int t = 0; t < NT; ++t)
         score_scale[t] = a.scale_log2;
-    half8_t qf[kQueriesInLds ? 1 : NT][KS];
-    if constexpr (kQueriesInLds) {
+    {
         constexpr int kShare = (NT * KS + kWaves - 1) / kWaves;
         u32x4 v[kShare];
 #pragma unroll
@@ -288,35 +304,6 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
                 bf16 ? lifted(v[i], lift_of(query_top[one / KS * 16 + n])) : __builtin_bit_cast(half8_t, v[i]);
         }
         lds_barrier();
-    } else {
-        u32x4 v[NT][KS];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int q = 0; q < KS; ++q)
-                v[t][q] = *query_at(t, q);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            int lift = 0;
-            if (bf16) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int q = 0; q < KS; ++q) {
-                    const uint32_t x = top_of(v[t][q]);
-                    top = x > top ? x : top;
-                }
-#pragma unroll
-                for (int d = 16; d < kWave; d *= 2) {
-                    const uint32_t x = __shfl_xor(top, d);
-                    top = x > top ? x : top;
-                }
-                lift = lift_of(top);
-                score_scale[t] = __builtin_amdgcn_ldexpf(a.scale_log2, -lift);
-            }
-#pragma unroll
-            for (int q = 0; q < KS; ++q)
-                qf[t][q] = bf16 ? lifted(v[t][q], lift) : __builtin_bit_cast(half8_t, v[t][q]);
-        }
     }
     int pos[NT];  // positions of this lane's columns (-1: no such column)
 #pragma unroll
@@ -338,38 +325,52 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
     {
         Tile kt, vt;
         Rows rows = rows_of(look_up(begin), begin);
-        load(kt, a.k_cache, a.k_sb, rows);
+        load(kt, a.k_cache, a.k_sb, rows, true);
         Pages pages = look_up(begin + 1);
-        load(vt, a.v_cache, a.v_sb, rows);
+        load(vt, a.v_cache, a.v_sb, rows, false);
         for (int x = begin; x < end; ++x) {
             const int j0 = first_of(x);  // the wave's first token
             const uint32_t present = ((uint32_t)__ballot(rows.mine[0] != kNoRow) & 0xFFFFu) |
                                      (uint32_t)__ballot(rows.mine[1] != kNoRow) << 16;
 
+            // K's codes change lanes; the next ones are on their way at once.
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    *reinterpret_cast<Raw *>(my_lds + (16 * u + (i * kWave + lane) / U) * kCodePitch +
+                                             (i * kWave + lane) % U * kPieceBytes) = kt.r[u][i];
+            uint32_t k_words[2][kPieces];
+#pragma unroll
+            for (int i = 0; i < 2 * kPieces; ++i)
+                k_words[i / kPieces][i % kPieces] = kt.sb[i / kPieces][i % kPieces];
+            rows = rows_of(pages, x + 1);
+            load(kt, a.k_cache, a.k_sb, rows, true);
+            pages = look_up(x + 2);
+            wave_lds_sync();
             float4_t s[2][NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
                 s[0][t] = s[1][t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = 0; q < KS; ++q) {
-                half8_t kf[2];
+            for (int i = 0; i < kPieces; ++i) {
+                Raw k[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                    kf[u] = __builtin_bit_cast(half8_t, numbers(kt.r[u][q / kEights], kt.sb[u][q / kEights], q % kEights));
+                    k[u] = *reinterpret_cast<const Raw *>(my_lds + (16 * u + n) * kCodePitch + (4 * i + c) * kPieceBytes);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    half8_t qv;
-                    if constexpr (kQueriesInLds)
-                        qv = q_lds[(t * KS + q) * kWave + lane];
-                    else
-                        qv = qf[t][q];
-                    s[0][t] = E::mfma(kf[0], qv, s[0][t]);
-                    s[1][t] = E::mfma(kf[1], qv, s[1][t]);
+                for (int e = 0; e < kEights; ++e) {
+                    const half8_t k0 = __builtin_bit_cast(half8_t, numbers(k[0], k_words[0][i], e));
+                    const half8_t k1 = __builtin_bit_cast(half8_t, numbers(k[1], k_words[1][i], e));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const half8_t qv = q_lds[(t * KS + i * kEights + e) * kWave + lane];
+                        s[0][t] = E::mfma(k0, qv, s[0][t]);
+                        s[1][t] = E::mfma(k1, qv, s[1][t]);
+                    }
                 }
             }
-            rows = rows_of(pages, x + 1);
-            load(kt, a.k_cache, a.k_sb, rows);
-            pages = look_up(x + 2);
+            wave_lds_sync();
 
             // Tiles that not every row sees whole: scores that a row does not see
             // are -infinity.
@@ -424,34 +425,29 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
             const uint32_t bad = not_finite(vt, present);
             auto through_lds = [&](uint32_t tokens, auto use) {
 #pragma unroll
-                for (int part = 0; part < kParts; ++part) {
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int piece = i * kWave + lane, token = 16 * u + piece / U;
+                        const uint32_t sb = tokens >> token & 1u ? vt.sb[u][i] : 0u;
 #pragma unroll
-                        for (int k = 0; k < kPartPieces; ++k) {
-                            const int i = part * kPartPieces + k;
-                            const uint32_t sb = tokens >> (16 * u + n) & 1u ? vt.sb[u][i] : 0u;
-#pragma unroll
-                            for (int e = 0; e < kEights; ++e)
-                                *reinterpret_cast<u32x4 *>(my_lds + (16 * u + n) * kPitch +
-                                                           ((4 * k + c) * P::codes + 8 * e) * 2) =
-                                    numbers(vt.r[u][i], sb, e);
-                        }
-                    wave_lds_sync();
-#pragma unroll
-                    for (int d = 0; d < kPartTiles; ++d) {
-                        typedef __attribute__((address_space(3))) short4_t lds4;
-                        const char *from = my_lds + tr_offset + d * 32;
-                        const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)from);
-                        const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(from + 16 * kPitch));
-                        const half8_t vf =
-                            __builtin_bit_cast(half8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            use(vf, t, acc[t][part * kPartTiles + d]);
+                        for (int e = 0; e < kEights; ++e)
+                            *reinterpret_cast<u32x4 *>(my_lds + token * kPitch + (piece % U * P::codes + 8 * e) * 2) =
+                                numbers(vt.r[u][i], sb, e);
                     }
-                    wave_lds_sync();
+                wave_lds_sync();
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    typedef __attribute__((address_space(3))) short4_t lds4;
+                    const char *from = my_lds + tr_offset + d * 32;
+                    const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)from);
+                    const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(from + 16 * kPitch));
+                    const half8_t vf = __builtin_bit_cast(half8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        use(vf, t, acc[t][d]);
                 }
+                wave_lds_sync();
             };
             through_lds(present & ~bad, [&](half8_t vf, int t, float4_t &o) { o = E::mfma(vf, weights[t], o); });
             // The others one by one, into the columns that see them alone.
@@ -478,7 +474,7 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
                     o = sees(t) ? with : o;
                 });
             }
-            load(vt, a.v_cache, a.v_sb, rows);
+            load(vt, a.v_cache, a.v_sb, rows, false);
         }
     }
     // What follows knows its lanes anew: nothing of it stays in registers over the loop.
