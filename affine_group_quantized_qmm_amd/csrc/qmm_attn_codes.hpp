@@ -12,16 +12,18 @@
 //                    of LDS as codes, from where a lane has the 16 bytes of the token whose
 //                    operand it holds (loading them so would ask the address unit for
 //                    64 places instead of 16: 64 sequences, 8 heads of 128, 8 bits
-//                    178 us). The order of the contraction is that of the pieces, for
-//                    the queries too.
+//                    178 us). The order of the contraction is that of the pieces, and
+//                    within eight 4-bit codes that of their pairs, for the queries too.
 //   p = 2^(s - m)    a lane holds tokens 4c .. 4c + 3 of both 16-token halves of one
 //                    column, which are the 8 places of the second product's operand
 //   O^T += V^T P^T   as they lie: P stays in registers. V^T comes out of the wave's part of
 //                    LDS with transposing reads.
 //
-// P is one fp16 number, scaled by 2^15: its rounding, 2^-11 at most, is below the codes'
-// own (half a step is 2^-9 of a group's range and more), and the largest weight, which is
-// a power of two when it raises the maximum, is exact. Over 16-bit rows it is two.
+// P is one fp16 number: its rounding, 2^-11 at most, is below the codes' own (half a step
+// is 2^-9 of a group's range and more), and the weight that raises the maximum is a
+// power of two and exact. Over 16-bit rows it is two. It is scaled by 2^8, so that a
+// maximum holds until a score passes it by 2^7: with less room nearly every turn of a short
+// run rescaled all accumulators (131071 tokens of heads of 256, 4 bits, with the paired order below: 83 us instead of 78).
 // bf16 queries become fp16, brought to a common size by a power of two for each column.
 #pragma once
 
@@ -42,6 +44,12 @@ struct Piece {
 };
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+
+// The weights' scale: p is at most 2^15, and steps of 2^-24 are 2^-32 of the weight
+// of a score at the maximum.
+struct CodeElem : Elem<_Float16> {
+    static constexpr float kLift = 8.0f, kUnlift = 0x1p-8f, kRaise = 7.0f;
+};
 
 // Four outputs in their type.
 __device__ __forceinline__ u32x2 rounded4(float4_t v, bool bf16)
@@ -82,7 +90,7 @@ __device__ __forceinline__ half8_t lifted(u32x4 v, int lift)
 template <int BITS, int D, int NT>
 __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, NT)) void attn_codes_kernel(const AttnArgs a)
 {
-    using E = Elem<_Float16>;
+    using E = CodeElem;
     using P = Piece<BITS, D>;
     using Raw = typename P::raw;
     constexpr int kWaves = kCodeWaves, kTile = kCodesTile;
@@ -230,7 +238,7 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
         if constexpr (BITS == 8)
             return eight_numbers(r[2 * e], r[2 * e + 1], sb);
         else
-            return eight_numbers(r[e], sb);
+            return eight_paired_numbers(r[e], sb);
     };
     // Tokens with a group whose last level may pass fp16's largest number, or whose
     // scale or bias is infinite or NaN already.
@@ -300,6 +308,8 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
 #pragma unroll
         for (int i = 0; i < kShare; ++i) {
             const int one = i * kWaves + wave < NT * KS ? i * kWaves + wave : wave;
+            if constexpr (BITS == 4)
+                v[i] = paired(v[i]);
             q_lds[one * kWave + lane] =
                 bf16 ? lifted(v[i], lift_of(query_top[one / KS * 16 + n])) : __builtin_bit_cast(half8_t, v[i]);
         }
@@ -528,10 +538,17 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
                 meet[(wave * 4 + k) * kWave + lane] = acc[t][d0 + k] * mine;
             lds_barrier();
             if (d0 + wave < DT) {
-                float4_t o = meet[wave * kWave + lane];
+                float4_t o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int v = 1; v < kWaves; ++v)
-                    o += meet[(v * 4 + wave) * kWave + lane];
+                for (int v = 0; v < kWaves; ++v) {
+                    const float4_t *from = meet + (v * 4 + wave) * kWave;
+                    if constexpr (BITS == 4) {  // out of the paired order
+                        const float4_t x = from[lane_end & ~16], y = from[lane_end | 16];
+                        o += c_end % 2 == 0 ? float4_t{x.x, x.z, y.x, y.z} : float4_t{x.y, x.w, y.y, y.w};
+                    } else {
+                        o += from[lane_end];
+                    }
+                }
                 const int d = (d0 + wave) * 16 + 4 * c_end;
                 if (live && all)
                     *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at_row * D + d) = rounded4(o * inv, bf16);
@@ -570,9 +587,9 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
         return e;
     const dim3 joins((uint32_t)p.items, p.join_columns);
     if (a.io_bf16)
-        attn_join_kernel<Elem<_Float16>, __bf16, D><<<joins, p.join_threads, 0, stream>>>(a, 16 * NT);
+        attn_join_kernel<CodeElem, __bf16, D><<<joins, p.join_threads, 0, stream>>>(a, 16 * NT);
     else
-        attn_join_kernel<Elem<_Float16>, _Float16, D><<<joins, p.join_threads, 0, stream>>>(a, 16 * NT);
+        attn_join_kernel<CodeElem, _Float16, D><<<joins, p.join_threads, 0, stream>>>(a, 16 * NT);
     return hipGetLastError();
 }
 
