@@ -13,7 +13,7 @@
 // and puts the candidates into a list, which is ranked element against element. A row's slices
 // meet in a second kernel, which finds the n best of theirs in the same way.
 //
-// Sums are fp32 within a thread (up to 32 terms) and 64 bits
+// Sums are fp32 within a wave (up to 32 terms a thread) and 64 bits
 // from there on, in a fixed order; the list's order is any, but ranks do not
 // depend on it. Bound by memory, or for a few rows by two launches.
 #include "qmm_device.hpp"
@@ -97,11 +97,11 @@ __device__ __forceinline__ float unordered(uint32_t o)
 {
     return __builtin_bit_cast(float, o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
-// The fp32 number below x; for -infinity NaN, which nothing is "not above".
+// The fp32 number below x (of -infinity, itself).
 __device__ __forceinline__ float below(float x)
 {
     if (x == -kInf)
-        return __builtin_nanf("");
+        return x;
     if (x == 0.f)
         return -0x1p-149f;
     const int b = __builtin_bit_cast(int, x);
@@ -114,40 +114,45 @@ struct Part {
     uint32_t ahead; // logits in front of the token
     double s, t;    // S and T about m; for m = +infinity the number of such logits, and 0
 };
-__device__ __forceinline__ void join(Part &a, const Part &b)
+// A part's sums about a larger maximum.
+__device__ __forceinline__ void raise(Part &p, float m)
 {
-    a.ahead += b.ahead;
-    if (b.m == -kInf)
-        return;
-    if (a.m == b.m) {
-        a.s += b.s;
-        a.t += b.t;
+    if (p.m == m || p.m == -kInf) {
+        p.s = p.m == m ? p.s : 0;
+        p.t = p.m == m ? p.t : 0;
         return;
     }
-    const bool up = b.m > a.m;
-    const double from_s = up ? a.s : b.s, from_t = up ? a.t : b.t;
-    const double d = up ? (double)a.m - b.m : (double)b.m - a.m;  // below 0, maybe -infinity
-    const double f = exp(d);
-    const double s = f > 0 ? from_s * f : 0, t = f > 0 ? f * (from_t + from_s * d) : 0;
-    a.s = (up ? b.s : a.s) + s;
-    a.t = (up ? b.t : a.t) + t;
-    a.m = up ? b.m : a.m;
+    const double d = (double)p.m - m, f = exp(d);  // below 0, maybe -infinity
+    p.t = f > 0 ? f * (p.t + p.s * d) : 0;
+    p.s = f > 0 ? p.s * f : 0;
 }
 
 constexpr int kGroups = 2 * kWave;
 
-// A bound that at least n of the 128 values (two a lane) reach, and nearly the
-// largest such: its upper 20 bits are the n-th largest value's.
-__device__ __forceinline__ uint32_t nth_largest(uint32_t v, uint32_t w, int n)
+// Largest and smallest of the wave's lanes.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-    uint32_t t = 0;
-#pragma unroll 4
-    for (int bit = 31; bit >= 12; --bit) {
-        const uint32_t with = t | 1u << bit;
-        if (__popcll(__ballot(v >= with)) + __popcll(__ballot(w >= with)) >= n)
-            t = with;
+    auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    v = up(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
+    v = up(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
+    v = up(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));  // row_ror:4
+    v = up(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));  // row_ror:8
+    return up(up(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+              up(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+
+// A bound that at least n (up to 128) of the 128 values (two a lane) reach, within
+// 2^-10 of their range of the largest such. All of them lie in [lo, hi].
+__device__ __forceinline__ uint32_t nth_largest(uint32_t v, uint32_t w, uint32_t lo, uint32_t hi, int n)
+{
+#pragma unroll 2
+    for (int i = 0; i < 10; ++i) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        const bool enough = __popcll(__ballot(v >= mid)) + __popcll(__ballot(w >= mid)) >= n;
+        lo = enough ? mid : lo;
+        hi = enough ? hi : mid - 1;  // (lo <= hi: for mid == lo all reach it)
     }
-    return t;
+    return lo;
 }
 
 struct Best {
@@ -160,18 +165,17 @@ __device__ __forceinline__ bool in_front(Best a, Best b) { return a.x > b.x || (
 template <int THREADS>
 struct Lds {
     uint32_t group_max[kGroups];
+    uint32_t bound;
     int listed;
     Best list[kList];
     Best wave_best[THREADS / kWave];
-    Part part[THREADS / kWave];
-    double s[THREADS / kWave], t[THREADS / kWave];
+    float s[THREADS / kWave], t[THREADS / kWave];
     uint32_t ahead[THREADS / kWave];
 };
 
 // The first n elements in order of those that threads hold, each handed to
 // put(rank, best) once; ranks without an element are handed over with index -1.
-// collect(add) calls add(has, best) by whole waves for at least every element that may
-// be among them; element(i, best) gives the i-th of `count` of a thread, false for
+// collect(add) calls add(has, best) for at least every element that may be among them; element(i, best) gives the i-th of `count` of a thread, false for
 // none. Called by all threads, after a barrier that follows the clearing of
 // lds.listed.
 template <int THREADS, typename Collect, typename Element, typename Put>
@@ -179,16 +183,11 @@ __device__ __forceinline__ void first_n(Lds<THREADS> &lds, int n, int count, Col
 {
     const int tid = threadIdx.x;
     collect([&](bool has, Best e) {
-        has = has && e.x > -kInf;
-        const uint64_t who = __ballot(has);
-        if (who == 0)
-            return;
-        int at = 0;
-        if (tid % kWave == 0)
-            at = atomicAdd(&lds.listed, __popcll(who));
-        at = __builtin_amdgcn_readfirstlane(at) + __popcll(who & ((1ull << tid % kWave) - 1));
-        if (has && at < kList)
-            lds.list[at] = e;
+        if (has && e.x > -kInf) {
+            const int at = atomicAdd(&lds.listed, 1);
+            if (at < kList)
+                lds.list[at] = e;
+        }
     });
     __syncthreads();
     const int listed = lds.listed;
@@ -256,14 +255,6 @@ __device__ __forceinline__ void finish_top(const LogprobArgs &a, int row, const 
                                                           : (float)((double)e.x - p.m - log_s);
 }
 
-__device__ __forceinline__ double wave_sum64(double v)
-{
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2)
-        v += __shfl_xor(v, d);
-    return v;
-}
-
 template <typename T, int THREADS, int LOADS>
 __global__ __launch_bounds__(THREADS) void logprobs_kernel(const LogprobArgs a)
 {
@@ -283,6 +274,7 @@ __global__ __launch_bounds__(THREADS) void logprobs_kernel(const LogprobArgs a)
     if (tid == 0)
         lds.listed = 0;
 
+    float x[LOADS][kVec];
     u32x4 v[LOADS];
     auto first_of = [&](int c) { return ((slice * LOADS + c) * THREADS + tid) * kVec - skew; };
 #pragma unroll
@@ -300,117 +292,113 @@ __global__ __launch_bounds__(THREADS) void logprobs_kernel(const LogprobArgs a)
         }
     }
     const float x_token = known ? __builtin_fmaxf(L::one(logits, token), -kInf) : -kInf;
-    auto values = [&](int c, float (&x)[kVec]) {
-        L::unpack(v[c], x);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            x[i] = __builtin_fmaxf(x[i], -kInf);
-    };
     float top[LOADS], most = -kInf;
 #pragma unroll
     for (int c = 0; c < LOADS; ++c) {
-        float x[kVec];
-        values(c, x);
-        top[c] = x[0];
+        L::unpack(v[c], x[c]);
+        top[c] = -kInf;  // (a maximum is never NaN)
 #pragma unroll
-        for (int i = 1; i < kVec; ++i)
-            top[c] = __builtin_fmaxf(top[c], x[i]);
+        for (int i = 0; i < kVec; ++i)
+            top[c] = __builtin_fmaxf(top[c], x[c][i]);
         most = __builtin_fmaxf(most, top[c]);
     }
     __syncthreads();
     atomicMax(&lds.group_max[tid % kGroups], ordered(most));
     __syncthreads();
     const uint32_t group0 = lds.group_max[lane], group1 = lds.group_max[lane + kWave];
-    uint32_t largest = group0 > group1 ? group0 : group1;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t o = __shfl_xor(largest, d);
-        largest = o > largest ? o : largest;
-    }
+    const uint32_t largest = wave_max(group0 > group1 ? group0 : group1);
     const float m = unordered(largest);
+    if (wave == 0 && a.n > 0) {
+        const uint32_t least = ~wave_max(~(group0 < group1 ? group0 : group1));
+        lds.bound = nth_largest(group0, group1, least, largest, a.n);
+    }
 
     // The second walk.
-    const float thr_behind = known ? x_token : kInf, thr_front = known ? below(x_token) : kInf;
     float s = 0.f, t = 0.f;
-    uint32_t ahead = 0, ahead_lane = 0;
     if (m == kInf) {
 #pragma unroll
-        for (int c = 0; c < LOADS; ++c) {
-            float x[kVec];
-            values(c, x);
+        for (int c = 0; c < LOADS; ++c)
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
-                s += x[i] == kInf ? 1.f : 0.f;
-        }
+                s += x[c][i] == kInf ? 1.f : 0.f;
     } else {
 #pragma unroll
-        for (int c = 0; c < LOADS; ++c) {
-            float x[kVec];
-            values(c, x);
+        for (int c = 0; c < LOADS; ++c)
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                // (a difference of infinities is NaN, and as far below as any)
-                const float d = __builtin_fmaxf(x[i] - m, -1e4f);
+                // (NaN, from NaN or from a difference of infinities, is as far below as any)
+                const float d = __builtin_fmaxf(x[c][i] - m, -1e4f);
                 const float e = __builtin_amdgcn_exp2f(d * 1.44269504088896340736f);
                 s += e;
                 t = __builtin_fmaf(e, d, t);
             }
-        }
     }
+    // Logits in front of the token: larger ones, and up to its own 16 bytes those above
+    // the number below it. NaN is above nothing.
+    const float thr_behind = known ? x_token : kInf, thr_front = known ? below(x_token) : kInf;
+    uint32_t ahead = 0, ahead_lane = 0;
 #pragma unroll
     for (int c = 0; c < LOADS; ++c) {
         const int j = first_of(c);
         const float thr = j + kVec <= token ? thr_front : thr_behind;
-        float x[kVec];
-        values(c, x);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            ahead += __popcll(__ballot(!(x[i] <= thr)));
-        if (j < token && j + kVec > token) {  // equal ones in front within the token's own 16 bytes
+        if (__any(top[c] > thr)) {  // (seldom for a likely token)
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
-                ahead_lane += j + i >= 0 && j + i < token && x[i] == x_token;
+                ahead += __popcll(__ballot(x[c][i] > thr));
         }
-        // places outside the row, which count as -infinity, are in front of nothing
-        if (thr != thr && j < 0)
-            ahead_lane += j;
-    }
-    const double ws = wave_sum64((double)s), wt = wave_sum64((double)t);
+        if (j < token && j + kVec > token) {
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2)
-        ahead_lane += __shfl_xor(ahead_lane, d);
+            for (int i = 0; i < kVec; ++i)
+                ahead_lane += j + i >= 0 && j + i < token && x[c][i] == x_token && x_token > -kInf;
+        }
+        // In front of a token of -infinity (or NaN) are all of lower index.
+        if (__builtin_expect(known && x_token == -kInf, 0)) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                ahead_lane += j + i >= 0 && j + i < token && !(x[c][i] > -kInf);
+        }
+    }
+    s = wave_sum(s);
+    t = wave_sum(t);
+    if (__any(ahead_lane != 0)) {
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2)
+            ahead_lane += __shfl_xor(ahead_lane, d);
+    }
     if (lane == 0) {
-        lds.s[wave] = ws;
-        lds.t[wave] = wt;
+        lds.s[wave] = s;
+        lds.t[wave] = t;
         lds.ahead[wave] = ahead + ahead_lane;
     }
     __syncthreads();
-    Part p{m, 0, 0, 0};
+    auto whole = [&] {
+        Part p{m, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        p.s += lds.s[w];
-        p.t += lds.t[w];
-        p.ahead += lds.ahead[w];
-    }
-    if (tid == 0) {
-        if (a.slices == 1)
+        for (int w = 0; w < kWaves; ++w) {
+            p.s += (double)lds.s[w];
+            p.t += (double)lds.t[w];
+            p.ahead += lds.ahead[w];
+        }
+        return p;
+    };
+    if (wave == 0) {
+        const Part p = whole();
+        if (tid == 0 && a.slices == 1)
             finish(a, row, p, token, x_token);
-        else
+        else if (tid == 0)
             a.parts[blockIdx.x] = LogprobPart{m, p.ahead, p.s, p.t};
     }
     if (a.n == 0)
         return;
-    const float least = unordered(nth_largest(group0, group1, a.n));  // (NaN below -infinity: everything reaches it)
+    const float least = unordered(lds.bound);  // (NaN below -infinity: everything reaches it)
     auto collect = [&](auto add) {
 #pragma unroll
         for (int c = 0; c < LOADS; ++c) {
             if (!__any(!(top[c] < least)))
                 continue;
-            float x[kVec];
-            values(c, x);
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
-                add(!(x[i] < least), Best{x[i], first_of(c) + i});
+                add(!(x[c][i] < least), Best{x[c][i], first_of(c) + i});
         }
     };
     auto element = [&](int i, Best &e) {  // rarely used: any order of registers will do
@@ -420,11 +408,9 @@ __global__ __launch_bounds__(THREADS) void logprobs_kernel(const LogprobArgs a)
         for (int c = 0; c < LOADS; ++c) {
             if (i / kVec != c)
                 continue;
-            float x[kVec];
-            values(c, x);
 #pragma unroll
             for (int k = 0; k < kVec; ++k)
-                y = i % kVec == k ? x[k] : y;
+                y = i % kVec == k ? x[c][k] : y;
             j = first_of(c) + i % kVec;
         }
         e = Best{y, j};
@@ -432,7 +418,7 @@ __global__ __launch_bounds__(THREADS) void logprobs_kernel(const LogprobArgs a)
     };
     first_n<THREADS>(lds, a.n, LOADS * kVec, collect, element, [&](int rank, Best e) {
         if (a.slices == 1)
-            finish_top(a, row, p, rank, e);
+            finish_top(a, row, whole(), rank, e);
         else
             a.best[(int64_t)blockIdx.x * a.n + rank] = float2{e.x, __builtin_bit_cast(float, e.index)};
     });
@@ -448,24 +434,30 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
         lds.group_max[tid] = 0;
     if (tid == 0)
         lds.listed = 0;
-    // The slices' sums: a few for each thread, then lanes and waves pairwise, which
-    // gives every thread the same bits.
-    Part p{-kInf, 0, 0, 0};
+    // The slices' sums about the row's maximum, lanes pairwise: the same bits in every
+    // thread.
     const LogprobPart *parts = a.parts + (int64_t)row * a.slices;
-    for (int i = tid; i < a.slices; i += kJoinThreads) {
-        const LogprobPart q = parts[i];
-        join(p, Part{q.m, q.ahead, q.s, q.t});
-    }
-#pragma unroll 1
+    float m = -kInf;
+    for (int i = lane; i < a.slices; i += kWave)
+        m = __builtin_fmaxf(m, parts[i].m);
+#pragma unroll
     for (int d = 1; d < kWave; d *= 2)
-        join(p, Part{__shfl_xor(p.m, d), (uint32_t)__shfl_xor((int)p.ahead, d), __shfl_xor(p.s, d), __shfl_xor(p.t, d)});
-    if (lane == 0)
-        lds.part[tid / kWave] = p;
-    __syncthreads();
-    p = lds.part[0];
-#pragma unroll 1
-    for (int w = 1; w < kJoinThreads / kWave; ++w)
-        join(p, lds.part[w]);
+        m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    Part p{m, 0, 0, 0};
+    for (int i = lane; i < a.slices; i += kWave) {  // (every wave sums them all)
+        const LogprobPart q = parts[i];
+        Part about{q.m, q.ahead, q.s, q.t};
+        raise(about, m);
+        p.s += about.s;
+        p.t += about.t;
+        p.ahead += q.ahead;
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        p.s += __shfl_xor(p.s, d);
+        p.t += __shfl_xor(p.t, d);
+        p.ahead += __shfl_xor(p.ahead, d);
+    }
     if (tid == 0) {
         const int token = a.tokens[row];
         float x = -kInf;
@@ -497,7 +489,9 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
     __syncthreads();
     atomicMax(&lds.group_max[tid % kGroups], ordered(most));
     __syncthreads();
-    const float least = unordered(nth_largest(lds.group_max[lane], lds.group_max[lane + kWave], a.n));
+    const uint32_t group0 = lds.group_max[lane], group1 = lds.group_max[lane + kWave];
+    const float least = unordered(nth_largest(group0, group1, ~wave_max(~(group0 < group1 ? group0 : group1)),
+                                              wave_max(group0 > group1 ? group0 : group1), a.n));
     auto collect = [&](auto add) {
         for (int i = 0; i < count; ++i) {
             Best e;
@@ -510,7 +504,7 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
 
 // Elements of a slice: 512 threads with 32 each where the rows' slices fill the
 // GPU, else 256 with 8.
-constexpr int kLong = 512 * 32, kShort = 256 * 8;
+constexpr int kLongThreads = 256, kLongEach = 16, kLong = kLongThreads * kLongEach, kShort = 256 * 8;
 int slice_of(int M, int V)
 {
     const int64_t slices = (int64_t)M * ((V + kLong - 1) / kLong);
@@ -521,7 +515,7 @@ hipError_t launch(const LogprobArgs &a, int slice, int type, hipStream_t stream)
 {
     const uint32_t blocks = (uint32_t)a.M * a.slices;
     if (slice == kLong)
-        logprobs_kernel<T, 512, 32 / Logits<T>::kVec><<<blocks, 512, 0, stream>>>(a);
+        logprobs_kernel<T, kLongThreads, kLongEach / Logits<T>::kVec><<<blocks, kLongThreads, 0, stream>>>(a);
     else
         logprobs_kernel<T, 256, 8 / Logits<T>::kVec><<<blocks, 256, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
@@ -537,7 +531,7 @@ LogprobPlan logprobs_plan(int M, int V, int n, int skew)
 {
     LogprobPlan p;
     p.slices = (V + skew + slice_of(M, V) - 1) / slice_of(M, V);
-    p.threads = (int64_t)M * p.slices * (slice_of(M, V) == kLong ? 512 : 256);
+    p.threads = (int64_t)M * p.slices * (slice_of(M, V) == kLong ? kLongThreads : 256);
     const size_t parts = p.slices == 1 ? 0 : (size_t)M * p.slices;
     p.workspace_bytes = parts * (sizeof(LogprobPart) + sizeof(float2) * n);
     return p;
