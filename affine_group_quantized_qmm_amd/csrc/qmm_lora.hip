@@ -10,15 +10,21 @@
 //
 // Down: 16 ranks by 16 rows in 16x16x32 instructions, the four waves of a workgroup
 // taking a quarter of its part of K each and adding up in LDS; parts of K in workgroups
-// of their own (a sum in order in the second kernel) until the GPU is full.
-// Up: 16 columns of the projection by 16 rows. h enters as the sum of 16-bit numbers
-// (two in fp16, three in bf16, whose products are exact), so that no rounding to the inputs'
-// type is added between the two products; in fp16 a row's h is multiplied by a power of two
-// that brings its largest value to 2^14 first. Ranks below 32 leave room in an
-// instruction's 32 places of contraction, which the further numbers take.
+// of their own (a sum in order in the second kernel) until the GPU is full. Operands hold
+// another row in every lane, which the address unit takes lane by lane; so whole rows
+// of 512 bytes are loaded, and change lanes in LDS.
+// Up: 16 rows by 16 columns of the projection, 16 lanes along a row of y. h enters as the
+// sum of 16-bit numbers (two in fp16, three in bf16, whose products are exact), so that
+// no rounding to the inputs' type is added between the two products; in fp16 a row's h is
+// multiplied by a power of two that brings its largest value to 2^14 first. Ranks below
+// 32 leave room in an instruction's 32 places of contraction, which the further numbers
+// take.
 //
-// Bound by the adapters' bytes for many requests, by y (read and written) for
-// prompts, and by two launches for few rows.
+// Bound by y (read and written) for prompts: 2048 rows, K 5120, N 17408, rank 32, fp16:
+// down 12.2 us, up 57.7 us, which is 5.0 TB/s, a large copy's rate. A batch of 64 rows
+// with 48 adapters of rank 16 beside three projections, bf16, moves 40 MB in 9.0 us and
+// 11.0 us: two short kernels, each ids -> leaders -> loads -> products -> store. One row
+// (5.0 us and 5.6 us) is the latency of the same two chains.
 #include "qmm_device.hpp"
 #include "qmm_kernels.hpp"
 #include "qmm_step.hpp"
@@ -30,6 +36,7 @@ constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr int kRows = 16;         // rows of a block
 constexpr int kBatch = 8;         // steps of 32 along K whose operands are in flight together
 constexpr int kPass = kWaves * kBatch * 32;  // of K, by a workgroup at a time
+constexpr int kPitch = kBatch * 64 + 16;     // bytes of a row in LDS: 16 shift consecutive rows by 4 banks
 constexpr int kTiles = 4;         // 16-column tiles of a wave in the second product
 
 template <typename T>
@@ -53,6 +60,13 @@ struct Elem<__bf16> {
     }
 };
 
+// The exponent of the power of two that brings a row's largest value (as bits) to
+// 2^14 .. 2^15.
+__device__ __forceinline__ int lift_of(uint32_t top)
+{
+    return top == 0 ? 0 : 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
+}
+
 // The adapter of row `block * 16 + lane % 16` (-1: none), and the rows of the block
 // that are the first of theirs, as bits.
 struct Block {
@@ -75,22 +89,35 @@ __device__ __forceinline__ Block block_of(const LoraArgs &a, int block)
 // h of one adapter: up to 32 ranks, one part of K.
 // ---------------------------------------------------------------------------
 template <typename T, int RT>  // tiles of 16 ranks
-__global__ __launch_bounds__(kThreads) void lora_down_kernel(const LoraArgs a)
+__global__ __launch_bounds__(kThreads, RT == 1 ? 4 : 3) void lora_down_kernel(const LoraArgs a)
 {
     using E = Elem<T>;
     using x8 = typename E::x8;
+    __shared__ __align__(16) char rows_lds[kWaves][kRows * kPitch];
     __shared__ float4_t sums[kWaves][RT][kWave];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, n = lane % 16, c = lane / 16;
     const int z = blockIdx.x % a.parts, group = blockIdx.x / a.parts % a.rank_groups, p = blockIdx.x / a.parts / a.rank_groups;
     const int block = blockIdx.y;
     const Block rows = block_of(a, block);
     const int row = block * kRows + n;
-    const T *x = static_cast<const T *>(a.x) + (int64_t)(row < a.M ? row : a.M - 1) * a.K + 8 * c;
     // This workgroup's steps of 32, then this wave's.
     const int steps = a.K / 32, per = (steps + a.parts - 1) / a.parts;
     const int begin = z * per < steps ? z * per : steps, end = begin + per < steps ? begin + per : steps;
     const int mine = (end - begin + kWaves - 1) / kWaves;
     const int from = begin + wave * mine < end ? begin + wave * mine : end, to = from + mine < end ? from + mine : end;
+    // Lane of a load: 8 values of row 2 i + lane / 32.
+    const int half = lane / 32, k8 = lane % 32 * 8;
+    char *const mine_lds = rows_lds[wave];
+    auto change_lanes = [&](const u32x4 (&v)[kRows / 2], x8 (&out)[kBatch]) {
+#pragma unroll
+        for (int i = 0; i < kRows / 2; ++i)
+            *reinterpret_cast<u32x4 *>(mine_lds + (2 * i + half) * kPitch + k8 * 2) = v[i];
+        wave_lds_sync();
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s)
+            out[s] = *reinterpret_cast<const x8 *>(mine_lds + n * kPitch + s * 64 + c * 16);
+        wave_lds_sync();
+    };
 
     uint32_t leaders = rows.leaders;
     for (int skip = blockIdx.z; leaders != 0; skip = gridDim.z - 1) {
@@ -102,37 +129,39 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(const LoraArgs a)
             break;
         const int id = __builtin_amdgcn_readlane(rows.id, __builtin_ctz(leaders));
         leaders &= leaders - 1;
-        const T *w[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const int j = (group * RT + t) * 16 + n;
-            w[t] = static_cast<const T *>(a.proj[p].a) + ((int64_t)id * a.r + (j < a.r ? j : a.r - 1)) * a.K + 8 * c;
-        }
+        const uint32_t own = (uint32_t)__ballot(rows.id == id) & 0xFFFFu;  // rows of this adapter (none past M)
+        const T *x = static_cast<const T *>(a.x) + ((int64_t)block * kRows + half) * a.K + k8;
+        const T *w = static_cast<const T *>(a.proj[p].a) + ((int64_t)id * a.r + group * RT * 16 + half) * a.K + k8;
         float4_t acc[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t)
             acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-        int s = from;
-        for (; s + kBatch <= to; s += kBatch) {
-            x8 xv[kBatch], wv[RT][kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                xv[i] = *reinterpret_cast<const x8 *>(x + (s + i) * 32);
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-                    wv[t][i] = *reinterpret_cast<const x8 *>(w[t] + (s + i) * 32);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-                    acc[t] = E::mfma(wv[t][i], xv[i], acc[t]);
-        }
-        for (; s < to; ++s) {
-            const x8 xv = *reinterpret_cast<const x8 *>(x + s * 32);
+        for (int s = from; s < to; s += kBatch) {
+            const bool in = s * 32 + k8 < to * 32;  // zeros past the wave's part, past the rank and for other rows
+            u32x4 xv[kRows / 2], wv[RT][kRows / 2];
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-                acc[t] = E::mfma(*reinterpret_cast<const x8 *>(w[t] + s * 32), xv, acc[t]);
+#pragma unroll
+                for (int i = 0; i < kRows / 2; ++i) {
+                    wv[t][i] = u32x4{0, 0, 0, 0};
+                    if (in && (group * RT + t) * 16 + 2 * i + half < a.r)
+                        wv[t][i] = *reinterpret_cast<const u32x4 *>(w + (int64_t)(t * 16 + 2 * i) * a.K + s * 32);
+                }
+#pragma unroll
+            for (int i = 0; i < kRows / 2; ++i) {
+                xv[i] = u32x4{0, 0, 0, 0};
+                if (in && (own >> (2 * i + half) & 1u))
+                    xv[i] = *reinterpret_cast<const u32x4 *>(x + (int64_t)(2 * i) * a.K + s * 32);
+            }
+            x8 xf[kBatch], wf[kBatch];
+            change_lanes(xv, xf);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                change_lanes(wv[t], wf);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    acc[t] = E::mfma(wf[i], xf[i], acc[t]);
+            }
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t)
@@ -163,8 +192,8 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
     constexpr int kSteps = RP < 32 ? 1 : RP / 32;         // operands of B
     constexpr int kSlots = RP < 32 ? 32 / RP : 1;         // parts of h in one instruction
     constexpr int kMul = (E::kParts + kSlots - 1) / kSlots;  // instructions for one operand of B
-    constexpr int kPitch = RP + 4;
-    __shared__ __align__(16) float h_lds[kRows * kPitch];
+    constexpr int kHPitch = RP + 4;
+    __shared__ __align__(16) float h_lds[kRows * kHPitch];
     __shared__ uint32_t row_top[kRows];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, n = lane % 16, c = lane / 16;
     int p = 0;
@@ -172,13 +201,12 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
     for (int q = 1; q < kMaxProj; ++q)
         p = q < a.count && (int)blockIdx.x >= a.proj[q].first ? q : p;
     const LoraProj proj = a.proj[p];
-    const int block = blockIdx.y, row = block * kRows + n;
+    const int block = blockIdx.y;
     const int N = proj.N, n0 = (((int)blockIdx.x - proj.first) * kWaves + wave) * kTiles * 16;
     const Block rows = block_of(a, block);
     // Places of a lane's 8 values of the contraction.
     const int j0 = RP >= 32 ? 8 * c : RP == 16 ? 8 * (c % 2) : 0;
     const int slot = RP >= 32 ? 0 : RP == 16 ? c / 2 : c;
-    const bool even = N % 4 == 0;
 
     uint32_t leaders = rows.leaders;
     for (int skip = blockIdx.z; leaders != 0; skip = gridDim.z - 1) {
@@ -190,7 +218,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
             break;
         const int id = __builtin_amdgcn_readlane(rows.id, __builtin_ctz(leaders));
         leaders &= leaders - 1;
-        const bool own = rows.id == id;  // of this lane's row
+        const uint32_t own = (uint32_t)__ballot(rows.id == id) & 0xFFFFu;  // rows of this adapter
         // B and y are on their way while h is put together.
         const T *b = static_cast<const T *>(proj.b) + (int64_t)id * N * a.r;
         x8 bv[kTiles][kSteps];
@@ -206,22 +234,17 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
                     bv[t][s] = x8{};
             }
         }
-        float *y = proj.y + (int64_t)(own ? row : 0) * N;
+        // y of rows 4c .. 4c+3, 16 columns a lane apart.
+        float *y = proj.y + (int64_t)(block * kRows + 4 * c) * N + n0 + n;
         float4_t yv[kTiles];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            const int col = n0 + t * 16 + 4 * c;
-            yv[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-            if (even) {
-                if (own && col < N)
-                    yv[t] = *reinterpret_cast<const float4_t *>(y + col);
-            } else {
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (own && col + i < N)
-                        yv[t][i] = y[col + i];
+            for (int i = 0; i < 4; ++i) {
+                yv[t][i] = 0.f;
+                if ((own >> (4 * c + i) & 1u) && n0 + t * 16 + n < N)
+                    yv[t][i] = y[(int64_t)i * N + t * 16];
             }
-        }
 
         if (threadIdx.x < kRows)
             row_top[threadIdx.x] = 0;
@@ -239,7 +262,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
                     h += *reinterpret_cast<const float4_t *>(from + (int64_t)z * a.M * a.r);
                 h *= scale;
             }
-            *reinterpret_cast<float4_t *>(h_lds + m * kPitch + 4 * q) = h;
+            *reinterpret_cast<float4_t *>(h_lds + m * kHPitch + 4 * q) = h;
             float top = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -250,8 +273,11 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
         }
         __syncthreads();
         // h of row n as operands: values j0 + 32 s .., part slot + kSlots q.
-        const uint32_t top = row_top[n];
-        const int lift = top == 0 ? 0 : 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
+        int lifts[4];  // of rows 4c .. 4c+3
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            lifts[i] = lift_of(row_top[4 * c + i]);
+        const int lift = lift_of(row_top[n]);
         x8 hv[kSteps][kMul];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -259,7 +285,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                v[k] = j < a.r ? __builtin_amdgcn_ldexpf(h_lds[n * kPitch + j + k], lift) : 0.f;
+                v[k] = j < a.r ? __builtin_amdgcn_ldexpf(h_lds[n * kHPitch + j + k], lift) : 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 float rest = v[k];
@@ -288,20 +314,11 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(const LoraArgs a)
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                 for (int q = 0; q < kMul; ++q)
-                    acc = E::mfma(bv[t][s], hv[s][q], acc);
-            const int col = n0 + t * 16 + 4 * c;
+                    acc = E::mfma(hv[s][q], bv[t][s], acc);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                yv[t][i] += __builtin_amdgcn_ldexpf(acc[i], -lift);
-            if (even) {
-                if (own && col < N)
-                    *reinterpret_cast<float4_t *>(y + col) = yv[t];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (own && col + i < N)
-                        y[col + i] = yv[t][i];
-            }
+                if ((own >> (4 * c + i) & 1u) && n0 + t * 16 + n < N)
+                    y[(int64_t)i * N + t * 16] = yv[t][i] + __builtin_amdgcn_ldexpf(acc[i], -lifts[i]);
         }
         __syncthreads();  // h_lds is free again
     }
@@ -341,17 +358,20 @@ LoraPlan lora_plan(int count, const int *N, int M, int K, int r, int adapters)
     p.blocks = (M + kRows - 1) / kRows;
     p.rank_groups = r <= 16 ? 1 : (r + 31) / 32;
     const int most = kRows < adapters ? kRows : adapters, slots = M < most ? M : most;
-    // Workgroups: parts of K first, down to one pass of a workgroup (1024 values);
-    // then the adapters of a block. Four on a CU are wanted.
+    // Workgroups: parts of K first, down to one pass of a workgroup (kPass values);
+    // then the adapters of a block. Four on a CU are wanted, which is what fits: a
+    // block's adapters taken by more workgroups wait for their rows' ids in vain (64
+    // rows with 48 adapters, up: 13.7 us with 16 workgroups for a block's adapters, 11.0
+    // with 8, 14.7 with 4; 2048 rows with 4 adapters, down: 13.5 us with 4, 12.2 with 2).
     const int64_t want = 4 * (int64_t)device_cu_count(), base = (int64_t)p.blocks * p.rank_groups * count;
     p.parts = clamped((want + base - 1) / base, 1, (K + kPass - 1) / kPass);
     p.down_x = p.parts * p.rank_groups * count;
-    p.down_z = clamped((want * 4 + base * p.parts - 1) / (base * p.parts), 1, slots);
+    p.down_z = clamped((want + base * p.parts - 1) / (base * p.parts), 1, slots);
     p.up_x = 0;
     for (int i = 0; i < count; ++i)
         p.up_x += (N[i] + kWaves * kTiles * 16 - 1) / (kWaves * kTiles * 16);
     const int64_t ups = (int64_t)p.up_x * p.blocks;
-    p.up_z = clamped((want * 4 + ups - 1) / ups, 1, slots);
+    p.up_z = clamped((want + ups - 1) / ups, 1, slots);
     p.workspace_bytes = sizeof(float) * count * p.parts * (size_t)M * r;
     return p;
 }
