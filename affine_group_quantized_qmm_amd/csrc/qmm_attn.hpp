@@ -331,10 +331,11 @@ constexpr int most_col_tiles(int D, bool codes = false)
 // Waves of a SIMD over codes: what the accumulators and a tile's codes leave room for.
 constexpr int codes_waves_per_simd(int bits, int D, int NT)
 {
-    return D == 64    ? (NT <= 2 ? 3 : 2)
-           : D == 96  ? (NT <= 2 ? 2 : 1)
-           : D == 128 ? (NT == 1 && bits == 4 ? 3 : NT <= 2 ? 2 : 1)
-                      : (NT == 1 && (D == 192 || bits == 4) ? 2 : 1);
+    return D == 64    ? (NT <= 2 ? 4 : NT == 3 && bits == 4 ? 3 : 2)
+           : D == 96  ? (NT == 1 || (NT == 2 && bits == 4) ? 3 : NT == 4 && bits == 8 ? 1 : 2)
+           : D == 128 ? (NT == 1 || (NT == 2 && bits == 4) ? 3 : 2)
+           : D == 192 ? (NT == 1 && bits == 4 ? 3 : 2)
+                      : (NT == 2 && bits == 8 ? 1 : 2);
 }
 
 // Join of the pieces of an item that several runs share:

@@ -40,6 +40,17 @@ template <int BITS, int D>
 struct Piece {
     static constexpr int codes = D % 128 == 0 && BITS == 4 ? 32 : D % 64 == 0 ? 16 : 8;
     static constexpr int in_row = D / codes, count = in_row / 4;  // of a lane: pieces of 16 rows
+    // V passes LDS in parts of the head, which leaves room for a second workgroup.
+    static constexpr int parts = D == 256 ? 2 : D == 192 ? 3 : 1;
+    static constexpr int in_part = in_row / parts, part_count = count / parts;
+    static_assert(in_part * parts == in_row && part_count * parts == count, "");
+    // Piece i of a lane among those of 16 rows of V: part after part, whole rows of a part in order.
+    static constexpr __device__ int at(int i, int lane) { return i % part_count * kWave + lane; }
+    static constexpr __device__ int token(int i, int lane) { return at(i, lane) / in_part; }
+    static constexpr __device__ int in_row_at(int i, int lane) { return i / part_count * in_part + at(i, lane) % in_part; }
+    // Pieces from that of i = 0 to it: whole groups.
+    static constexpr __device__ int beyond(int i) { return token(i, 0) * in_row + in_row_at(i, 0); }
+    static_assert(parts == 1 || kWave % in_part == 0, "");
     typedef uint32_t raw __attribute__((ext_vector_type(codes * BITS / 32)));
 };
 
@@ -103,8 +114,8 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
     // A wave's part of LDS holds 32 rows: first K's as codes, then V's as numbers. 32
     // bytes past the data shift consecutive rows of V by 8 banks, so that the 8 rows
     // that a transposing read touches at a time do not collide; 16 do it for K's.
-    constexpr int kPitch = 2 * D + 32, kCodePitch = kRowBytes + 16;
-    constexpr int kWaveLds = 32 * kPitch;
+    constexpr int kPitch = 2 * D / P::parts + 32, kCodePitch = kRowBytes + 16;
+    constexpr int kWaveLds = 32 * (kPitch > kCodePitch ? kPitch : kCodePitch);
     // At the end of an item: 4 tiles of 16 columns of each wave.
     constexpr int kJoinBytes = kWaves * 4 * kWave * 16;
     __shared__ __align__(16) char lds[kWaves * kWaveLds > kJoinBytes ? kWaves * kWaveLds : kJoinBytes];
@@ -112,8 +123,8 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
     __shared__ uint32_t query_top[kColumns];
     __shared__ float wave_max[kWaves][kColumns], wave_sums[kWaves][kColumns];
 
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const int c = lane / 16, n = lane % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    int lane = threadIdx.x % kWave, c = lane / 16, n = lane % 16;
     const int G = a.G;
     Start at_first;
     if (!find_start<kTile, kColumns>(a, at_first))
@@ -124,12 +135,7 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
     const int w = at_first.w, here = at_first.here;
     const Runs runs = at_first.runs;
     char *const my_lds = lds + wave * kWaveLds;
-    const int tr_offset = (4 * c + n / 4) * kPitch + n % 4 * 8;
     const uint32_t row_words = (D % 96 == 0 ? 3u : 1u) << a.words_shift;  // groups of a row
-    // Words of a lane's first piece among those of 16 rows, as values and as keys; the
-    // further ones are whole groups of 4 or 64 pieces behind it.
-    const uint32_t value_word = (uint32_t)(lane * P::codes) >> a.code_shift;
-    const uint32_t key_piece_word = (uint32_t)(c * P::codes) >> a.code_shift;
     const bool one_page = a.one_page, bf16 = a.io_bf16;
     const int capacity = a.max_pages * a.page_size;
 
@@ -209,6 +215,10 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
     };
     auto words_at = [&](const uint32_t *sb, uint32_t row) { return sb + (uint64_t)(row == kNoRow ? 0u : row) * row_words; };
     auto load = [&](Tile &t, const void *cache, const uint32_t *sb, const Rows &rows, bool keys) {
+        // Words of a lane's first piece among those of 16 rows, as values and as keys;
+        // the further ones are whole groups behind it.
+        const uint32_t value_word = (uint32_t)((P::token(0, lane) * U + P::in_row_at(0, lane)) * P::codes) >> a.code_shift;
+        const uint32_t key_piece_word = (uint32_t)(c * P::codes) >> a.code_shift;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             // read once: past the caches
@@ -217,19 +227,23 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
                 const uint32_t *words = words_at(sb, rows.first[u]);
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
-                    t.r[u][i] = __builtin_nontemporal_load(from + (i * kWave + lane));
-                    t.sb[u][i] = keys ? words[n * row_words + key_piece_word + ((uint32_t)(i * 4 * P::codes) >> a.code_shift)]
-                                      : words[value_word + ((uint32_t)(i * kWave * P::codes) >> a.code_shift)];
+                    if (keys) {
+                        t.r[u][i] = __builtin_nontemporal_load(from + (i * kWave + lane));
+                        t.sb[u][i] = words[n * row_words + key_piece_word + ((uint32_t)(i * 4 * P::codes) >> a.code_shift)];
+                    } else {
+                        t.r[u][i] = __builtin_nontemporal_load(from + (P::token(0, lane) * U + P::in_row_at(0, lane)) + P::beyond(i));
+                        t.sb[u][i] = words[value_word + ((uint32_t)(P::beyond(i) * P::codes) >> a.code_shift)];
+                    }
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
-                    const int piece = i * kWave + lane;
-                    const uint32_t row = __shfl(rows.mine[u], piece / U);
-                    t.r[u][i] = __builtin_nontemporal_load(reinterpret_cast<const Raw *>(row_at(cache, row)) + piece % U);
+                    const int place = keys ? (i * kWave + lane) % U : P::in_row_at(i, lane);
+                    const uint32_t row = __shfl(rows.mine[u], keys ? (i * kWave + lane) / U : P::token(i, lane));
+                    t.r[u][i] = __builtin_nontemporal_load(reinterpret_cast<const Raw *>(row_at(cache, row)) + place);
                     t.sb[u][i] =
                         keys ? words_at(sb, rows.mine[u])[key_piece_word + ((uint32_t)(i * 4 * P::codes) >> a.code_shift)]
-                             : words_at(sb, row)[(uint32_t)(piece % U * P::codes) >> a.code_shift];
+                             : words_at(sb, row)[(uint32_t)(place * P::codes) >> a.code_shift];
                 }
             }
         }
@@ -262,7 +276,7 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-                tokens |= last_level(u, i) >= E::exponent ? 1u << (16 * u + (i * kWave + lane) / U) : 0u;
+                tokens |= last_level(u, i) >= E::exponent ? 1u << (16 * u + P::token(i, lane)) : 0u;
 #pragma unroll
         for (int d = 1; d < kWave; d *= 2)
             tokens |= __shfl_xor(tokens, d);
@@ -339,6 +353,11 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
         Pages pages = look_up(begin + 1);
         load(vt, a.v_cache, a.v_sb, rows, false);
         for (int x = begin; x < end; ++x) {
+            // What follows from the lane is found anew in each turn: kept over the loop it
+            // costs the registers of a second workgroup on the CU.
+            pin_register(lane);
+            c = lane / 16;
+            n = lane % 16;
             const int j0 = first_of(x);  // the wave's first token
             const uint32_t present = ((uint32_t)__ballot(rows.mine[0] != kNoRow) & 0xFFFFu) |
                                      (uint32_t)__ballot(rows.mine[1] != kNoRow) << 16;
@@ -434,30 +453,35 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
             // column: a scale and bias of 0 make zeros of them.
             const uint32_t bad = not_finite(vt, present);
             auto through_lds = [&](uint32_t tokens, auto use) {
+                const int tr_offset = (4 * c + n / 4) * kPitch + n % 4 * 8;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int part = 0; part < P::parts; ++part) {
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int piece = i * kWave + lane, token = 16 * u + piece / U;
-                        const uint32_t sb = tokens >> token & 1u ? vt.sb[u][i] : 0u;
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int e = 0; e < kEights; ++e)
-                            *reinterpret_cast<u32x4 *>(my_lds + token * kPitch + (piece % U * P::codes + 8 * e) * 2) =
-                                numbers(vt.r[u][i], sb, e);
+                        for (int i = part * P::part_count; i < (part + 1) * P::part_count; ++i) {
+                            const int token = 16 * u + P::token(i, lane);
+                            const uint32_t sb = tokens >> token & 1u ? vt.sb[u][i] : 0u;
+#pragma unroll
+                            for (int e = 0; e < kEights; ++e)
+                                *reinterpret_cast<u32x4 *>(my_lds + token * kPitch +
+                                                           (P::at(i, lane) % P::in_part * P::codes + 8 * e) * 2) =
+                                    numbers(vt.r[u][i], sb, e);
+                        }
+                    wave_lds_sync();
+#pragma unroll
+                    for (int d = 0; d < DT / P::parts; ++d) {
+                        typedef __attribute__((address_space(3))) short4_t lds4;
+                        const char *from = my_lds + tr_offset + d * 32;
+                        const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)from);
+                        const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(from + 16 * kPitch));
+                        const half8_t vf = __builtin_bit_cast(half8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            use(vf, t, acc[t][part * (DT / P::parts) + d]);
                     }
-                wave_lds_sync();
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    typedef __attribute__((address_space(3))) short4_t lds4;
-                    const char *from = my_lds + tr_offset + d * 32;
-                    const short4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)from);
-                    const short4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(from + 16 * kPitch));
-                    const half8_t vf = __builtin_bit_cast(half8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        use(vf, t, acc[t][d]);
+                    wave_lds_sync();
                 }
-                wave_lds_sync();
             };
             through_lds(present & ~bad, [&](half8_t vf, int t, float4_t &o) { o = E::mfma(vf, weights[t], o); });
             // The others one by one, into the columns that see them alone.
@@ -488,9 +512,8 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
         }
     }
     // What follows knows its lanes anew: nothing of it stays in registers over the loop.
-    int lane_end = lane;
-    pin_register(lane_end);
-    const int n_end = lane_end % 16, c_end = lane_end / 16;
+    pin_register(lane);
+    const int lane_end = lane, n_end = lane_end % 16, c_end = lane_end / 16;
     // The waves' sums meet.
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
