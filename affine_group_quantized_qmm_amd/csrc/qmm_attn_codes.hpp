@@ -3,7 +3,7 @@
 // (qmm_attn.hip), on the fp16 numbers that the codes stand for.
 //
 // Forming the numbers is what the kernel spends most of its instructions on (three
-// for two 8-bit codes, 17 for eight 4-bit ones), with a half or a
+// for two 8-bit codes, 11 for eight 4-bit ones), with a half or a
 // quarter of the bytes to wait for. So the rest is kept short: a wave is alone with
 // 32 tokens at a time from their loads to its own output, and workgroups meet only
 // at the end of an item.
@@ -567,7 +567,7 @@ __global__ __launch_bounds__(kCodeWaves * kWave, codes_waves_per_simd(BITS, D, N
                     const float4_t *from = meet + (v * 4 + wave) * kWave;
                     if constexpr (BITS == 4) {  // out of the paired order
                         const float4_t x = from[lane_end & ~16], y = from[lane_end | 16];
-                        o += c_end % 2 == 0 ? float4_t{x.x, x.z, y.x, y.z} : float4_t{x.y, x.w, y.y, y.w};
+                        o += c_end % 2 == 0 ? float4_t{x.x, y.x, x.y, y.y} : float4_t{x.z, y.z, x.w, y.w};
                     } else {
                         o += from[lane_end];
                     }

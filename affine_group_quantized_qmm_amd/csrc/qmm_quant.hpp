@@ -52,25 +52,27 @@ __device__ __forceinline__ u32x4 eight_numbers(uint32_t codes, uint32_t sb)
     return eight_numbers(__builtin_amdgcn_perm(odd, even, 0x05010400u), __builtin_amdgcn_perm(odd, even, 0x07030602u), sb);
 }
 
-// Eight 4-bit codes in the order 0, 4, 1, 5, 2, 6, 3, 7, which takes 15 operations
-// instead of 17: codes i and i + 4 lie 16 bits apart.
+// Eight 4-bit codes in the order 0, 2, 4, 6, 1, 3, 5, 7, which takes 11 operations
+// instead of 17: a byte of 0 .. 15 is that many steps of 2^-9 as an e4m3 number (the
+// subnormal ones and the first binade), so a conversion forms two codes.
 __device__ __forceinline__ u32x4 eight_paired_numbers(uint32_t codes, uint32_t sb)
 {
     const half2_t both = __builtin_bit_cast(half2_t, sb);
-    const half2_t s = {both.x, both.x}, b = {both.y, both.y}, magic = {(_Float16)1024.0f, (_Float16)1024.0f};
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const half2_t c = __builtin_bit_cast(half2_t, and_or(codes >> 4 * i, 0x000F000Fu, 0x64006400u)) - magic;
-        r[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, s, b));
-    }
-    return r;
+    const half2_t s = {both.x, both.x}, b = {both.y, both.y};
+    const uint32_t even = codes & 0x0F0F0F0Fu, odd = codes >> 4 & 0x0F0F0F0Fu;
+    auto two = [&](auto c) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, c), s, b));
+    };
+    return u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(even, 0x1p9f, false)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(even, 0x1p9f, true)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(odd, 0x1p9f, false)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(odd, 0x1p9f, true))};
 }
 // Eight 16-bit values in that order.
 __device__ __forceinline__ u32x4 paired(u32x4 v)
 {
-    return u32x4{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                 __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+    return u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
+                 __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)};
 }
 
 }  // namespace qmm
