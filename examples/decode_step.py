@@ -3,8 +3,11 @@
 Every projection is a quantized product (``qmm_forward_fused``, ``qmm_forward``);
 between them ``qmm_qk_norm_rope`` norms and rotates queries and keys into the
 paged cache, ``qmm_paged_attention`` attends over it, and after the last
-projection ``qmm_sample`` chooses the tokens. Residuals, the layers' norms and
-the gate are plain torch. Weights are random: the point is how the calls fit
+projection ``qmm_sample`` chooses the tokens. With ``cache_bits`` the cache holds
+8- or 4-bit codes (``qmm_qk_norm_rope_quant``, ``qmm_paged_attention_quant``); with
+``adapters`` each row may have a low-rank adapter of its own beside the
+projections (``qmm_lora``); ``qmm_logprobs`` reports what the chosen tokens'
+probabilities were. Residuals, the layers' norms and the gate are plain torch. Weights are random: the point is how the calls fit
 together, for a prompt, for one token at a time, for several drafted rows of a
 verify step, and captured into a graph.
 
@@ -41,6 +44,10 @@ class Config:
     window: int = 0        # of the odd layers; 0: all tokens
     sinks: int = 0
     eps: float = 1e-6
+    cache_bits: int = 0    # 8 or 4: a cache of codes; 0: of fp16 rows
+    cache_group: int = 32
+    adapters: int = 0      # beside q, k, v and the output projection
+    rank: int = 8
 
 
 def random_weight(N: int, K: int, gen, dev):
@@ -67,27 +74,50 @@ class Decoder:
                             k_norm=(1 + 0.1 * torch.randn(D, generator=g)).to(self.dev)) for _ in range(c.layers)]
         self.head = w(c.vocab, c.hidden)
         self.inv_freq = (1e4 ** (-torch.arange(0, c.rotary, 2).double() / c.rotary)).float().to(self.dev)
-        shape = (c.pages, c.kv_heads, c.page_size, D)
-        self.caches = [(torch.zeros(shape, dtype=torch.float16, device=self.dev),
-                        torch.zeros(shape, dtype=torch.float16, device=self.dev)) for _ in range(c.layers)]
+        shape = (c.pages, c.kv_heads, c.page_size)
+
+        def cache():  # rows, or (codes, scales and biases)
+            if c.cache_bits == 0:
+                return (torch.zeros(*shape, D, dtype=torch.float16, device=self.dev),)
+            return tuple(torch.zeros(*shape, n, dtype=torch.int32, device=self.dev)
+                         for n in (D * c.cache_bits // 32, D // c.cache_group))
+        self.caches = [cache() + cache() for _ in range(c.layers)]
+        # (A [n, r, K], B [n, N, r]) of each projection that has adapters, and their scales.
+        sizes = dict(q=(c.heads * D, c.hidden), k=(c.kv_heads * D, c.hidden), v=(c.kv_heads * D, c.hidden),
+                     o=(c.hidden, c.heads * D))
+        self.adapters = [{m: ((torch.randn(c.adapters, c.rank, K, generator=g) * K ** -0.5).half().to(self.dev),
+                              (torch.randn(c.adapters, N, c.rank, generator=g) * 0.2).half().to(self.dev))
+                          for m, (N, K) in sizes.items()} for _ in range(c.layers if c.adapters else 0)]
+        self.adapter_scales = torch.rand(c.adapters, generator=g).to(self.dev) + 0.5
 
     def norm(self, x):
         return (x * torch.rsqrt((x * x).mean(-1, keepdim=True) + self.c.eps)).half()
+
+    def adapted(self, layer, names, x, ys, batch):
+        """The products `ys` of `x` with what each row's adapter adds to them."""
+        if self.c.adapters == 0 or batch.adapters is None:
+            return ys
+        return qmm.qmm_lora(x, [self.adapters[layer][m] for m in names], batch.adapters, ys, scales=self.adapter_scales)
 
     def logits(self, tokens, batch) -> torch.Tensor:
         """fp32 [T, vocab] of the rows `tokens` [T], whose keys and values join the cache."""
         c, T, D = self.c, tokens.shape[0], self.c.head_dim
         x = self.embedding[tokens.long()]
         for i, p in enumerate(self.layers):
-            q, k, v = qmm.qmm_forward_fused(self.norm(x), [p["q"], p["k"], p["v"]], BITS, G)
-            kc, vc = self.caches[i]
-            q = qmm.qmm_qk_norm_rope(q.view(T, c.heads, D), k.view(T, c.kv_heads, D), v.view(T, c.kv_heads, D),
-                                     p["q_norm"], p["k_norm"], batch.positions, self.inv_freq, batch.slots, kc, vc,
-                                     eps=c.eps)
-            a = qmm.qmm_paged_attention(q, kc, vc, batch.block_table, batch.context_lens, batch.row_starts,
-                                        batch.max_rows, batch.max_context, window=c.window if i % 2 else 0,
-                                        sinks=c.sinks)
-            x = x + qmm.qmm_forward(a.view(T, c.heads * D), *p["o"], BITS, G)
+            h = self.norm(x)
+            q, k, v = self.adapted(i, "qkv", h, qmm.qmm_forward_fused(h, [p["q"], p["k"], p["v"]], BITS, G), batch)
+            new = (q.view(T, c.heads, D), k.view(T, c.kv_heads, D), v.view(T, c.kv_heads, D), p["q_norm"], p["k_norm"],
+                   batch.positions, self.inv_freq, batch.slots, *self.caches[i])
+            where = (batch.block_table, batch.context_lens, batch.row_starts, batch.max_rows, batch.max_context)
+            seen = dict(window=c.window if i % 2 else 0, sinks=c.sinks)
+            if c.cache_bits:
+                q = qmm.qmm_qk_norm_rope_quant(*new, c.cache_bits, c.cache_group, eps=c.eps)
+                a = qmm.qmm_paged_attention_quant(q, *self.caches[i], c.cache_bits, c.cache_group, *where, **seen)
+            else:
+                q = qmm.qmm_qk_norm_rope(*new, eps=c.eps)
+                a = qmm.qmm_paged_attention(q, *self.caches[i], *where, **seen)
+            a = a.view(T, c.heads * D)
+            x = x + self.adapted(i, "o", a, [qmm.qmm_forward(a, *p["o"], BITS, G)], batch)[0]
             gate, up = qmm.qmm_forward_fused(self.norm(x), [p["gate"], p["up"]], BITS, G)
             x = x + qmm.qmm_forward((torch.nn.functional.silu(gate) * up).half(), *p["down"], BITS, G)
         return qmm.qmm_forward(self.norm(x), *self.head, BITS, G)
@@ -96,12 +126,18 @@ class Decoder:
         """One token for each row."""
         return qmm.qmm_sample(self.logits(tokens, batch), u, **sampling)
 
+    def step_with_logprobs(self, tokens, batch, u, top_n: int = 0, **sampling):
+        """One token for each row, and qmm_logprobs of it."""
+        logits = self.logits(tokens, batch)
+        chosen = qmm.qmm_sample(logits, u, **sampling)
+        return chosen, qmm.qmm_logprobs(logits, chosen, top_n)
+
 
 class Batch:
     """Where the rows of a call stand: `rows[b]` new rows after `past[b]` tokens
-    of each sequence b, whose pages are `pages[b]`."""
+    of each sequence b, whose pages are `pages[b]`, under `adapters[b]` (-1: none)."""
 
-    def __init__(self, c: Config, pages, past, rows, device="cuda"):
+    def __init__(self, c: Config, pages, past, rows, device="cuda", adapters=None):
         def ints(v):
             return torch.tensor(v, dtype=torch.int32, device=device)
         positions, slots, starts = [], [], [0]
@@ -113,6 +149,7 @@ class Batch:
         self.positions, self.slots, self.row_starts = ints(positions), ints(slots), ints(starts)
         self.context_lens = ints([p + n for p, n in zip(past, rows)])
         self.block_table = ints([list(pg) + [-1] * (c.max_pages - len(pg)) for pg in pages])
+        self.adapters = None if adapters is None else ints([i for i, n in zip(adapters, rows) for _ in range(n)])
         self.max_rows = max(rows)
         self.max_context = c.max_pages * c.page_size
 
@@ -139,6 +176,18 @@ def main() -> None:
         for t, n in zip(text, last.tolist()):
             t.append(n)
     print("tokens:", text)
+
+    # The same prompts over a cache of 8-bit codes, the second under an adapter.
+    c = Config(cache_bits=8, adapters=2)
+    model = Decoder(c)
+    rows = [len(p) for p in prompts]
+    u = torch.zeros(sum(rows), device="cuda")
+    chosen, (logprobs, ranks, entropy, top_tokens, _) = model.step_with_logprobs(
+        torch.cat(prompts).cuda(), Batch(c, pages, [0, 0], rows, adapters=[-1, 1]), u, top_n=3,
+        temperature=torch.zeros_like(u))
+    for b, row in enumerate((rows[0] - 1, sum(rows) - 1)):
+        print(f"sequence {b}: token {int(chosen[row])}, log probability {float(logprobs[row]):.2f}, rank "
+              f"{int(ranks[row])}, entropy {float(entropy[row]):.2f}, likeliest {top_tokens[row].tolist()}")
 
 
 if __name__ == "__main__":
