@@ -549,7 +549,7 @@ def qmm_lora(x, adapters, ids, ys, *, scales=None, workspace=None):
     """Adds to each y_p (float32 [M, N_p]) of `ys` scales[i] * B_p[i] (A_p[i] x[m]) of
     row m's adapter i = ids[m] (int32; negative: none), and returns `ys`.
     `adapters` holds a pair (a [n, r, K], b [n, N_p, r]) for each of up to four
-    projections of x [M, K], all float16 or all bfloat16."""
+    projections of x [M, K], all float16 or all bfloat16. No two of `ys` overlap."""
     return _step_result(_binding.lora(x, adapters, ids, ys, scales, workspace, _step_stream(x)), "qmm_lora")
 
 

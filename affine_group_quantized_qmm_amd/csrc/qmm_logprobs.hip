@@ -13,7 +13,7 @@
 // and puts the candidates into a list, which is ranked element against element. A row's slices
 // meet in a second kernel, which finds the n best of theirs in the same way.
 //
-// Sums are fp32 within a wave (up to 32 terms a thread) and 64 bits
+// Sums are fp32 within a wave (up to 16 terms a thread, then in pairs) and 64 bits
 // from there on, in a fixed order; the list's order is any, but ranks do not
 // depend on it. Bound by memory, or for a few rows by two launches.
 #include "qmm_device.hpp"

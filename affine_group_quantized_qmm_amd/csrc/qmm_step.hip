@@ -428,6 +428,10 @@ int qmm_lora(const void *x, int type, int count, const void *const *a, const voi
     }
     if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(scales, 4))
         return QMM_ERR_ALIGN;
+    for (int i = 0; i < count; ++i)  // both would be read, and added to, at once
+        for (int j = 0; j < i; ++j)
+            if (y[i] < y[j] + (int64_t)M * N[j] && y[j] < y[i] + (int64_t)M * N[i])
+                return QMM_ERR_SHAPE;
     l.x = x;
     l.ids = ids;
     l.scales = scales;

@@ -474,7 +474,8 @@ int qmm_paged_attention(const void *q, int64_t q_stride, const void *k_cache, co
  * and the code is the integer nearest to (y - bias) / scale (to 2^-14 of a step),
  * so that a value is stored to within half a step, and the fp16 rounding of the
  * number. A group that holds a NaN stands for NaN in all its places. Arguments as
- * for qmm_qk_norm_rope; slots that are negative or past the cache write nothing.
+ * for qmm_qk_norm_rope; slots that are negative or past the cache write nothing. Two rows
+ * with the same slot may leave the codes of one with the scales of the other there.
  * Errors: those of qmm_qk_norm_rope, QMM_ERR_BITS, QMM_ERR_GROUP, QMM_ERR_HEAD
  * also for D % G != 0.
  */
@@ -572,8 +573,8 @@ int qmm_sample(const void *logits, int64_t row_stride, int type, const float *u,
  * on top of what the products (qmm_forward, qmm_forward_bf16, qmm_forward_fused)
  * left in y. x [M, K] of `type` (fp16 or bf16) is what the products take; a, b, y and
  * N are host arrays of `count` entries, read during the call only: a[p]
- * [adapters, r, K] and b[p] [adapters, N[p], r] of `type`, y[p] fp32 [M, N[p]], no two
- * of them overlapping. ids int32 [M]; a number that is negative or not below `adapters`
+ * [adapters, r, K] and b[p] [adapters, N[p], r] of `type`, y[p] fp32 [M, N[p]] (no two
+ * of them overlapping: QMM_ERR_SHAPE). ids int32 [M]; a number that is negative or not below `adapters`
  * means no adapter: that row of y is neither read nor written. scales fp32 [adapters]
  * may be NULL (1). K a multiple of 32, r a multiple of 8 up to 128 (adapters of a lower
  * rank are filled up with zeros), M up to 1048560. Rows may come in any order; rows of
@@ -611,8 +612,8 @@ int qmm_lora(const void *x, int type, int count, const void *const *a, const voi
  * rank -1; a row without any logit above -infinity has logprobs of -infinity and entropy
  * 0. Tokens of logit -infinity are never among the top_tokens: places without one hold
  * -1 and -infinity.
- * Sums are fp32 over up to 32 terms and 64 bits over those, results are rounded
- * once from there: logprobs are good to about 1e-6 absolutely. Reruns are bitwise
+ * Sums are fp32 over up to 1024 terms (16 in order, 64 such sums in pairs) and 64 bits over
+ * those, results are rounded once from there: logprobs are good to about 1e-6 absolutely. Reruns are bitwise
  * identical. V <= 2^23; M times ((V + 7) / 2048 + 1) * 256 below 2^32 is always taken.
  * workspace: qmm_logprobs_workspace_bytes(M, V, n) bytes (0 for invalid sizes and where
  * none is needed), 16-byte aligned, contents irrelevant.

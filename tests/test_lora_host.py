@@ -31,6 +31,8 @@ def call(count=2, a=(A, A), b=(A, A), y=(A, A), N=(64, 33), arrays=True, **kw):
     (dict(wsb=100), -6),
     (dict(x=A + 8), -7), (dict(a=(A, A + 8)), -7), (dict(b=(A + 2, A)), -7), (dict(y=(A, A + 4)), -7), (dict(ids=A + 2), -7),
     (dict(scales=A + 2), -7), (dict(ws=A + 8), -7),
+    # outputs that overlap: the same one twice, the second's first value in the first's last row
+    (dict(), -2), (dict(y=(A, A + 20 * 64 * 4 - 16)), -2), (dict(y=(A + 20 * 33 * 4 - 16, A)), -2),
 ])
 def test_refuses(kw, code):
     assert call(**kw) == code
