@@ -425,6 +425,7 @@ __global__ __launch_bounds__(THREADS) void logprobs_kernel(const LogprobArgs a)
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kHeld = 6;  // of the slices' best that a thread loads ahead
 
 __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const LogprobArgs a, int type)
 {
@@ -434,18 +435,39 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
         lds.group_max[tid] = 0;
     if (tid == 0)
         lds.listed = 0;
+    // All that is needed is on its way before the first of it is used (one row of
+    // 131072 fp32 with its 20 best: 6.1 us instead of 8.2).
+    const int64_t all = (int64_t)a.slices * a.n;
+    const float2 *best = a.best + row * all;
+    const float2 none{-kInf, __builtin_bit_cast(float, -1)};
+    float2 held[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        held[i] = none;
+        if (i * kJoinThreads + tid < all)
+            held[i] = best[i * kJoinThreads + tid];
+    }
+    const LogprobPart *parts = a.parts + (int64_t)row * a.slices;
+    const LogprobPart first = lane < a.slices ? parts[lane] : LogprobPart{-kInf, 0, 0, 0};
+    const int token = a.tokens[row];
+    float x = -kInf;
+    if (token >= 0 && token < a.V) {
+        const int64_t at = row * a.row_stride + token;
+        x = type == 0 ? Logits<_Float16>::one(a.logits, at) : type == 1 ? Logits<__bf16>::one(a.logits, at)
+                                                                         : Logits<float>::one(a.logits, at);
+        x = __builtin_fmaxf(x, -kInf);
+    }
     // The slices' sums about the row's maximum, lanes pairwise: the same bits in every
     // thread.
-    const LogprobPart *parts = a.parts + (int64_t)row * a.slices;
-    float m = -kInf;
-    for (int i = lane; i < a.slices; i += kWave)
+    float m = first.m;
+    for (int i = lane + kWave; i < a.slices; i += kWave)
         m = __builtin_fmaxf(m, parts[i].m);
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2)
         m = __builtin_fmaxf(m, __shfl_xor(m, d));
     Part p{m, 0, 0, 0};
     for (int i = lane; i < a.slices; i += kWave) {  // (every wave sums them all)
-        const LogprobPart q = parts[i];
+        const LogprobPart q = i == lane ? first : parts[i];
         Part about{q.m, q.ahead, q.s, q.t};
         raise(about, m);
         p.s += about.s;
@@ -458,52 +480,41 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
         p.t += __shfl_xor(p.t, d);
         p.ahead += __shfl_xor(p.ahead, d);
     }
-    if (tid == 0) {
-        const int token = a.tokens[row];
-        float x = -kInf;
-        if (token >= 0 && token < a.V) {
-            const int64_t at = row * a.row_stride + token;
-            x = type == 0 ? Logits<_Float16>::one(a.logits, at) : type == 1 ? Logits<__bf16>::one(a.logits, at)
-                                                                             : Logits<float>::one(a.logits, at);
-            x = __builtin_fmaxf(x, -kInf);
-        }
+    if (tid == 0)
         finish(a, row, p, token, x);
-    }
     if (a.n == 0)
         return;
-    const int64_t all = (int64_t)a.slices * a.n;
-    const float2 *best = a.best + row * all;
+    auto best_of = [&](float2 v) { return Best{v.x, __builtin_bit_cast(int, v.y)}; };
     auto element = [&](int i, Best &e) {
         const int64_t at = (int64_t)i * kJoinThreads + tid;
-        const float2 v = at < all ? best[at] : float2{-kInf, 0.f};
-        e = Best{v.x, __builtin_bit_cast(int, v.y)};
+        e = best_of(at < all ? best[at] : none);
         return at < all;
     };
     const int count = (int)((all + kJoinThreads - 1) / kJoinThreads);
+    auto each = [&](auto use) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            use(best_of(held[i]));
+        for (int i = kHeld; i < count; ++i) {
+            Best e;
+            element(i, e);
+            use(e);
+        }
+    };
     float most = -kInf;
-    for (int i = 0; i < count; ++i) {
-        Best e;
-        if (element(i, e))
-            most = __builtin_fmaxf(most, e.x);
-    }
+    each([&](Best e) { most = __builtin_fmaxf(most, e.x); });
     __syncthreads();
     atomicMax(&lds.group_max[tid % kGroups], ordered(most));
     __syncthreads();
     const uint32_t group0 = lds.group_max[lane], group1 = lds.group_max[lane + kWave];
     const float least = unordered(nth_largest(group0, group1, ~wave_max(~(group0 < group1 ? group0 : group1)),
                                               wave_max(group0 > group1 ? group0 : group1), a.n));
-    auto collect = [&](auto add) {
-        for (int i = 0; i < count; ++i) {
-            Best e;
-            const bool has = element(i, e);
-            add(has && !(e.x < least), e);
-        }
-    };
+    auto collect = [&](auto add) { each([&](Best e) { add(!(e.x < least), e); }); };  // (none are -infinity)
     first_n<kJoinThreads>(lds, a.n, count, collect, element, [&](int rank, Best e) { finish_top(a, row, p, rank, e); });
 }
 
-// Elements of a slice: 512 threads with 32 each where the rows' slices fill the
-// GPU, else 256 with 8.
+// Elements of a slice: 256 threads with 16 each where the rows' slices fill the
+// GPU, else 8 each.
 constexpr int kLongThreads = 256, kLongEach = 16, kLong = kLongThreads * kLongEach, kShort = 256 * 8;
 int slice_of(int M, int V)
 {
