@@ -328,10 +328,14 @@ constexpr int most_col_tiles(int D, bool codes = false)
 {
     return codes ? (D <= 96 ? 4 : D == 128 ? 3 : 2) : D == 64 || D == 128 ? 6 : D == 96 ? 4 : 3;
 }
-// Waves of a SIMD over codes: what the accumulators and a tile's codes leave room for.
+// Waves of a SIMD over codes, which are workgroups on a CU: the most for which the accumulators
+// and a tile's codes fit the registers. 32 sequences of 8000 tokens, 8 heads, 4 bits, against
+// one less: heads of 64 with 3 column tiles 91 us (102), of 96 with 2 81 (91), of 128 with 1 74 (79), 2
+// 97 (107), 3 131 (172), of 192 with 2 157 (201); 8 bits, 128 with 1 107 (110), 4 heads of 256
+// with 1 109 (129). A fourth for heads of 64 gains nothing (8 bits 81 us, with three 77).
 constexpr int codes_waves_per_simd(int bits, int D, int NT)
 {
-    return D == 64    ? (NT <= 2 ? 4 : NT == 3 && bits == 4 ? 3 : 2)
+    return D == 64    ? (NT <= 2 || (NT == 3 && bits == 4) ? 3 : 2)
            : D == 96  ? (NT == 1 || (NT == 2 && bits == 4) ? 3 : NT == 4 && bits == 8 ? 1 : 2)
            : D == 128 ? (NT == 1 || (NT == 2 && bits == 4) ? 3 : 2)
            : D == 192 ? (NT == 1 && bits == 4 ? 3 : 2)
