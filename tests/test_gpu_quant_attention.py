@@ -126,6 +126,34 @@ def test_infinities_in_fully_visible_tiles():
     assert (out[..., 64:] == float("inf")).all()
 
 
+@pytest.mark.parametrize("bits,D,G,page", [(8, 192, 64, 16), (4, 192, 32, 7), (8, 256, 128, 5), (4, 256, 64, 32), (8, 256, 32, 48),
+                                           (4, 96, 32, 16)])
+def test_infinities_in_any_group_of_wide_heads(bits, D, G, page):
+    """One group of one token each, in every part of the head: infinity there, and
+    everywhere else what it was."""
+    p = Problem([400], [2], 1, 3, D, page, F16, bits, G, seed=D + bits, q_scale=1.0)
+    clean, lse0 = p.check()
+    # (the places that hold no token stand for NaN)
+    largest = np.nan_to_num(np.abs(_quant.numbers(p.caches[2], p.caches[3], bits, G))).max()
+    assert largest < 10
+    for group in range(D // G):
+        for token in (0, 77 + 37 * group):
+            at = (int(p.table[0, token // page]), 0, token % page, group)
+            before = int(p.caches[3][at])
+            p.caches[3][at] = 0x7C00 << 16 | 0x3800
+            out, lse = p.run()
+            p.caches[3][at] = before
+            rest = torch.ones(D, dtype=torch.bool)
+            rest[group * G:(group + 1) * G] = False
+            # The token's finite groups are added apart from its tile: at most 400 terms of up to
+            # max |v| times a weight, the weights adding up to 1, in another order, 2^-24 of that
+            # an addition on either side, then one step of fp16 where that crosses a rounding.
+            away = (out[..., rest].double() - clean[..., rest].double()).abs()
+            steps = clean[..., rest].double().abs() * 2.0 ** -10 + 2.0 ** -24
+            assert torch.equal(lse, lse0) and (away <= 2 * 400 * 2.0 ** -24 * largest + steps).all(), (group, token)
+            assert (out[..., ~rest] == float("inf")).all(), (group, token)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_lowest_and_large_scores(dtype):
     """Scores of hundreds: the running maximum moves far, weights underflow."""
