@@ -143,13 +143,17 @@ __device__ __forceinline__ void store_codes(const RopeArgs &a, float4_t y0, floa
     if (!in_head || !kept)
         return;
     const Levels g = levels_of(lo, hi, levels);
-    // v_rcp_f32 is good to 2^-23: a code's place is off by at most 2^-14 of a step.
-    const float b = (float)g.bias, inv = g.scale > (_Float16)0 ? __builtin_amdgcn_rcpf((float)g.scale) : 0.f;
+    // A value's place between the levels in 64 bits, where it is off by less than 2^-40 of a
+    // step (y - b is exact where it is small): in fp32, at place 255, it is 2^-15, and twice as
+    // many values land on the other side of a middle. It lies in 0 .. levels; the sum with
+    // 1.5 * 2^52 rounds it.
+    const double inv = g.scale > (_Float16)0 ? 1.0 / (double)(float)g.scale : 0.0, b = (double)(float)g.bias;
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float y = j < 4 ? y0[j % 4] : y1[j % 4];
-        c[j] = odd ? 0u : (uint32_t)__builtin_amdgcn_fmed3f(rintf((y - b) * inv), 0.f, (float)levels);
+        const double place = __builtin_fma((double)y - b, inv, 0x1.8p52);
+        c[j] = odd ? 0u : (uint32_t)__builtin_bit_cast(uint64_t, place);
     }
     uint32_t *to = static_cast<uint32_t *>(is_v ? a.v_cache : a.k_cache) + row * (a.D * a.bits / 32);
     if (a.bits == 8) {
@@ -205,8 +209,14 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
         const float4_t f = *reinterpret_cast<const float4_t *>(a.inv_freq + 4 * u);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const double t = pos * (double)f[j];
-            sincospif(2.0f * (float)(t - rint(t)), &sine[j], &cosine[j]);
+            const double t = pos * (double)f[j], turn = t - rint(t);
+            sincospif(2.0f * (float)turn, &sine[j], &cosine[j]);
+            if constexpr (QUANT) {  // what the rounding left out, to first order: it moves values over the borders between codes
+                const float rest = (float)((turn - (double)(float)turn) * 6.28318530717958647693);
+                const float s = sine[j], c = cosine[j];
+                sine[j] = __builtin_fmaf(c, rest, s);
+                cosine[j] = __builtin_fmaf(-s, rest, c);
+            }
         }
     }
     // Where this row's key and value go; -1: nowhere.
@@ -228,7 +238,12 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             ss += x0[j] * x0[j] + x1[j] * x1[j];
-        const float r = rsqrtf(head_sum<L>(ss) * (1.0f / (float)a.D) + a.eps);
+        const float mean = head_sum<L>(ss) * (1.0f / (float)a.D) + a.eps;
+        float r = rsqrtf(mean);
+        if constexpr (QUANT) {  // one step of Newton's
+            const double r0 = r;
+            r = (float)(r0 * __builtin_fma(-0.5 * (double)mean * r0, r0, 1.5));
+        }
         float4_t y0 = x0, y1 = x1;
         if (in_head) {
             if (!is_v) {
